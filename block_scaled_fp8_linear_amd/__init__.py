@@ -10,11 +10,14 @@ Entry points mirror ``include/bsf8.h``:
 * ``validate(...)``                     header-only geometry check, returns a status name
 * ``BlockFP8Weight(members, ...)``      handle over borrowed device tensors
 * ``quant_act(x)``                      per-token 1x128 E4M3 quantization -> (xq, xs)
+* ``quant_norm(x, weight, ...)``        residual add, norms and gate between two blocks -> codes, scales, stream
+* ``expert_plan(ids, n_experts)``       router choices -> row ranges of the experts, gather rows, slots
 * ``linear_w8a16(w, x)``                F32-activation arm
 * ``linear_w8a8(w, xq, xs)``            FP8 x FP8 arm with F32 epilogue
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -50,6 +53,20 @@ class MemberDesc(ctypes.Structure):
 
 class Decl(ctypes.Structure):
     _fields_ = [("quant_method_fp8", ctypes.c_int32), ("block_n", ctypes.c_int32), ("block_k", ctypes.c_int32)]
+
+
+_i32, _i64, _f64, _ptr = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_void_p
+
+
+class NormArgs(ctypes.Structure):
+    """bsf8_norm_args."""
+    _fields_ = [("M", _i64), ("K", _i64), ("kind", _i32), ("eps", _f64), ("residual_scale", _f64), ("x", _ptr),
+                ("x_dtype", _i32), ("ldx", _i64), ("x_rows", _i64), ("slots", _ptr), ("probs", _ptr), ("top", _i32),
+                ("post_weight", _ptr), ("post_bias", _ptr), ("post_dtype", _i32), ("gate", _ptr),
+                ("gate_dtype", _i32), ("ldg", _i64), ("residual", _ptr), ("ldr", _i64), ("h", _ptr), ("ldh", _i64),
+                ("h_dtype", _i32), ("weight", _ptr), ("bias", _ptr), ("weight_dtype", _i32), ("n", _ptr),
+                ("n_dtype", _i32), ("ldn", _i64), ("xq", _ptr), ("ldq", _i64), ("xs", _ptr), ("xs_sm", _i64),
+                ("xs_sk", _i64)]
 
 
 class Unit(ctypes.Structure):
@@ -102,6 +119,10 @@ EXPORTS = [
                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_glu_act", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    ("bsf8_quant_norm", ctypes.c_int, [ctypes.POINTER(NormArgs), ctypes.c_void_p]),
+    ("bsf8_expert_plan", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
+                                        ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
     ("bsf8_upcast", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_dense_workspace_size", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(ctypes.c_size_t)]),
@@ -417,6 +438,144 @@ def glu_act(y, out=None):
     return out
 
 
+def _on_current(device):
+    """The library launches on the current device: make ``device`` that for the call, where it is another."""
+    torch = _torch()
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _rows_of(name, t, shape, dtypes):
+    """``t`` is a matrix of ``shape`` with unit column stride and rows that do not overlap, of one of ``dtypes``."""
+    if tuple(t.shape) != shape or t.dtype not in dtypes or (shape[1] > 1 and t.stride(1) != 1) \
+            or (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise ValueError(f"{name} must be {list(shape)} with unit column stride, of one of {dtypes}")
+    return max(t.stride(0), shape[1])
+
+
+def _vector_of(name, t, n, dtypes):
+    if tuple(t.shape) != (n,) or t.dtype not in dtypes or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor of one of {dtypes}")
+    return t.data_ptr()
+
+
+NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def quant_norm(x, weight, *, bias=None, kind="rms", eps=1e-6, residual=None, residual_scale=1.0, gate=None,
+               post_weight=None, post_bias=None, slots=None, probs=None, quantize=True, xq=None, xs=None, h=None,
+               out_dtype=None, out=None):
+    """The step between two blocks of a residual stream, in one pass:
+
+        o = x, or sum_j probs[:, j] x[slots[:, j]]         h = residual_scale * residual + gate * post_norm(o)
+        n = norm(h) * weight + bias                        (xq, xs) = quant_act(n)
+
+    x: the block's output [M, K] (float32 or bfloat16), or with ``slots`` (int32 [M, top]) and ``probs``
+    (float32 [M, top]) the rows of an expert product.  ``kind``: "rms" or "layer", of both norms; the one after
+    the block runs when ``post_weight`` is given.  ``gate``: [K] or [M, K].  ``residual`` and ``h`` have one type
+    (x's when there is no residual); ``h`` may be ``residual`` itself.  Returns (xq, xs, h, n): codes and scales
+    as quant_act gives them (None with ``quantize=False``), the stream h (None when there is neither ``residual``
+    nor ``h``), and n when ``out`` or ``out_dtype`` asks for it, else None."""
+    torch = _torch()
+    f32, bf16 = torch.float32, torch.bfloat16
+    real = (f32, bf16)
+    _on_device(None, x=x)
+    dev = x.device
+    _on_device(dev, weight=weight, bias=bias, residual=residual, gate=gate, post_weight=post_weight,
+               post_bias=post_bias, slots=slots, probs=probs, xq=xq, xs=xs, h=h, out=out)
+    if kind not in NORM_KINDS:
+        raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}")
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    rows, K = x.shape
+    M, top = rows, 0
+    if (slots is None) != (probs is None):
+        raise ValueError("slots and probs: both or neither")
+    if slots is not None:
+        if slots.dim() != 2 or slots.dtype != torch.int32 or not slots.is_contiguous() or probs.shape != slots.shape \
+                or probs.dtype != f32 or not probs.is_contiguous():
+            raise ValueError("slots must be int32 and probs float32, both contiguous [M, top]")
+        M, top = slots.shape
+        if top < 1:
+            raise ValueError("slots and probs need at least one column")
+    if not (quantize or out is not None or out_dtype is not None):
+        raise ValueError("nothing to write: quantize, out_dtype or out")
+    if not quantize and (xq is not None or xs is not None):
+        raise ValueError("xq and xs are written only with quantize=True")
+    a = NormArgs(M, K, NORM_KINDS[kind], eps, residual_scale)
+    a.x, a.x_dtype, a.ldx, a.x_rows = x.data_ptr(), _dt_of(x), _rows_of("x", x, (rows, K), real), rows
+    if top:
+        a.slots, a.probs, a.top = slots.data_ptr(), probs.data_ptr(), top
+    a.weight, a.weight_dtype = _vector_of("weight", weight, K, real), _dt_of(weight)
+    if bias is not None:
+        a.bias = _vector_of("bias", bias, K, (weight.dtype,))
+    if post_weight is not None:
+        a.post_weight, a.post_dtype = _vector_of("post_weight", post_weight, K, real), _dt_of(post_weight)
+    if post_bias is not None:
+        if post_weight is None:
+            raise ValueError("post_bias without post_weight")
+        a.post_bias = _vector_of("post_bias", post_bias, K, (post_weight.dtype,))
+    if gate is not None:
+        if gate.dim() == 1:
+            a.gate = _vector_of("gate", gate, K, real)
+        else:
+            a.gate, a.ldg = gate.data_ptr(), _rows_of("gate", gate, (M, K), real)
+        a.gate_dtype = _dt_of(gate)
+    stream_dtype = residual.dtype if residual is not None else h.dtype if h is not None else x.dtype
+    if residual is not None:
+        a.residual, a.ldr = residual.data_ptr(), _rows_of("residual", residual, (M, K), real)
+        if h is None:
+            h = torch.empty((M, K), dtype=stream_dtype, device=dev)
+    if h is not None:
+        a.h, a.ldh = h.data_ptr(), _rows_of("h", h, (M, K), (stream_dtype,) if residual is not None else real)
+    a.h_dtype = DT_BF16 if stream_dtype == bf16 else DT_F32
+    if out is None and out_dtype is not None:
+        out = torch.empty((M, K), dtype=out_dtype, device=dev)
+    if out is not None:
+        a.n, a.n_dtype = out.data_ptr(), _dt_of(out)
+        a.ldn = _rows_of("out", out, (M, K), real if out_dtype is None else (out_dtype,))
+    if quantize:
+        Kb = -(-K // BLOCK)
+        if xq is None:
+            xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+        if xs is None:
+            xs = scales_kmajor(M, Kb, dev)
+        if tuple(xs.shape) != (M, Kb) or xs.dtype != f32:
+            raise ValueError(f"xs must be float32 [M, Kb] = [{M}, {Kb}]")
+        a.xq, a.ldq = xq.data_ptr(), _rows_of("xq", xq, (M, K), (torch.uint8, torch.float8_e4m3fn))
+        a.xs, a.xs_sm, a.xs_sk = xs.data_ptr(), xs.stride(0), xs.stride(1)
+    with _on_current(dev):
+        _check(lib().bsf8_quant_norm(ctypes.byref(a), _stream_ptr(dev)), "quant_norm")
+    return xq, xs, h, out
+
+
+def expert_plan(ids, n_experts: int, offsets=None, rows=None, slots=None):
+    """The router's choices ids [M, top] (int32 or int64, contiguous) -> (offsets int32 [n_experts + 1],
+    rows int32 [M * top], slots int32 [M, top]): expert e has rows offsets[e] .. offsets[e+1] - 1, row r is token
+    rows[r], choice (m, j) is row slots[m, j].  A number outside [0, n_experts) has no row and slot -1; entries of
+    rows from offsets[n_experts] on keep what they hold."""
+    torch = _torch()
+    _on_device(None, ids=ids)
+    dev = ids.device
+    _on_device(dev, offsets=offsets, rows=rows, slots=slots)
+    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 or int64 [M, top] tensor")
+    M, top = ids.shape
+    for name, t, shape in (("offsets", offsets, (n_experts + 1,)), ("rows", rows, (M * top,)),
+                           ("slots", slots, (M, top))):
+        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
+    if offsets is None:
+        offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=dev)
+    if rows is None:
+        rows = torch.empty(M * top, dtype=torch.int32, device=dev)
+    if slots is None:
+        slots = torch.empty((M, top), dtype=torch.int32, device=dev)
+    with _on_current(dev):
+        _check(lib().bsf8_expert_plan(ids.data_ptr(), ids.element_size(), M, top, n_experts, offsets.data_ptr(),
+                                      rows.data_ptr(), slots.data_ptr(), _stream_ptr(dev)), "expert_plan")
+    return offsets, rows, slots
+
+
 def linear_w8a16(w: BlockFP8Weight, x, out_dtype=None, out=None, workspace=None):
     """F32-activation arm: y [M, N] = x . dequant(W)^T (float32 output unless out_dtype says bfloat16)."""
     torch = _torch()
@@ -543,7 +702,7 @@ def linear_dense(wd, x, out_dtype=None, out=None, workspace=None):
     return y
 
 
-__all__ = ["BSF8Error", "BlockFP8Weight", "validate", "quant_act", "quant_glu", "glu_act", "linear_w8a16", "linear_w8a8",
+__all__ = ["BSF8Error", "BlockFP8Weight", "validate", "quant_act", "quant_glu", "glu_act", "quant_norm", "expert_plan", "linear_w8a16", "linear_w8a8",
            "linear_w8a8_dynamic", "linear_w8a8_noalloc", "NOALLOC_SCRATCH_BYTES", "upcast",
            "linear_dense", "dense_workspace_size", "lib", "status_name", "ARM_W8A16", "ARM_W8A8", "ARM_DENSE",
            "ARM_W8A8_DYNAMIC",

@@ -24,6 +24,9 @@ LIB = os.path.join(PKG, "libbsf8.so")
 
 SOURCES = ["bsf8_host.cpp", "bsf8_inspect.cpp", "bsf8_quant.hip", "bsf8_w8a16.hip", "bsf8_w8a8.hip", "bsf8_dense.hip",
            "bsf8_stream.hip"]
+# Sources compiled apart (in parallel) and joined into the object of the source
+# they belong to, so that one object holds each kind of kernel.
+JOINED = {"bsf8_quant.hip": ["bsf8_norm.hip", "bsf8_route.hip"]}
 ARCH = "gfx950"
 
 
@@ -57,9 +60,23 @@ def compile_one(src: str, asm: bool) -> str:
     return obj
 
 
+def join(obj: str, parts) -> None:
+    """Add the objects ``parts`` to ``obj`` (a relocatable link)."""
+    tmp = obj + ".tmp"
+    ld = shutil.which("ld") or os.path.join(os.path.dirname(hipcc()), "..", "llvm", "bin", "ld.lld")
+    r = subprocess.run([ld, "-r", "-o", tmp, obj] + list(parts), capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"join failed: {obj}\n{r.stderr}")
+    os.replace(tmp, obj)
+
+
 def build(jobs: int = 4, asm: bool = False) -> str:
+    sources = SOURCES + [s for parts in JOINED.values() for s in parts]
     with cf.ThreadPoolExecutor(max_workers=max(1, jobs)) as ex:
-        objs = list(ex.map(lambda s: compile_one(s, asm), SOURCES))
+        made = dict(zip(sources, ex.map(lambda s: compile_one(s, asm), sources)))
+    for src, parts in JOINED.items():
+        join(made[src], [made[s] for s in parts])
+    objs = [made[s] for s in SOURCES]
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

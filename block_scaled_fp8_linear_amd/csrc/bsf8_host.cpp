@@ -1,6 +1,7 @@
 // Host side of libbsf8: status names, the header-only validator, weight handles,
 // argument checks and dispatch to the kernel launchers.  No device memory is
 // touched here except through the launchers.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -279,6 +280,107 @@ bsf8_status bsf8_glu_act(const void* y, int32_t y_dtype, int64_t M, int64_t F, i
   if (reinterpret_cast<uintptr_t>(y) % esz || reinterpret_cast<uintptr_t>(h) % 4)
     return fail(BSF8_E_ALIGNMENT, "y or h not element aligned");
   return launch_glu_act(y, y_dtype == BSF8_DT_BF16, M, F, ldy, h, ldh, static_cast<hipStream_t>(stream));
+}
+
+bsf8_status bsf8_quant_norm(const bsf8_norm_args* p, void* stream) {
+  if (p == nullptr) return fail(BSF8_E_INVALID_ARG, "null arguments");
+  const bsf8_norm_args& q = *p;
+  if (q.M < 0 || q.K < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (q.kind != BSF8_NORM_RMS && q.kind != BSF8_NORM_LAYER) return fail(BSF8_E_INVALID_ARG, "norm kind %d", q.kind);
+  if (!(q.eps > 0.0) || !std::isfinite(q.eps) || !std::isfinite(q.residual_scale))
+    return fail(BSF8_E_INVALID_ARG, "eps %g (positive) or residual_scale %g", q.eps, q.residual_scale);
+  if (!dtype_ok(q.x_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "x dtype %d (F32 or BF16)", q.x_dtype);
+  if (!dtype_ok(q.h_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "h dtype %d (F32 or BF16)", q.h_dtype);
+  if (!dtype_ok(q.weight_dtype, true, true) || (q.post_weight && !dtype_ok(q.post_dtype, true, true)) ||
+      (q.gate && !dtype_ok(q.gate_dtype, true, true)) || (q.n && !dtype_ok(q.n_dtype, true, true)))
+    return fail(BSF8_E_INVALID_ARG, "weight, post, gate or n dtype (F32 or BF16)");
+  if ((q.slots == nullptr) != (q.probs == nullptr)) return fail(BSF8_E_INVALID_ARG, "slots and probs: both or neither");
+  if (q.slots && (q.top < 1 || q.x_rows < 0)) return fail(BSF8_E_INVALID_ARG, "top %d or x_rows %lld", q.top, (long long)q.x_rows);
+  if ((q.xq == nullptr) != (q.xs == nullptr)) return fail(BSF8_E_INVALID_ARG, "xq and xs: both or neither");
+  if (q.M == 0 || q.K == 0) return BSF8_OK;
+  // an experts' output without a row may have no address
+  if ((q.x == nullptr && !(q.slots && q.x_rows == 0)) || q.weight == nullptr) return fail(BSF8_E_INVALID_ARG, "null pointer");
+  if (q.n == nullptr && q.xq == nullptr) return fail(BSF8_E_INVALID_ARG, "neither n nor xq is given");
+  if (q.residual && !q.h) return fail(BSF8_E_INVALID_ARG, "a residual without h");
+  if (q.post_bias && !q.post_weight) return fail(BSF8_E_INVALID_ARG, "post_bias without post_weight");
+  if (q.ldx < q.K || (q.residual && q.ldr < q.K) || (q.h && q.ldh < q.K) || (q.n && q.ldn < q.K) ||
+      (q.xq && q.ldq < q.K) || (q.gate && q.ldg != 0 && q.ldg < q.K))
+    return fail(BSF8_E_INVALID_ARG, "leading dimension too small");
+  if (q.xq && !scale_layout_ok(q.M, ceil_div(q.K, kBlock), q.xs_sm, q.xs_sk))
+    return fail(BSF8_E_INVALID_ARG, "xs strides (%lld, %lld): neither token-major nor K-major", (long long)q.xs_sm,
+                (long long)q.xs_sk);
+  if (q.K > BSF8_NORM_MAX_K || q.M > INT32_MAX || (q.slots && q.x_rows > INT32_MAX))
+    return fail(BSF8_E_UNSUPPORTED, "K beyond %d, or M or x_rows too large", BSF8_NORM_MAX_K);
+  NormDev a{};
+  bool misaligned = false;
+  // element alignment is required; 16-byte rows are taken where they are there
+  const auto vec = [&](const void* ptr, bool bf16, int64_t ld) -> int32_t {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(ptr);
+    const int64_t esz = bf16 ? 2 : 4;
+    misaligned = misaligned || at % uintptr_t(esz) != 0;
+    return at % 16 == 0 && (ld * esz) % 16 == 0 ? 1 : 0;
+  };
+  const bool x_bf16 = q.x_dtype == BSF8_DT_BF16, h_bf16 = q.h_dtype == BSF8_DT_BF16;
+  a.M = int32_t(q.M);
+  a.K = int32_t(q.K);
+  a.layer = q.kind == BSF8_NORM_LAYER ? 1 : 0;
+  a.top = q.top;
+  a.R = q.slots ? int32_t(q.x_rows) : 0;
+  a.post_bf16 = q.post_dtype == BSF8_DT_BF16;
+  a.gate_bf16 = q.gate_dtype == BSF8_DT_BF16;
+  a.w_bf16 = q.weight_dtype == BSF8_DT_BF16;
+  a.n_bf16 = q.n_dtype == BSF8_DT_BF16;
+  a.x_vec = vec(q.x, x_bf16, q.ldx);
+  a.res_vec = vec(q.residual, h_bf16, q.ldr);
+  a.h_vec = vec(q.h, h_bf16, q.ldh);
+  a.n_vec = vec(q.n, a.n_bf16 != 0, q.ldn);
+  a.post_vec = vec(q.post_weight, a.post_bf16 != 0, 0) & vec(q.post_bias, a.post_bf16 != 0, 0);
+  a.gate_vec = vec(q.gate, a.gate_bf16 != 0, q.ldg);
+  a.w_vec = vec(q.weight, a.w_bf16 != 0, 0) & vec(q.bias, a.w_bf16 != 0, 0);
+  a.q_vec = reinterpret_cast<uintptr_t>(q.xq) % 8 == 0 && q.ldq % 8 == 0 ? 1 : 0;
+  misaligned = misaligned || reinterpret_cast<uintptr_t>(q.xs) % 4 || reinterpret_cast<uintptr_t>(q.slots) % 4 ||
+               reinterpret_cast<uintptr_t>(q.probs) % 4;
+  if (misaligned) return fail(BSF8_E_ALIGNMENT, "an address is not element aligned");
+  a.eps = q.eps;
+  a.alpha = q.residual_scale;
+  a.x = q.x;
+  a.slots = q.slots;
+  a.probs = q.probs;
+  a.post_w = q.post_weight;
+  a.post_b = q.post_bias;
+  a.gate = q.gate;
+  a.res = q.residual;
+  a.w = q.weight;
+  a.b = q.bias;
+  a.h = q.h;
+  a.n = q.n;
+  a.xq = q.xq;
+  a.xs = q.xs;
+  a.ldx = q.ldx;
+  a.ldg = q.ldg;
+  a.ldr = q.ldr;
+  a.ldh = q.ldh;
+  a.ldn = q.ldn;
+  a.ldq = q.ldq;
+  a.xs_sm = q.xs_sm;
+  a.xs_sk = q.xs_sk;
+  return launch_quant_norm(a, x_bf16, h_bf16, static_cast<hipStream_t>(stream));
+}
+
+bsf8_status bsf8_expert_plan(const void* ids, int32_t ids_bytes, int64_t M, int64_t top, int64_t n_experts,
+                             int32_t* offsets, int32_t* rows, int32_t* slots, void* stream) {
+  if (M < 0 || top < 1 || n_experts < 1) return fail(BSF8_E_INVALID_ARG, "M %lld, top %lld or n_experts %lld",
+                                                     (long long)M, (long long)top, (long long)n_experts);
+  if (ids_bytes != 4 && ids_bytes != 8) return fail(BSF8_E_INVALID_ARG, "ids of %d bytes (4 or 8)", ids_bytes);
+  if (offsets == nullptr || (M > 0 && (ids == nullptr || rows == nullptr || slots == nullptr)))
+    return fail(BSF8_E_INVALID_ARG, "null pointer");
+  if (top > INT32_MAX || M > INT32_MAX / top || n_experts > 65535)
+    return fail(BSF8_E_UNSUPPORTED, "M * top beyond 2^31 - 1, or n_experts beyond 65535");
+  if (reinterpret_cast<uintptr_t>(ids) % uintptr_t(ids_bytes) || reinterpret_cast<uintptr_t>(offsets) % 4 ||
+      reinterpret_cast<uintptr_t>(rows) % 4 || reinterpret_cast<uintptr_t>(slots) % 4)
+    return fail(BSF8_E_ALIGNMENT, "ids or an output not element aligned");
+  return launch_expert_plan(ids, ids_bytes == 8, M, top, n_experts, offsets, rows, slots,
+                            static_cast<hipStream_t>(stream));
 }
 
 // Workspace of the two-step form of bsf8_linear_w8a8_dynamic: the codes (row

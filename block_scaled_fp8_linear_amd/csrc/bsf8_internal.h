@@ -56,6 +56,26 @@ bsf8_status launch_quant_glu(const void* y, bool y_bf16, int64_t M, int64_t F, i
 bsf8_status launch_glu_act(const void* y, bool y_bf16, int64_t M, int64_t F, int64_t ldy, float* h, int64_t ldh,
                            hipStream_t stream);
 
+// bsf8_quant_norm's arguments as its kernel takes them (null pointers: absent terms).
+struct NormDev {
+  int32_t M, K, layer, top, R;
+  int32_t post_bf16, gate_bf16, w_bf16, n_bf16;
+  int32_t x_vec, res_vec, h_vec, n_vec, q_vec, post_vec, gate_vec, w_vec;   // wide accesses allowed
+  double eps, alpha;
+  const void* x;
+  const int32_t* slots;
+  const float* probs;
+  const void *post_w, *post_b, *gate, *res, *w, *b;
+  void *h, *n;
+  uint8_t* xq;
+  float* xs;
+  int64_t ldx, ldg, ldr, ldh, ldn, ldq, xs_sm, xs_sk;
+};
+bsf8_status launch_quant_norm(const NormDev& a, bool x_bf16, bool h_bf16, hipStream_t stream);
+
+bsf8_status launch_expert_plan(const void* ids, bool ids64, int64_t M, int64_t top, int64_t E, int32_t* offsets,
+                               int32_t* rows, int32_t* slots, hipStream_t stream);
+
 size_t w8a16_workspace_bytes(const WeightDev& w, int64_t M);
 bsf8_status launch_w8a16(const WeightDev& w, bool aligned, const void* x, bool x_bf16, int64_t M,
                          int64_t ldx, void* y, bool y_bf16, int64_t ldy, void* ws, size_t ws_bytes,

@@ -267,6 +267,98 @@ bsf8_status bsf8_glu_act(const void* y, int32_t y_dtype, int64_t M, int64_t F, i
                          void* stream);
 
 /*
+ * bsf8_quant_norm -- the step between two blocks of a residual stream: the
+ * output of the block before, an optional norm of it, a gate, the scaled
+ * residual add, the norm before the next block, and the codes its W8A8
+ * projection reads, in one pass over the row.
+ * ("Qwen checkpoints with block FP8 weights", operator paragraph: attention,
+ *  GDN and FFN projections share the operator; the norms and the residual
+ *  stream stand between them and keep their own representation.)  For token m:
+ *   o  = x[m]                                      (slots NULL)
+ *      = sum_j probs[m, j] * x[slots[m, j]]        (slots given; j ascending)
+ *   o' = o, or norm(o) * post_weight + post_bias when post_weight is given
+ *   h  = residual_scale * residual[m] + gate * o'  (terms that are NULL drop out)
+ *   n  = norm(h) * weight + bias
+ * with norm(v) = v / sqrt(mean(v^2) + eps) (BSF8_NORM_RMS) or
+ * (v - mean(v)) / sqrt(mean((v - mean(v))^2) + eps) (BSF8_NORM_LAYER).
+ * All of it is F64 but for two roundings: h is rounded to F32 and, for a BF16
+ * stream, then to BF16, and the second norm reads that stored value; n is
+ * rounded to F32.  xq and xs are what bsf8_quant_act writes for n; the output
+ * n is its F32 value, or that rounded to BF16.  Non-finite inputs are outside
+ * the defined domain, as they are for the quantizer.
+ *
+ * x        : [M, K], or [x_rows, K] with slots (an expert product's output);
+ *            F32 or BF16.  A slot outside [0, x_rows) adds nothing, so a token
+ *            with no slot has o = 0.
+ * slots, probs : [M, top], both or neither (bsf8_expert_plan's slots and the
+ *            router's F32 weights).
+ * gate     : F32 or BF16, one row for every token (ldg == 0) or [M, K].
+ * residual, h : [M, K] of h_dtype.  h may be NULL only when residual is.  h may
+ *            be residual itself, or x without slots (same address, pitch and
+ *            type); no other overlap of an output with an input.
+ * weight, bias : [K], F32 or BF16; bias and post_bias may be NULL.
+ * n        : [M, K] F32 or BF16, or NULL.   xq, xs : both or neither (NULL);
+ *            at least one of n and xq is needed.
+ * Errors: INVALID_ARG, ALIGNMENT (an address not element aligned), UNSUPPORTED
+ * (K > BSF8_NORM_MAX_K), DEVICE.
+ */
+#define BSF8_NORM_MAX_K 32768
+typedef enum bsf8_norm_kind { BSF8_NORM_RMS = 0, BSF8_NORM_LAYER = 1 } bsf8_norm_kind;
+typedef struct bsf8_norm_args {
+  int64_t M, K;
+  int32_t kind;          /* bsf8_norm_kind, of both norms */
+  double eps;            /* positive */
+  double residual_scale;
+  const void* x;
+  int32_t x_dtype;
+  int64_t ldx;
+  int64_t x_rows;        /* rows of x when slots is given */
+  const int32_t* slots;
+  const float* probs;
+  int32_t top;
+  const void* post_weight;
+  const void* post_bias;
+  int32_t post_dtype;    /* of post_weight and post_bias */
+  const void* gate;
+  int32_t gate_dtype;
+  int64_t ldg;
+  const void* residual;
+  int64_t ldr;
+  void* h;
+  int64_t ldh;
+  int32_t h_dtype;       /* of residual and h; what h is rounded to where neither is given */
+  const void* weight;
+  const void* bias;
+  int32_t weight_dtype;  /* of weight and bias */
+  void* n;
+  int32_t n_dtype;
+  int64_t ldn;
+  uint8_t* xq;
+  int64_t ldq;
+  float* xs;
+  int64_t xs_sm, xs_sk;
+} bsf8_norm_args;
+bsf8_status bsf8_quant_norm(const bsf8_norm_args* args, void* stream);
+
+/*
+ * bsf8_expert_plan -- the router's choices as the expert product reads them: a
+ * stable counting sort of M * top expert numbers.
+ * ids : [M, top] contiguous, int32 (ids_bytes 4) or int64 (8).  A number outside
+ *       [0, n_experts) is a choice without an expert (dropped by a capacity
+ *       rule, a padded token).
+ * offsets [n_experts + 1] : expert e has rows offsets[e] .. offsets[e + 1] - 1.
+ * rows    [M * top] : the token of each row, by expert and within an expert in
+ *       the order of ids; entries from offsets[n_experts] on keep what they hold.
+ * slots   [M, top] : the row of each choice, -1 for one without an expert.
+ * One launch, no workspace; the result does not depend on timing.  M == 0
+ * writes the offsets, all zero.
+ * Errors: INVALID_ARG, ALIGNMENT (ids not element aligned, an output not 4-byte
+ * aligned), UNSUPPORTED (M * top > 2^31 - 1, n_experts > 65535), DEVICE.
+ */
+bsf8_status bsf8_expert_plan(const void* ids, int32_t ids_bytes, int64_t M, int64_t top, int64_t n_experts,
+                             int32_t* offsets, int32_t* rows, int32_t* slots, void* stream);
+
+/*
  * bsf8_workspace_size -- device workspace bytes a compute call of this handle
  * needs for M tokens on the given arm (0 when none).  The W8A8 arm uses one
  * when its tile grid is too small to occupy the device (few tokens against few
