@@ -124,6 +124,17 @@ __device__ __forceinline__ void store_row(void* p, bool bf16, int64_t off, int v
   }
 }
 
+// The rounding to F32.  The compiler must not see past it: it would merge it
+// with a rounding to BF16 that follows into one from F64, which lands on the
+// other side where the F32 value is a BF16 midpoint, so the stored BF16 would
+// not be the rounding of the F32 value that the codes are made of (and the
+// merged form takes nine instructions more).
+__device__ __forceinline__ float to_f32(double v) {
+  float f = static_cast<float>(v);
+  asm("" : "+v"(f));
+  return f;
+}
+
 // Sum over the threads of a row, the same value in each: a butterfly within the
 // wave, then the waves' sums in wave order.
 template <int T>
@@ -245,7 +256,7 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
     float h[EPL];
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      h[e] = float(v[i][e]);
+      h[e] = to_f32(v[i][e]);
       if (HBF16) h[e] = float(static_cast<__bf16>(h[e]));
       v[i][e] = e < valid[i] ? double(h[e]) : 0.0;
     }
@@ -263,7 +274,7 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
     float amax = 0.0f;
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
-      n[e] = float(fma((v[i][e] - mean) * rstd, double(w[e]), double(b[e])));
+      n[e] = to_f32(fma((v[i][e] - mean) * rstd, double(w[e]), double(b[e])));
       if (e < valid[i]) amax = fmaxf(amax, fabsf(n[e]));
     }
     if (a.n != nullptr) store_row(a.n, a.n_bf16, m * a.ldn + k[i], valid[i], a.n_vec, n);

@@ -200,6 +200,26 @@ def test_zero_and_equal_rows():
     assert np.allclose(n[2:].cpu().numpy(), 3.5 / np.sqrt(3.5 ** 2 + EPS), rtol=2.0 ** -23, atol=0)
 
 
+def test_both_roundings():
+    """The stream and the norm are rounded to F32 and then to BF16: 1 + 2^-8 + 2^-40 is 1 + 2^-8 in F32, the midpoint
+    of 1 and 1 + 2^-7, and so 1 in BF16 (one rounding from F64 would give 1 + 2^-7)."""
+    t = torch()
+    banner("quant_norm roundings")
+    K = 256
+    one = t.ones((2, K), device=device())
+    w = t.ones(K, device=device())
+    x = t.zeros((2, K), device=device()).bfloat16()
+    _, _, h, n = B.quant_norm(x, w, residual=one.bfloat16(), residual_scale=1 + 2.0 ** -8 + 2.0 ** -40, eps=1e-300,
+                              out_dtype=t.bfloat16)
+    assert bool((h == 1.0).all())
+    # the rms norm of ones is 1 up to 2^-40, times the weight (1 + 2^-8), plus a bias that F32 rounds away
+    wd = t.full((K,), 1 + 2.0 ** -8, device=device())
+    for bias, want in ((2.0 ** -30, 1.0), (2.0 ** -22, 1 + 2.0 ** -7)):
+        n = B.quant_norm(one, wd, bias=t.full((K,), bias, device=device()), eps=1e-300, quantize=False,
+                         out_dtype=t.bfloat16)[3]
+        assert bool((n == want).all()), bias
+
+
 def test_fused_equals_its_parts():
     """One call gives what the same steps in separate calls give, bit for bit: the stream first, then its norm."""
     t = torch()
