@@ -17,7 +17,6 @@ Entry points mirror ``include/bsf8.h``:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from typing import Dict, List, Optional, Sequence, Tuple
@@ -238,15 +237,26 @@ def inspect_safetensors(path: str, quant_method: str = "fp8", block=(BLOCK, BLOC
 
 # ------------------------------------------------------------------ torch glue
 
+_T = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _T
+    if _T is None:
+        import torch
+        _T = torch
+    return _T
+
+
+_DT_OF: Dict[object, int] = {}
 
 
 def _dt_of(t) -> int:
-    torch = _torch()
-    return {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.uint8: DT_U8,
-            torch.float8_e4m3fn: DT_F8_E4M3, torch.float8_e5m2: DT_F8_E5M2}.get(t.dtype, DT_OTHER)
+    if not _DT_OF:
+        torch = _torch()
+        _DT_OF.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.uint8: DT_U8,
+                       torch.float8_e4m3fn: DT_F8_E4M3, torch.float8_e5m2: DT_F8_E5M2})
+    return _DT_OF.get(t.dtype, DT_OTHER)
 
 
 def _on_device(device, **tensors):
@@ -271,6 +281,9 @@ def _codes_dtype_ok(t) -> bool:
 
 def _stream_ptr(device) -> int:
     torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no Stream object: 0.1 us in place of 2
+    if raw is not None and device.index is not None:
+        return raw(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 
@@ -438,22 +451,48 @@ def glu_act(y, out=None):
     return out
 
 
-def _on_current(device):
-    """The library launches on the current device: make ``device`` that for the call, where it is another."""
+# The calls below take few microseconds on the GPU, so their checks are made of
+# few Python operations: device numbers instead of device objects, one stride
+# tuple per tensor, no checks of what is allocated here.
+
+def _same_device(idx, **tensors):
+    """_on_device against the device number ``idx``, in one comparison per tensor where all is well."""
+    for t in tensors.values():
+        if t is not None and t.get_device() != idx:
+            _on_device(_torch().device("cuda", idx), **tensors)
+
+
+def _gpu_index(name, t) -> int:
+    idx = t.get_device() if t.is_cuda else -1
+    if idx < 0:
+        _on_device(None, **{name: t})
+    return idx
+
+
+def _launch(what, idx, fn, *args):
+    """fn(*args, stream) on device ``idx``, which is made the current one for the call where it is another."""
     torch = _torch()
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    if torch.cuda.current_device() == idx:
+        st = fn(*args, _stream_ptr(torch.device("cuda", idx)))
+    else:
+        with torch.cuda.device(idx):
+            st = fn(*args, _stream_ptr(torch.device("cuda", idx)))
+    if st != 0:
+        _check(st, what)
 
 
-def _rows_of(name, t, shape, dtypes):
-    """``t`` is a matrix of ``shape`` with unit column stride and rows that do not overlap, of one of ``dtypes``."""
-    if tuple(t.shape) != shape or t.dtype not in dtypes or (shape[1] > 1 and t.stride(1) != 1) \
-            or (shape[0] > 1 and t.stride(0) < shape[1]):
-        raise ValueError(f"{name} must be {list(shape)} with unit column stride, of one of {dtypes}")
-    return max(t.stride(0), shape[1])
+def _pitch(name, t, M, K, dtypes) -> int:
+    """Row pitch of ``t``, which must be [M, K] of one of ``dtypes`` with unit column stride and rows that do not
+    overlap."""
+    if t.shape == (M, K) and t.dtype in dtypes:
+        s0, s1 = t.stride()
+        if (s1 == 1 or K <= 1) and (s0 >= K or M <= 1):
+            return s0 if s0 > K else K
+    raise ValueError(f"{name} must be [{M}, {K}] with unit column stride, of one of {dtypes}")
 
 
-def _vector_of(name, t, n, dtypes):
-    if tuple(t.shape) != (n,) or t.dtype not in dtypes or not t.is_contiguous():
+def _vector(name, t, n, dtypes) -> int:
+    if t.shape != (n,) or t.dtype not in dtypes or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor of one of {dtypes}")
     return t.data_ptr()
 
@@ -478,73 +517,80 @@ def quant_norm(x, weight, *, bias=None, kind="rms", eps=1e-6, residual=None, res
     torch = _torch()
     f32, bf16 = torch.float32, torch.bfloat16
     real = (f32, bf16)
-    _on_device(None, x=x)
-    dev = x.device
-    _on_device(dev, weight=weight, bias=bias, residual=residual, gate=gate, post_weight=post_weight,
-               post_bias=post_bias, slots=slots, probs=probs, xq=xq, xs=xs, h=h, out=out)
+    idx = _gpu_index("x", x)
+    _same_device(idx, weight=weight, bias=bias, residual=residual, gate=gate, post_weight=post_weight,
+                 post_bias=post_bias, slots=slots, probs=probs, xq=xq, xs=xs, h=h, out=out)
     if kind not in NORM_KINDS:
         raise ValueError(f"kind must be one of {sorted(NORM_KINDS)}")
     if x.dim() != 2:
         raise ValueError("x must be 2-D")
     rows, K = x.shape
-    M, top = rows, 0
-    if (slots is None) != (probs is None):
-        raise ValueError("slots and probs: both or neither")
-    if slots is not None:
+    a = NormArgs(rows, K, NORM_KINDS[kind], eps, residual_scale, x.data_ptr(), DT_BF16 if x.dtype is bf16 else DT_F32,
+                 _pitch("x", x, rows, K, real), rows)
+    M = rows
+    if slots is not None or probs is not None:
+        if slots is None or probs is None:
+            raise ValueError("slots and probs: both or neither")
         if slots.dim() != 2 or slots.dtype != torch.int32 or not slots.is_contiguous() or probs.shape != slots.shape \
                 or probs.dtype != f32 or not probs.is_contiguous():
             raise ValueError("slots must be int32 and probs float32, both contiguous [M, top]")
         M, top = slots.shape
         if top < 1:
             raise ValueError("slots and probs need at least one column")
-    if not (quantize or out is not None or out_dtype is not None):
-        raise ValueError("nothing to write: quantize, out_dtype or out")
-    if not quantize and (xq is not None or xs is not None):
-        raise ValueError("xq and xs are written only with quantize=True")
-    a = NormArgs(M, K, NORM_KINDS[kind], eps, residual_scale)
-    a.x, a.x_dtype, a.ldx, a.x_rows = x.data_ptr(), _dt_of(x), _rows_of("x", x, (rows, K), real), rows
-    if top:
-        a.slots, a.probs, a.top = slots.data_ptr(), probs.data_ptr(), top
-    a.weight, a.weight_dtype = _vector_of("weight", weight, K, real), _dt_of(weight)
+        a.M, a.slots, a.probs, a.top = M, slots.data_ptr(), probs.data_ptr(), top
+    a.weight, a.weight_dtype = _vector("weight", weight, K, real), _dt_of(weight)
     if bias is not None:
-        a.bias = _vector_of("bias", bias, K, (weight.dtype,))
+        a.bias = _vector("bias", bias, K, (weight.dtype,))
     if post_weight is not None:
-        a.post_weight, a.post_dtype = _vector_of("post_weight", post_weight, K, real), _dt_of(post_weight)
+        a.post_weight, a.post_dtype = _vector("post_weight", post_weight, K, real), _dt_of(post_weight)
     if post_bias is not None:
         if post_weight is None:
             raise ValueError("post_bias without post_weight")
-        a.post_bias = _vector_of("post_bias", post_bias, K, (post_weight.dtype,))
+        a.post_bias = _vector("post_bias", post_bias, K, (post_weight.dtype,))
     if gate is not None:
         if gate.dim() == 1:
-            a.gate = _vector_of("gate", gate, K, real)
+            a.gate = _vector("gate", gate, K, real)
         else:
-            a.gate, a.ldg = gate.data_ptr(), _rows_of("gate", gate, (M, K), real)
+            a.gate, a.ldg = gate.data_ptr(), _pitch("gate", gate, M, K, real)
         a.gate_dtype = _dt_of(gate)
-    stream_dtype = residual.dtype if residual is not None else h.dtype if h is not None else x.dtype
+    stream_dtype = x.dtype
     if residual is not None:
-        a.residual, a.ldr = residual.data_ptr(), _rows_of("residual", residual, (M, K), real)
+        stream_dtype = residual.dtype
+        a.residual, a.ldr = residual.data_ptr(), _pitch("residual", residual, M, K, real)
         if h is None:
-            h = torch.empty((M, K), dtype=stream_dtype, device=dev)
-    if h is not None:
-        a.h, a.ldh = h.data_ptr(), _rows_of("h", h, (M, K), (stream_dtype,) if residual is not None else real)
-    a.h_dtype = DT_BF16 if stream_dtype == bf16 else DT_F32
-    if out is None and out_dtype is not None:
-        out = torch.empty((M, K), dtype=out_dtype, device=dev)
+            h = torch.empty((M, K), dtype=stream_dtype, device=x.device)
+            a.h, a.ldh = h.data_ptr(), K
+        else:
+            a.h, a.ldh = h.data_ptr(), _pitch("h", h, M, K, (stream_dtype,))
+    elif h is not None:
+        stream_dtype = h.dtype
+        a.h, a.ldh = h.data_ptr(), _pitch("h", h, M, K, real)
+    a.h_dtype = DT_BF16 if stream_dtype is bf16 else DT_F32
     if out is not None:
-        a.n, a.n_dtype = out.data_ptr(), _dt_of(out)
-        a.ldn = _rows_of("out", out, (M, K), real if out_dtype is None else (out_dtype,))
+        a.n, a.ldn = out.data_ptr(), _pitch("out", out, M, K, real if out_dtype is None else (out_dtype,))
+        a.n_dtype = _dt_of(out)
+    elif out_dtype is not None:
+        if out_dtype not in real:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        out = torch.empty((M, K), dtype=out_dtype, device=x.device)
+        a.n, a.n_dtype, a.ldn = out.data_ptr(), _dt_of(out), K
     if quantize:
         Kb = -(-K // BLOCK)
         if xq is None:
-            xq = torch.empty((M, K), dtype=torch.uint8, device=dev)
+            xq = torch.empty((M, K), dtype=torch.uint8, device=x.device)
+            a.xq, a.ldq = xq.data_ptr(), K
+        else:
+            a.xq, a.ldq = xq.data_ptr(), _pitch("xq", xq, M, K, (torch.uint8, torch.float8_e4m3fn))
         if xs is None:
-            xs = scales_kmajor(M, Kb, dev)
-        if tuple(xs.shape) != (M, Kb) or xs.dtype != f32:
-            raise ValueError(f"xs must be float32 [M, Kb] = [{M}, {Kb}]")
-        a.xq, a.ldq = xq.data_ptr(), _rows_of("xq", xq, (M, K), (torch.uint8, torch.float8_e4m3fn))
-        a.xs, a.xs_sm, a.xs_sk = xs.data_ptr(), xs.stride(0), xs.stride(1)
-    with _on_current(dev):
-        _check(lib().bsf8_quant_norm(ctypes.byref(a), _stream_ptr(dev)), "quant_norm")
+            xs = torch.empty_strided((M, Kb), (1, M), dtype=f32, device=x.device)
+            a.xs, a.xs_sm, a.xs_sk = xs.data_ptr(), 1, M
+        else:
+            if xs.shape != (M, Kb) or xs.dtype != f32:
+                raise ValueError(f"xs must be float32 [M, Kb] = [{M}, {Kb}]")
+            a.xs, (a.xs_sm, a.xs_sk) = xs.data_ptr(), xs.stride()
+    elif out is None or xq is not None or xs is not None:
+        raise ValueError("without quantize, out or out_dtype is needed and xq and xs are not written")
+    _launch("quant_norm", idx, lib().bsf8_quant_norm, ctypes.byref(a))
     return xq, xs, h, out
 
 
@@ -554,25 +600,26 @@ def expert_plan(ids, n_experts: int, offsets=None, rows=None, slots=None):
     rows[r], choice (m, j) is row slots[m, j].  A number outside [0, n_experts) has no row and slot -1; entries of
     rows from offsets[n_experts] on keep what they hold."""
     torch = _torch()
-    _on_device(None, ids=ids)
-    dev = ids.device
-    _on_device(dev, offsets=offsets, rows=rows, slots=slots)
-    if ids.dim() != 2 or ids.dtype not in (torch.int32, torch.int64) or not ids.is_contiguous():
+    idx = _gpu_index("ids", ids)
+    _same_device(idx, offsets=offsets, rows=rows, slots=slots)
+    i32 = torch.int32
+    if ids.dim() != 2 or ids.dtype not in (i32, torch.int64) or not ids.is_contiguous():
         raise ValueError("ids must be a contiguous int32 or int64 [M, top] tensor")
     M, top = ids.shape
+    if n_experts < 1:
+        raise ValueError("n_experts must be positive")
     for name, t, shape in (("offsets", offsets, (n_experts + 1,)), ("rows", rows, (M * top,)),
                            ("slots", slots, (M, top))):
-        if t is not None and (tuple(t.shape) != shape or t.dtype != torch.int32 or not t.is_contiguous()):
+        if t is not None and (t.shape != shape or t.dtype != i32 or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous int32 {list(shape)} tensor")
     if offsets is None:
-        offsets = torch.empty(max(0, n_experts) + 1, dtype=torch.int32, device=dev)
+        offsets = torch.empty(n_experts + 1, dtype=i32, device=ids.device)
     if rows is None:
-        rows = torch.empty(M * top, dtype=torch.int32, device=dev)
+        rows = torch.empty(M * top, dtype=i32, device=ids.device)
     if slots is None:
-        slots = torch.empty((M, top), dtype=torch.int32, device=dev)
-    with _on_current(dev):
-        _check(lib().bsf8_expert_plan(ids.data_ptr(), ids.element_size(), M, top, n_experts, offsets.data_ptr(),
-                                      rows.data_ptr(), slots.data_ptr(), _stream_ptr(dev)), "expert_plan")
+        slots = torch.empty((M, top), dtype=i32, device=ids.device)
+    _launch("expert_plan", idx, lib().bsf8_expert_plan, ids.data_ptr(), ids.element_size(), M, top, n_experts,
+            offsets.data_ptr(), rows.data_ptr(), slots.data_ptr())
     return offsets, rows, slots
 
 

@@ -338,6 +338,9 @@ bsf8_status bsf8_quant_norm(const bsf8_norm_args* p, void* stream) {
   a.gate_vec = vec(q.gate, a.gate_bf16 != 0, q.ldg);
   a.w_vec = vec(q.weight, a.w_bf16 != 0, 0) & vec(q.bias, a.w_bf16 != 0, 0);
   a.q_vec = reinterpret_cast<uintptr_t>(q.xq) % 8 == 0 && q.ldq % 8 == 0 ? 1 : 0;
+  a.wide = q.K % 8 == 0 && a.x_vec && a.res_vec && a.h_vec && a.n_vec && a.q_vec && a.post_vec && a.gate_vec && a.w_vec &&
+                   (!q.post_weight || a.post_bf16 == a.w_bf16) && (!q.gate || a.gate_bf16 == a.w_bf16)
+               ? 1 : 0;
   misaligned = misaligned || reinterpret_cast<uintptr_t>(q.xs) % 4 || reinterpret_cast<uintptr_t>(q.slots) % 4 ||
                reinterpret_cast<uintptr_t>(q.probs) % 4;
   if (misaligned) return fail(BSF8_E_ALIGNMENT, "an address is not element aligned");

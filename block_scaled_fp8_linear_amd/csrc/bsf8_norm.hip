@@ -175,6 +175,43 @@ __device__ __forceinline__ void row_stats(const double (&v)[V][EPL], const int (
   rstd = 1.0 / sqrt(row_sum<T>(q, lds) / double(K) + eps);
 }
 
+// The scale of a group, max(amax, 1e-10) / 448, and EPL codes, bit for bit what
+// the IEEE divisions of the activation quantizer give, without dividing.  With r
+// = RN(1 / b), q0 = a * r and the exact remainder e = a - q0 * b (one FMA), RN(q0
+// + e * r) is the correctly rounded quotient a / b (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990).  For
+// the scale r is a constant.  For the codes r comes from the hardware's F64
+// reciprocal and two Newton steps (relative error below 2^-52; 1 / s is at least
+// 2^-49 from a midpoint of two F32 values), rounded to F32.  The remainder is
+// exact for |n| >= 2^-100; below, n / s < 2^-57 and its code is zero whatever
+// its last bit.  A negative zero passes the remainder as +0, so the sign of n
+// is put back.  No clamp: |n| <= amax makes the quotient at most 448 (1 +
+// 2^-23), which rounds to the code of 448.
+__device__ __forceinline__ void encode(const float (&n)[EPL], float amax, float& s, uint32_t (&packed)[EPL / 4]) {
+  const float a = fmaxf(amax, kAmaxFloor);
+  constexpr float kInv = 1.0f / kE4M3Max;
+  const float s0 = a * kInv;
+  s = fmaf(fmaf(-s0, kE4M3Max, a), kInv, s0);
+  const double sd = double(s);
+  double rd = __builtin_amdgcn_rcp(sd);
+  rd = fma(fma(-sd, rd, 1.0), rd, rd);
+  rd = fma(fma(-sd, rd, 1.0), rd, rd);
+  const float r = static_cast<float>(rd);
+#pragma unroll
+  for (int q = 0; q < EPL / 4; ++q) {
+    float f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float v = n[4 * q + e];
+      const float f0 = v * r;
+      f[e] = copysignf(fmaf(fmaf(-f0, s, v), r, f0), v);
+    }
+    int pk = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+    pk = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], pk, true);
+    packed[q] = uint32_t(pk);
+  }
+}
+
 // T threads per row (64: four rows per block), V vectors of EPL channels each.
 template <int T, int V, bool XBF16, bool HBF16>
 __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(NormDev a) {
@@ -281,21 +318,9 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
     if (a.xq == nullptr) continue;
 #pragma unroll
     for (int d = LPG / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, LPG));
-    // as the activation quantizer: the F64 product with fl64(1 / s) rounds to
-    // the IEEE F32 quotient n / s
-    const float s = fmaxf(amax, kAmaxFloor) / kE4M3Max;
-    const double rs = 1.0 / static_cast<double>(s);
+    float s;
     uint32_t packed[EPL / 4];
-#pragma unroll
-    for (int q = 0; q < EPL / 4; ++q) {
-      float f[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        f[e] = fminf(fmaxf(static_cast<float>(static_cast<double>(n[4 * q + e]) * rs), -kE4M3Max), kE4M3Max);
-      int pk = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-      pk = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], pk, true);
-      packed[q] = uint32_t(pk);
-    }
+    encode(n, amax, s, packed);
     if (valid[i] > 0) {
       uint8_t* q = a.xq + m * a.ldq + k[i];
       if (valid[i] == EPL && a.q_vec) {
@@ -310,6 +335,294 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
   }
 }
 
+// ---------------------------------------------------------------------------
+// Rows whose length is a multiple of EPL, up to 16384, and whose addresses all
+// allow 16-byte accesses: no tests inside a vector.  One row per block of
+// blockDim.x threads with V vectors each; only the last vector can lie past K,
+// and it then reads the row's first vector and is zeroed.
+//
+// What bounds it: some 20 to 45 instructions per channel at about 5 cycles per
+// wave and instruction (F64 FMAs and the conversions run at the F32 rate) lie
+// close to the time of the memory traffic, so the two must overlap, and waves
+// in flight are what overlaps them: the test-free form at 128 registers (four
+// waves per SIMD) takes [8192, 7168] BF16 with residual, post norm and gate in
+// 118 us and with the residual alone in 87 us (410 MB; a copy of as much takes
+// 84 us), [8192, 5120] in 78 and 58 us.  Tried and slower: the general kernel
+// above for these rows (205 us; two waves per SIMD and a branch around every
+// load), blocks that stay and prefetch their next row (175 us; the registers of
+// the second row halve the waves), two rows per block sharing the weights'
+// conversions (155 us), one vector per thread (132 us; more waves wait at each
+// barrier), IEEE divisions in place of encode() and 1 / sqrt() in place of
+// rsqrt64().  One row takes 3.5 us.
+// ---------------------------------------------------------------------------
+
+template <bool BF16>
+__device__ __forceinline__ void load_wide(const void* p, int64_t off, Raw<BF16>& r) {
+  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + off * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const uint4 u = q[i];
+    r.w[4 * i] = u.x;
+    r.w[4 * i + 1] = u.y;
+    r.w[4 * i + 2] = u.z;
+    r.w[4 * i + 3] = u.w;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void clear(Raw<BF16>& r) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? EPL / 2 : EPL); ++i) r.w[i] = 0;
+}
+
+// s moved by a DPP control word, 0.0 where no lane is the source
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp(double s) {
+  const int2 v = __builtin_bit_cast(int2, s);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_update_dpp(0, v.x, CTRL, ROWS, 0xf, false),
+                                              __builtin_amdgcn_update_dpp(0, v.y, CTRL, ROWS, 0xf, false)));
+}
+
+__device__ __forceinline__ double lane_value(double s, int lane) {
+  const int2 v = __builtin_bit_cast(int2, s);
+  return __builtin_bit_cast(double, make_int2(__builtin_amdgcn_readlane(v.x, lane), __builtin_amdgcn_readlane(v.y, lane)));
+}
+
+// Sum over the block, in every thread: lanes through DPP (rows of 16, then the
+// rows' last lanes onwards; lane 63 ends with the wave's sum), waves through
+// LDS in wave order.  Two exchange rows taken in turn: a row is written again
+// only after the barrier of the sum between, which every thread reaches after
+// it has read the row.
+__device__ __forceinline__ double block_sum(double s, double (*lds)[16], int& turn) {
+  s += dpp<0x111, 0xf>(s);   // row_shr:1
+  s += dpp<0x112, 0xf>(s);   // row_shr:2
+  s += dpp<0x114, 0xf>(s);   // row_shr:4
+  s += dpp<0x118, 0xf>(s);   // row_shr:8
+  s += dpp<0x142, 0xa>(s);   // row_bcast:15 into rows 1 and 3
+  s += dpp<0x143, 0xc>(s);   // row_bcast:31 into rows 2 and 3
+  s = lane_value(s, 63);
+  const int waves = blockDim.x >> 6;
+  if (waves == 1) return s;
+  turn ^= 1;
+  const int lane = threadIdx.x & 63;
+  if (lane == 0) lds[turn][threadIdx.x >> 6] = s;
+  __syncthreads();
+  s = (lane & 15) < waves ? lds[turn][lane & 15] : 0.0;
+  s += dpp<0x111, 0xf>(s);
+  s += dpp<0x112, 0xf>(s);
+  s += dpp<0x114, 0xf>(s);
+  s += dpp<0x118, 0xf>(s);
+  return lane_value(s, 15);
+}
+
+// 1 / sqrt(x) to within an F64 rounding or two: the hardware's estimate and two Newton steps
+__device__ __forceinline__ double rsqrt64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = fma(0.5 * y, fma(-x * y, y, 1.0), y);
+  return y;
+}
+
+// norm(v) as v * rstd + c; `on`: the last vector lies in the row
+template <int V>
+__device__ __forceinline__ void wide_stats(const double (&v)[V][EPL], bool on, const NormDev& a, double inv_k,
+                                           double (*lds)[16], int& turn, double& rstd, double& c) {
+  double mean = 0.0, q = 0.0;
+  if (a.layer) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) mean += v[i][e];
+    mean = block_sum(mean, lds, turn) * inv_k;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i == V - 1 && !on) continue;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        const double d = v[i][e] - mean;
+        q = fma(d, d, q);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) q = fma(v[i][e], v[i][e], q);
+  }
+  rstd = rsqrt64(fma(block_sum(q, lds, turn), inv_k, a.eps));
+  c = -mean * rstd;
+}
+
+// COMBINE: x holds the experts' rows.
+template <int V, bool COMBINE, bool XBF16, bool HBF16, bool WBF16>
+__global__ __launch_bounds__(V == 1 ? 128 : 1024) void quant_norm_wide_kernel(NormDev a) {
+  __shared__ double lds[2][16];
+  int turn = 0;
+  const int t = threadIdx.x;
+  const int K = a.K;
+  int k[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) k[i] = (t + int(blockDim.x) * i) * EPL;
+  const bool on = k[V - 1] < K;
+  if (!on) k[V - 1] = 0;
+  const double inv_k = 1.0 / double(K);
+  const int64_t m = blockIdx.x;
+
+  // ---- the block's output; the residual's loads go out with it
+  Raw<HBF16> res[V];
+  double v[V][EPL];
+  if constexpr (!COMBINE) {
+    Raw<XBF16> x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) load_wide<XBF16>(a.x, m * a.ldx + k[i], x[i]);
+    if (a.res != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) load_wide<HBF16>(a.res, m * a.ldr + k[i], res[i]);
+    }
+    if (!on) clear(x[V - 1]);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = double(value<XBF16>(x[i], e));
+  } else {
+    if (a.res != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) load_wide<HBF16>(a.res, m * a.ldr + k[i], res[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = 0.0;
+    // four choices at a time: their rows' loads are in flight together
+    constexpr int J = 4;
+    for (int j0 = 0; j0 < a.top; j0 += J) {
+      Raw<XBF16> xj[J][V];
+      double p[J];
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const int64_t at = m * a.top + min(j0 + j, a.top - 1);
+        const int slot = a.slots[at];
+        const bool ok = j0 + j < a.top && slot >= 0 && slot < a.R;
+        p[j] = ok ? double(a.probs[at]) : 0.0;
+        if (ok) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) load_wide<XBF16>(a.x, int64_t(slot) * a.ldx + k[i], xj[j][i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) clear(xj[j][i]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          if (i == V - 1 && !on) clear(xj[j][i]);
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) v[i][e] = fma(p[j], double(value<XBF16>(xj[j][i], e)), v[i][e]);
+        }
+    }
+  }
+  Raw<WBF16> w[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) load_wide<WBF16>(a.w, k[i], w[i]);
+  // lanes past the row: weight zero, so that n is 0 and leaves the group's amax to the others
+  if (!on) clear(w[V - 1]);
+
+  // ---- norm of the block's output
+  if (a.post_w != nullptr) {
+    Raw<WBF16> wp[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) load_wide<WBF16>(a.post_w, k[i], wp[i]);
+    double rstd, c;
+    wide_stats<V>(v, on, a, inv_k, lds, turn, rstd, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = fma(v[i][e], rstd, c) * double(value<WBF16>(wp[i], e));
+    if (a.post_b != nullptr) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        load_wide<WBF16>(a.post_b, k[i], wp[i]);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) v[i][e] += double(value<WBF16>(wp[i], e));
+      }
+    }
+  }
+  // ---- gate
+  if (a.gate != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      Raw<WBF16> g;
+      load_wide<WBF16>(a.gate, m * a.ldg + k[i], g);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] *= double(value<WBF16>(g, e));
+    }
+  }
+  // ---- residual, the stored stream
+  if (a.res != nullptr) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = fma(a.alpha, double(value<HBF16>(res[i], e)), v[i][e]);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool past = i == V - 1 && !on;
+    float h[EPL];
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      h[e] = to_f32(v[i][e]);
+      if (past) h[e] = 0.f;
+    }
+    if (HBF16) {
+      const uint32_t p[4] = {bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3]), bf16_pair(h[4], h[5]), bf16_pair(h[6], h[7])};
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        v[i][e] = double(__uint_as_float((e & 1) ? p[e >> 1] & 0xFFFF0000u : p[e >> 1] << 16));
+      if (a.h != nullptr && !past)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h) + m * a.ldh + k[i]) = make_uint4(p[0], p[1], p[2], p[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) v[i][e] = double(h[e]);
+      if (a.h != nullptr && !past) store_row(a.h, false, m * a.ldh + k[i], EPL, true, h);
+    }
+  }
+
+  // ---- the next block's norm, and its codes
+  double rstd, c;
+  wide_stats<V>(v, on, a, inv_k, lds, turn, rstd, c);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool past = i == V - 1 && !on;
+    float n[EPL];
+    if (a.b != nullptr) {
+      Raw<WBF16> b;
+      load_wide<WBF16>(a.b, k[i], b);
+      if (past) clear(b);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e)
+        n[e] = to_f32(fma(fma(v[i][e], rstd, c), double(value<WBF16>(w[i], e)), double(value<WBF16>(b, e))));
+    } else {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) n[e] = to_f32(fma(v[i][e], rstd, c) * double(value<WBF16>(w[i], e)));
+    }
+    if (a.n != nullptr && !past) store_row(a.n, a.n_bf16, m * a.ldn + k[i], EPL, true, n);
+    if (a.xq == nullptr) continue;
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(n[e]));
+#pragma unroll
+    for (int d = LPG / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, LPG));
+    float s;
+    uint32_t q[EPL / 4];
+    encode(n, amax, s, q);
+    if (!past) {
+      *reinterpret_cast<uint2*>(a.xq + m * a.ldq + k[i]) = make_uint2(q[0], q[1]);
+      if ((t & (LPG - 1)) == 0) a.xs[m * a.xs_sm + int64_t(k[i] / kBlock) * a.xs_sk] = s;
+    }
+  }
+}
+
 using Kern = void (*)(NormDev);
 
 template <int T, int V>
@@ -318,27 +631,38 @@ Kern pick(bool x_bf16, bool h_bf16) {
                 : (h_bf16 ? quant_norm_kernel<T, V, false, true> : quant_norm_kernel<T, V, false, false>);
 }
 
+template <int V, bool COMBINE>
+Kern pick_wide(bool x_bf16, bool h_bf16, bool w_bf16) {
+#define BSF8_WIDE(X, H) (w_bf16 ? quant_norm_wide_kernel<V, COMBINE, X, H, true> : quant_norm_wide_kernel<V, COMBINE, X, H, false>)
+  return x_bf16 ? (h_bf16 ? BSF8_WIDE(true, true) : BSF8_WIDE(true, false))
+                : (h_bf16 ? BSF8_WIDE(false, true) : BSF8_WIDE(false, false));
+#undef BSF8_WIDE
+}
+
 }  // namespace
 
 bsf8_status launch_quant_norm(const NormDev& a, bool x_bf16, bool h_bf16, hipStream_t stream) {
   const int vecs = (a.K + EPL - 1) / EPL;
   Kern kern;
-  int T;
-  if (vecs <= 64) {
-    T = 64;
+  int threads, rows;
+  if (a.wide && vecs <= 2048) {
+    // a block's first vector must lie in the row, so fewer than 128 vectors take one each
+    rows = 1;
+    threads = vecs < 128 ? (vecs + 63) / 64 * 64 : ((vecs + 1) / 2 + 63) / 64 * 64;
+    if (vecs < 128)
+      kern = a.slots ? pick_wide<1, true>(x_bf16, h_bf16, a.w_bf16) : pick_wide<1, false>(x_bf16, h_bf16, a.w_bf16);
+    else
+      kern = a.slots ? pick_wide<2, true>(x_bf16, h_bf16, a.w_bf16) : pick_wide<2, false>(x_bf16, h_bf16, a.w_bf16);
+  } else if (vecs <= 64) {
+    threads = kSmallBlock;
+    rows = kSmallBlock / 64;
     kern = pick<64, 1>(x_bf16, h_bf16);
-  } else if (vecs <= 1024) {
-    T = 256;
-    kern = vecs <= 256 ? pick<256, 1>(x_bf16, h_bf16)
-           : vecs <= 512 ? pick<256, 2>(x_bf16, h_bf16)
-           : vecs <= 768 ? pick<256, 3>(x_bf16, h_bf16)
-                         : pick<256, 4>(x_bf16, h_bf16);
   } else {
-    T = 1024;
-    kern = vecs <= 2048 ? pick<1024, 2>(x_bf16, h_bf16) : pick<1024, 4>(x_bf16, h_bf16);
+    threads = vecs <= 1024 ? 256 : 1024;
+    rows = 1;
+    kern = vecs <= 1024 ? pick<256, 4>(x_bf16, h_bf16) : pick<1024, 4>(x_bf16, h_bf16);
   }
-  const int rows = T == 64 ? kSmallBlock / 64 : 1;
-  hipLaunchKernelGGL(kern, dim3(unsigned((a.M + rows - 1) / rows)), dim3(T == 64 ? kSmallBlock : T), 0, stream, a);
+  hipLaunchKernelGGL(kern, dim3(unsigned((int64_t(a.M) + rows - 1) / rows)), dim3(threads), 0, stream, a);
   return device_status(hipGetLastError(), "quant_norm launch");
 }
 
