@@ -13,6 +13,8 @@ Entry points mirror ``include/bsf8.h``:
 * ``quant_norm(x, weight, ...)``        residual add, norms and gate between two blocks -> codes, scales, stream
 * ``expert_plan(ids, n_experts)``       router choices -> row ranges of the experts, gather rows, slots
 * ``linear_w8a16(w, x)``                F32-activation arm
+* ``linear_w8a8_epilogue(w, xq, xs, ...)``  linear_w8a8 with bias, activation and residual in the same call
+* ``ExpertsFP8Weight(members)``, ``linear_w8a8_experts(w, xq, xs, offsets, rows)``  products grouped by expert
 * ``linear_w8a8(w, xq, xs)``            FP8 x FP8 arm with F32 epilogue
 """
 from __future__ import annotations
@@ -27,7 +29,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("BSF8_LIBRARY") or os.path.join(_HERE, "libbsf8.so")
 
 DT_INVALID, DT_F8_E4M3, DT_F8_E5M2, DT_BF16, DT_F16, DT_F32, DT_U8, DT_OTHER = range(8)
-ARM_W8A16, ARM_W8A8, ARM_DENSE, ARM_W8A8_DYNAMIC = 0, 1, 2, 3
+ARM_W8A16, ARM_W8A8, ARM_DENSE, ARM_W8A8_DYNAMIC, ARM_W8A8_EPILOGUE = 0, 1, 2, 3, 4
 DTYPE_NAMES = {"F8_E4M3": DT_F8_E4M3, "F8_E5M2": DT_F8_E5M2, "BF16": DT_BF16, "F16": DT_F16,
                "F32": DT_F32, "U8": DT_U8}
 MAX_MEMBERS = 8
@@ -66,6 +68,12 @@ class NormArgs(ctypes.Structure):
                 ("h_dtype", _i32), ("weight", _ptr), ("bias", _ptr), ("weight_dtype", _i32), ("n", _ptr),
                 ("n_dtype", _i32), ("ldn", _i64), ("xq", _ptr), ("ldq", _i64), ("xs", _ptr), ("xs_sm", _i64),
                 ("xs_sk", _i64)]
+
+
+class Epilogue(ctypes.Structure):
+    """bsf8_epilogue."""
+    _fields_ = [("bias", _ptr), ("bias_dtype", _i32), ("activation", _i32), ("residual", _ptr),
+                ("residual_dtype", _i32), ("ldr", _i64), ("residual_scale", ctypes.c_float)]
 
 
 class Unit(ctypes.Structure):
@@ -118,6 +126,15 @@ EXPORTS = [
                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_glu_act", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                     ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p]),
+    ("bsf8_linear_w8a8_epilogue", ctypes.c_int, [_ptr, _ptr, _i64, _ptr, _i64, _i64, _i64, ctypes.POINTER(Epilogue),
+                                                 _ptr, _i32, _i64, _ptr, ctypes.c_size_t, _ptr]),
+    ("bsf8_experts_create", ctypes.c_int, [ctypes.POINTER(Decl), ctypes.POINTER(MemberDesc), _i32,
+                                           ctypes.POINTER(_ptr)]),
+    ("bsf8_experts_destroy", None, [_ptr]),
+    ("bsf8_experts_geometry", ctypes.c_int, [_ptr, ctypes.POINTER(_i64), ctypes.POINTER(_i64), ctypes.POINTER(_i64)]),
+    ("bsf8_linear_w8a8_experts", ctypes.c_int, [_ptr, _ptr, _i64, _ptr, _i64, _i64, _i64, _ptr, _ptr, _i64, _ptr,
+                                                _i32, _i64, _ptr]),
+    ("bsf8_experts_describe", ctypes.c_char_p, [_ptr, _i64]),
     ("bsf8_quant_norm", ctypes.c_int, [ctypes.POINTER(NormArgs), ctypes.c_void_p]),
     ("bsf8_expert_plan", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
@@ -660,6 +677,134 @@ def linear_w8a8(w: BlockFP8Weight, xq, xs, out_dtype=None, out=None, workspace=N
     return y
 
 
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _quantized(xq, xs, K):
+    """(tokens, code pitch, scale strides) of a quantizer's output for K channels."""
+    torch = _torch()
+    if xq.dim() != 2:
+        raise ValueError("xq must be 2-D")
+    M = xq.shape[0]
+    ldq = _pitch("xq", xq, M, K, (torch.uint8, torch.float8_e4m3fn))
+    if xs.shape != (M, -(-K // BLOCK)) or xs.dtype != torch.float32:
+        raise ValueError("xs must be float32 [M, ceil(K/128)]")
+    sm, sk = xs.stride()
+    return M, ldq, sm, sk
+
+
+def _output(out, M, N, dtype, device):
+    """(out, pitch): ``out`` checked, or a new [M, N] of ``dtype``."""
+    if out is None:
+        return _torch().empty((M, N), dtype=dtype, device=device), N
+    out = _out(out, M, N, dtype, device)
+    if M > 1 and out.stride(0) < N:
+        raise ValueError("out's rows must not overlap")
+    return out, max(out.stride(0), N)
+
+
+def linear_w8a8_epilogue(w: BlockFP8Weight, xq, xs, *, bias=None, activation=None, residual=None, residual_scale=1.0,
+                         out_dtype=None, out=None, workspace=None):
+    """linear_w8a8 and what follows it in one call: y = activation(x . W^T + bias) + residual_scale * residual.
+
+    bias: [N]; residual: [M, N], which may be ``out`` itself (float32 or bfloat16 both); activation: None, "relu",
+    "silu", "gelu" or "gelu_tanh".  y is bfloat16 unless out_dtype says float32."""
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    out_dtype = out_dtype or torch.bfloat16
+    idx = w.device.index
+    _same_device(idx, xq=xq, xs=xs, bias=bias, residual=residual, out=out,
+                 workspace=workspace[0] if workspace is not None else None)
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
+    M, ldq, sm, sk = _quantized(xq, xs, w.K)
+    N = w.n_total
+    e = Epilogue()
+    e.activation = ACTIVATIONS[activation]
+    if bias is not None:
+        e.bias, e.bias_dtype = _vector("bias", bias, N, real), _dt_of(bias)
+    if residual is not None:
+        e.residual, e.ldr = residual.data_ptr(), _pitch("residual", residual, M, N, real)
+        e.residual_dtype, e.residual_scale = _dt_of(residual), residual_scale
+    y, ldy = _output(out, M, N, out_dtype, w.device)
+    ws, wsb = workspace if workspace is not None else w.workspace(ARM_W8A8_EPILOGUE, M)
+    _launch("linear_w8a8_epilogue", idx, lib().bsf8_linear_w8a8_epilogue, w.handle, xq.data_ptr(), ldq, xs.data_ptr(),
+            sm, sk, M, ctypes.byref(e), y.data_ptr(), _dt_of(y), ldy, ws.data_ptr() if ws is not None else None, wsb)
+    return y
+
+
+class ExpertsFP8Weight:
+    """Immutable handle over the block-FP8 weights of E experts on the GPU.
+
+    ``members``: list of (weight, scale_inv) device tensors; weight is uint8 or float8_e4m3fn [E, N_i, K], scale_inv
+    bfloat16 or float32 [E, ceil(N_i/128), ceil(K/128)], both contiguous.  A gated layer has two members, gate and
+    up (or one that holds both, where their rows are a multiple of 128).  The tensors are borrowed, as
+    BlockFP8Weight's are."""
+
+    def __init__(self, members: Sequence[Tuple[object, object]], quant_method: str = "fp8", block=(BLOCK, BLOCK)):
+        L = lib()
+        if len(members) == 0:
+            raise ValueError("a weight needs at least one member")
+        descs, self._tensors = [], []
+        dev0 = members[0][0].device
+        for i, (w, s) in enumerate(members):
+            _on_device(dev0 if dev0.type == "cuda" else None, **{f"member {i} weight": w, f"member {i} scale": s})
+            if not (w.is_contiguous() and s.is_contiguous()):
+                raise ValueError("weights and scale grids must be contiguous")
+            if w.dim() > 4 or s.dim() > 4:
+                raise ValueError("weights and scale grids must be 3-D")
+            wdt = DT_F8_E4M3 if _dt_of(w) in (DT_U8, DT_F8_E4M3) else _dt_of(w)
+            descs.append({"weight": dict(dtype=wdt, shape=tuple(w.shape), addr=w.data_ptr()),
+                          "scale_inv": dict(dtype=_dt_of(s), shape=tuple(s.shape), addr=s.data_ptr())})
+            self._tensors += [w, s]
+        decl = _decl(quant_method, block)
+        arr, _keep = _members_array(descs)
+        h = ctypes.c_void_p()
+        _check(L.bsf8_experts_create(ctypes.byref(decl), arr, len(descs), ctypes.byref(h)), "experts_create")
+        self._h = h
+        self.device = dev0
+        e, n, k = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+        _check(L.bsf8_experts_geometry(h, ctypes.byref(e), ctypes.byref(n), ctypes.byref(k)), "experts_geometry")
+        self.n_experts, self.n_total, self.K = e.value, n.value, k.value
+
+    @property
+    def handle(self):
+        return self._h
+
+    def __del__(self):
+        h = getattr(self, "_h", None)
+        if h is not None and _lib is not None:
+            _lib.bsf8_experts_destroy(h)
+            self._h = None
+
+    def describe(self, R: int) -> str:
+        return lib().bsf8_experts_describe(self._h, R).decode()
+
+
+def linear_w8a8_experts(w: ExpertsFP8Weight, xq, xs, offsets, rows=None, out_dtype=None, out=None):
+    """The experts' products of ragged row runs: y[r] = x[rows[r]] . W_e^T for r in [offsets[e], offsets[e+1]).
+
+    xq, xs: M tokens as the quantizers give them; offsets: int32 [E + 1] and rows: int32 [R], on the GPU, as
+    expert_plan gives them (without ``rows``, row r is token r and R = M).  y [R, N] is bfloat16 unless out_dtype
+    says float32; rows outside every run keep what ``out`` holds, and a row whose token is outside [0, M) is zero.
+    The runs are read on the GPU: nothing here waits for them, and a captured call follows their new values."""
+    torch = _torch()
+    out_dtype = out_dtype or torch.bfloat16
+    idx = w.device.index
+    _same_device(idx, xq=xq, xs=xs, offsets=offsets, rows=rows, out=out)
+    M, ldq, sm, sk = _quantized(xq, xs, w.K)
+    i32 = (torch.int32,)
+    off = _vector("offsets", offsets, w.n_experts + 1, i32)
+    R, at = M, None
+    if rows is not None:
+        R = rows.numel()
+        at = _vector("rows", rows, R, i32)
+    y, ldy = _output(out, R, w.n_total, out_dtype, w.device)
+    _launch("linear_w8a8_experts", idx, lib().bsf8_linear_w8a8_experts, w.handle, xq.data_ptr(), ldq, xs.data_ptr(),
+            sm, sk, M, off, at, R, y.data_ptr(), _dt_of(y), ldy)
+    return y
+
+
 def linear_w8a8_dynamic(w: BlockFP8Weight, x, out_dtype=None, out=None, workspace=None):
     """W8A8 arm on unquantized activations: x (float32 or bfloat16 [M, K]) is quantized per
     token in 1x128 groups as quant_act does and multiplied as linear_w8a8 does, bit for bit,
@@ -750,7 +895,8 @@ def linear_dense(wd, x, out_dtype=None, out=None, workspace=None):
 
 
 __all__ = ["BSF8Error", "BlockFP8Weight", "validate", "quant_act", "quant_glu", "glu_act", "quant_norm", "expert_plan", "linear_w8a16", "linear_w8a8",
-           "linear_w8a8_dynamic", "linear_w8a8_noalloc", "NOALLOC_SCRATCH_BYTES", "upcast",
+           "linear_w8a8_dynamic", "linear_w8a8_noalloc", "linear_w8a8_epilogue", "linear_w8a8_experts",
+           "ExpertsFP8Weight", "ARM_W8A8_EPILOGUE", "NOALLOC_SCRATCH_BYTES", "upcast",
            "linear_dense", "dense_workspace_size", "lib", "status_name", "ARM_W8A16", "ARM_W8A8", "ARM_DENSE",
            "ARM_W8A8_DYNAMIC",
            "EXPORTS", "LIB_PATH", "MAX_MEMBERS", "scales_kmajor"]

@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <new>
 #include <string>
 
 #include "bsf8_internal.h"
@@ -411,6 +412,7 @@ bsf8_status bsf8_workspace_size(const bsf8_weight* w, int32_t arm, int64_t M, si
   else if (arm == BSF8_ARM_W8A8) *bytes = M ? w8a8_workspace_bytes(w->dev, M) : 0;
   else if (arm == BSF8_ARM_DENSE) *bytes = M ? dense_workspace_bytes(w->n_total, w->dev.K, M) : 0;
   else if (arm == BSF8_ARM_W8A8_DYNAMIC) *bytes = M ? dyn_layout(w->dev, M).total : 0;
+  else if (arm == BSF8_ARM_W8A8_EPILOGUE) *bytes = 0;
   else return fail(BSF8_E_INVALID_ARG, "arm %d", arm);
   return BSF8_OK;
 }
@@ -542,6 +544,159 @@ bsf8_status bsf8_linear_w8a8_dynamic(const bsf8_weight* w, const void* x, int32_
                      L.gemm_bytes ? base + L.gemm_off : nullptr, L.gemm_bytes, st);
 }
 
+bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, int64_t ldq, const float* xs,
+                                      int64_t xs_sm, int64_t xs_sk, int64_t M, const bsf8_epilogue* e, void* y,
+                                      int32_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                      void* stream) {
+  if (w == nullptr) return fail(BSF8_E_INVALID_ARG, "null handle");
+  if (e == nullptr) return fail(BSF8_E_INVALID_ARG, "null epilogue");
+  if (M < 0) return fail(BSF8_E_INVALID_ARG, "negative M");
+  if (!dtype_ok(y_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "y dtype %d (F32 or BF16)", y_dtype);
+  if (e->activation < BSF8_ACT_NONE || e->activation > BSF8_ACT_GELU_TANH)
+    return fail(BSF8_E_INVALID_ARG, "activation %d", e->activation);
+  if ((e->bias && !dtype_ok(e->bias_dtype, true, true)) || (e->residual && !dtype_ok(e->residual_dtype, true, true)))
+    return fail(BSF8_E_INVALID_ARG, "bias or residual dtype (F32 or BF16)");
+  if (M == 0) return BSF8_OK;
+  if (xq == nullptr || xs == nullptr || y == nullptr) return fail(BSF8_E_INVALID_ARG, "null pointer");
+  if (ldq < w->dev.K || ldy < w->n_total || (e->residual && e->ldr < w->n_total))
+    return fail(BSF8_E_INVALID_ARG, "leading dimension too small");
+  if (!scale_layout_ok(M, w->dev.Kb, xs_sm, xs_sk))
+    return fail(BSF8_E_INVALID_ARG, "xs strides (%lld, %lld): neither token-major nor K-major", (long long)xs_sm,
+                (long long)xs_sk);
+  if (M > INT32_MAX / 2) return fail(BSF8_E_UNSUPPORTED, "M too large");
+  const size_t ye = y_dtype == BSF8_DT_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(xs) % 4 || reinterpret_cast<uintptr_t>(y) % ye ||
+      reinterpret_cast<uintptr_t>(e->bias) % (e->bias_dtype == BSF8_DT_BF16 ? 2 : 4) ||
+      reinterpret_cast<uintptr_t>(e->residual) % (e->residual_dtype == BSF8_DT_BF16 ? 2 : 4))
+    return fail(BSF8_E_ALIGNMENT, "xs, y, bias or residual not element aligned");
+  EpilogueDev ep{};
+  ep.bias = e->bias;
+  ep.res = e->residual;
+  ep.ldr = e->ldr;
+  ep.alpha = e->residual_scale;
+  ep.bias_bf16 = e->bias_dtype == BSF8_DT_BF16;
+  ep.res_bf16 = e->residual_dtype == BSF8_DT_BF16;
+  ep.act = e->activation;
+  const bool aligned = w->aligned16 && (reinterpret_cast<uintptr_t>(xq) % 16 == 0) && (ldq % 16 == 0);
+  return launch_w8a8_rows(w->dev, aligned, xq, ldq, xs, xs_sm, xs_sk, M, ep, y, y_dtype == BSF8_DT_BF16, ldy,
+                          static_cast<hipStream_t>(stream));
+}
+
+bsf8_status bsf8_experts_create(const bsf8_decl* decl, const bsf8_member_desc* members, int32_t n_members,
+                                bsf8_experts** out) {
+  if (out == nullptr) return fail(BSF8_E_INVALID_ARG, "out is NULL");
+  *out = nullptr;
+  if (decl == nullptr || (members == nullptr && n_members > 0)) return fail(BSF8_E_INVALID_ARG, "null descriptor");
+  if (n_members < 1 || n_members > kMaxMembers)
+    return fail(BSF8_E_GROUP, "%d members (1..%d allowed)", n_members, kMaxMembers);
+  if (decl->block_n == 0 && decl->block_k == 0) return fail(BSF8_E_DECL, "experts need weight_block_size [128,128]");
+  // one expert's slice of every member; a descriptor of another rank becomes
+  // one that the slice's checks refuse by rank
+  bsf8_member_desc slice[kMaxMembers];
+  bsf8_tensor_desc grid[kMaxMembers][2];
+  const auto cut = [](const bsf8_tensor_desc& t) {
+    bsf8_tensor_desc s = t;
+    s.rank = t.rank == 3 ? 2 : (t.rank < 0 || t.rank > 4 ? t.rank : 3);
+    for (int d = 0; d + 1 < 4; ++d) s.shape[d] = t.shape[d + 1];
+    return s;
+  };
+  for (int i = 0; i < n_members; ++i) {
+    slice[i].weight = cut(members[i].weight);
+    slice[i].scale_inv = slice[i].scale = nullptr;
+    if (members[i].scale_inv) {
+      grid[i][0] = cut(*members[i].scale_inv);
+      slice[i].scale_inv = &grid[i][0];
+    }
+    if (members[i].scale) {
+      grid[i][1] = cut(*members[i].scale);
+      slice[i].scale = &grid[i][1];
+    }
+  }
+  const bsf8_status st = validate_impl(decl, slice, n_members);
+  if (st != BSF8_OK) return st;
+  const int64_t E = members[0].weight.shape[0], K = slice[0].weight.shape[1];
+  int64_t total = 0;
+  for (int i = 0; i < n_members; ++i) {
+    const bsf8_member_desc& m = members[i];
+    if (m.weight.shape[0] <= 0) return fail(BSF8_E_WEIGHT_EMPTY, "member %d: %lld experts", i, (long long)m.weight.shape[0]);
+    if (m.weight.shape[0] != E) return fail(BSF8_E_GROUP, "member %d: another number of experts than member 0", i);
+    if (scale_leaf(m)->shape[0] != E) return fail(BSF8_E_SCALE_GRID, "member %d: grids of %lld experts, weights of %lld", i,
+                                                  (long long)scale_leaf(m)->shape[0], (long long)E);
+    if (m.weight.data == nullptr || scale_leaf(m)->data == nullptr)
+      return fail(BSF8_E_INVALID_ARG, "member %d: a handle needs device addresses", i);
+    total += m.weight.shape[1];
+  }
+  if (K > INT32_MAX / 2 || total > INT32_MAX / 2 || E > 65535)
+    return fail(BSF8_E_UNSUPPORTED, "N or K beyond 2^30, or more than 65535 experts");
+  bsf8_experts* h = new (std::nothrow) bsf8_experts();
+  if (h == nullptr) return fail(BSF8_E_UNSUPPORTED, "out of host memory");
+  std::memset(&h->dev, 0, sizeof(h->dev));
+  h->dev.n_members = n_members;
+  h->dev.K = int32_t(K);
+  h->dev.Kb = int32_t(ceil_div(K, kBlock));
+  h->dev.scale_bf16 = scale_leaf(members[0])->dtype == BSF8_DT_BF16 ? 1 : 0;
+  h->dev.s_rs = h->dev.Kb;
+  h->dev.s_cs = 1;
+  h->n_experts = E;
+  h->n_total = total;
+  h->aligned16 = K % 16 == 0;
+  int64_t col = 0;
+  for (int i = 0; i < n_members; ++i) {
+    h->dev.m[i].w = static_cast<const uint8_t*>(members[i].weight.data);
+    h->dev.m[i].s = scale_leaf(members[i])->data;
+    h->dev.m[i].rows = int32_t(members[i].weight.shape[1]);
+    h->dev.m[i].col0 = int32_t(col);
+    col += members[i].weight.shape[1];
+  }
+  *out = h;
+  return BSF8_OK;
+}
+
+void bsf8_experts_destroy(bsf8_experts* w) { delete w; }
+
+bsf8_status bsf8_experts_geometry(const bsf8_experts* w, int64_t* n_experts, int64_t* n_total, int64_t* k) {
+  if (w == nullptr) return fail(BSF8_E_INVALID_ARG, "null handle");
+  if (n_experts) *n_experts = w->n_experts;
+  if (n_total) *n_total = w->n_total;
+  if (k) *k = w->dev.K;
+  return BSF8_OK;
+}
+
+bsf8_status bsf8_linear_w8a8_experts(const bsf8_experts* w, const uint8_t* xq, int64_t ldq, const float* xs,
+                                     int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
+                                     const int32_t* rows, int64_t R, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* stream) {
+  if (w == nullptr) return fail(BSF8_E_INVALID_ARG, "null handle");
+  if (M < 0 || R < 0) return fail(BSF8_E_INVALID_ARG, "negative M or R");
+  if (!dtype_ok(y_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "y dtype %d (F32 or BF16)", y_dtype);
+  if (R == 0) return BSF8_OK;
+  // (M == 0 with rows: every row is one without a token, and there is nothing to point at)
+  if (M == 0) return fail(BSF8_E_INVALID_ARG, "%lld rows of no tokens", (long long)R);
+  if (xq == nullptr || xs == nullptr || offsets == nullptr || y == nullptr) return fail(BSF8_E_INVALID_ARG, "null pointer");
+  if (rows == nullptr && M < R) return fail(BSF8_E_INVALID_ARG, "%lld tokens for %lld rows without gather rows", (long long)M, (long long)R);
+  if (ldq < w->dev.K || ldy < w->n_total) return fail(BSF8_E_INVALID_ARG, "leading dimension too small");
+  if (!scale_layout_ok(M, w->dev.Kb, xs_sm, xs_sk))
+    return fail(BSF8_E_INVALID_ARG, "xs strides (%lld, %lld): neither token-major nor K-major", (long long)xs_sm,
+                (long long)xs_sk);
+  if (M > INT32_MAX / 2 || R > INT32_MAX / 2) return fail(BSF8_E_UNSUPPORTED, "M or R too large");
+  const size_t ye = y_dtype == BSF8_DT_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(xs) % 4 || reinterpret_cast<uintptr_t>(y) % ye ||
+      reinterpret_cast<uintptr_t>(offsets) % 4 || reinterpret_cast<uintptr_t>(rows) % 4)
+    return fail(BSF8_E_ALIGNMENT, "xs, offsets, rows or y not element aligned");
+  const bool aligned = w->aligned16 && (reinterpret_cast<uintptr_t>(xq) % 16 == 0) && (ldq % 16 == 0);
+  return launch_w8a8_experts(w->dev, w->n_experts, aligned, xq, ldq, xs, xs_sm, xs_sk, M, offsets, rows, R, y,
+                             y_dtype == BSF8_DT_BF16, ldy, static_cast<hipStream_t>(stream));
+}
+
+const char* bsf8_experts_describe(const bsf8_experts* w, int64_t R) {
+  if (w == nullptr) return nullptr;
+  char geo[256];
+  snprintf(geo, sizeof(geo), " | experts E=%lld N=%lld K=%d members=%d scales=%s", (long long)w->n_experts,
+           (long long)w->n_total, w->dev.K, w->dev.n_members, w->dev.scale_bf16 ? "bf16" : "f32");
+  g_describe = describe_w8a8_experts(w->dev, w->n_experts, w->aligned16, R > 0 ? R : 1) + geo;
+  return g_describe.c_str();
+}
+
 bsf8_status bsf8_linear_w8a8_noalloc(const bsf8_weight* w, const uint8_t* xq, int64_t ldq, const float* xs,
                                      int64_t xs_sm, int64_t xs_sk, int64_t M, void* y, int32_t y_dtype, int64_t ldy,
                                      void* stream) {
@@ -584,6 +739,7 @@ const char* bsf8_describe(const bsf8_weight* w, int32_t arm, int64_t M) {
                       ? describe_w8a8_dyn_stream(w->dev, M > 0 ? M : 1)
                       : "quant_act into the workspace (K-major scales), then " + describe_w8a8(w->dev, w->aligned16, M)) +
                   geo;
+  else if (arm == BSF8_ARM_W8A8_EPILOGUE) g_describe = describe_w8a8_epilogue(w->dev, w->aligned16, M > 0 ? M : 1) + geo;
   else g_describe = "unknown arm";
   return g_describe.c_str();
 }

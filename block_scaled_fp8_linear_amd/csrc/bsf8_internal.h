@@ -105,6 +105,25 @@ bsf8_status launch_w8a8_dyn_stream(const WeightDev& w, const void* x, bool x_bf1
 // (BSF8_NOALLOC_SCRATCH_BYTES bytes), looked up once per device.
 bsf8_status w8a8_noalloc_scratch(void** ptr);
 
+// What a product's epilogue does (null pointers: absent terms).
+struct EpilogueDev {
+  const void* bias;
+  const void* res;
+  int64_t ldr;
+  float alpha;
+  int32_t bias_bf16, res_bf16, act;
+};
+
+// The few-row kernel: one weight with an epilogue, and the experts' products.
+bsf8_status launch_w8a8_rows(const WeightDev& w, bool aligned, const uint8_t* xq, int64_t ldq, const float* xs,
+                             int64_t xs_sm, int64_t xs_sk, int64_t M, const EpilogueDev& ep, void* y, bool y_bf16,
+                             int64_t ldy, hipStream_t stream);
+bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
+                                const float* xs, int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
+                                const int32_t* rows, int64_t R, void* y, bool y_bf16, int64_t ldy, hipStream_t stream);
+std::string describe_w8a8_epilogue(const WeightDev& w, bool aligned, int64_t M);
+std::string describe_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, int64_t R);
+
 // Dense arm: the upcast copy and the BF16 GEMM over it (the fast W8A8 kernel's
 // dense instance).
 bsf8_status launch_upcast(const WeightDev& w, int64_t n_total, bool vec, void* out, bool out_bf16, int64_t ldo,
@@ -128,4 +147,11 @@ struct bsf8_weight {
   int64_t srow0[bsf8::kMaxMembers];  // B_i: origin of member i in the stacked grids
   bool aligned16;                    // K % 16 == 0 and every weight pointer 16-byte aligned
   bool per_tensor;                   // one scale per member (per-tensor layout) instead of a block grid
+};
+
+struct bsf8_experts {
+  bsf8::WeightDev dev;   // expert 0's members; expert e's lie e * rows * K bytes and e * grid elements on
+  int64_t n_experts;
+  int64_t n_total;
+  bool aligned16;
 };

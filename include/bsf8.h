@@ -92,8 +92,9 @@ typedef enum bsf8_arm {
   BSF8_ARM_W8A8 = 1,   /* per-token 1x128 E4M3 activations, F32 epilogue */
   BSF8_ARM_DENSE = 2,  /* the handle's upcast dense BF16 copy times BF16 activations (bsf8_linear_dense);
                           for bsf8_workspace_size and bsf8_describe */
-  BSF8_ARM_W8A8_DYNAMIC = 3  /* W8A8 on F32 or BF16 activations quantized in the same call
+  BSF8_ARM_W8A8_DYNAMIC = 3, /* W8A8 on F32 or BF16 activations quantized in the same call
                                 (bsf8_linear_w8a8_dynamic) */
+  BSF8_ARM_W8A8_EPILOGUE = 4 /* bsf8_linear_w8a8_epilogue */
 } bsf8_arm;
 
 /* Header-level description of one tensor.  data may be NULL for a header-only
@@ -422,6 +423,88 @@ bsf8_status bsf8_linear_w8a16(const bsf8_weight* w, const void* x, int32_t x_dty
 bsf8_status bsf8_linear_w8a8(const bsf8_weight* w, const uint8_t* xq, int64_t ldq, const float* xs,
                              int64_t xs_sm, int64_t xs_sk, int64_t M, void* y, int32_t y_dtype, int64_t ldy,
                              void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * bsf8_linear_w8a8_epilogue -- bsf8_linear_w8a8 with the element-wise step that
+ * follows a projection in the same launch:
+ *   y[m, n] = act(acc[m, n] + bias[n]) + residual_scale * residual[m, n]
+ * acc the F32 product of bsf8_linear_w8a8, everything F32, rounded once to
+ * y_dtype.  (The sums behind acc may be ordered otherwise than in
+ * bsf8_linear_w8a8, so the two agree within its bound, not bit for bit.)
+ *
+ * e->bias     : [N] F32 or BF16, or NULL.
+ * e->activation : bsf8_activation: none, relu, silu = v / (1 + exp(-v)), gelu =
+ *               v * Phi(v), gelu_tanh (its usual approximation
+ *               v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))).
+ * e->residual : [M, N] F32 or BF16, leading dimension ldr, or NULL.  It may be y
+ *               itself (same address, pitch and type); no other overlap.
+ * workspace   : bsf8_workspace_size with arm W8A8_EPILOGUE.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, WORKSPACE, DEVICE.
+ */
+typedef enum bsf8_activation {
+  BSF8_ACT_NONE = 0,
+  BSF8_ACT_RELU = 1,
+  BSF8_ACT_SILU = 2,
+  BSF8_ACT_GELU = 3,
+  BSF8_ACT_GELU_TANH = 4
+} bsf8_activation;
+typedef struct bsf8_epilogue {
+  const void* bias;
+  int32_t bias_dtype;
+  int32_t activation;
+  const void* residual;
+  int32_t residual_dtype;
+  int64_t ldr;
+  float residual_scale;
+} bsf8_epilogue;
+bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, int64_t ldq, const float* xs,
+                                      int64_t xs_sm, int64_t xs_sk, int64_t M, const bsf8_epilogue* e, void* y,
+                                      int32_t y_dtype, int64_t ldy, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Products grouped by expert, with ragged row counts.
+ * ("Module w8a8_prefill", section "WHY (#917 / #928)": the same FP8 product; a
+ *  routed layer has one weight per expert, stored as the checkpoint stores it:
+ *  E4M3 rows with their own 128x128 scale grid.)
+ *
+ * bsf8_experts_create -- an immutable handle over borrowed device pointers of
+ * E experts' weights.  Member i (gate and up of a gated layer are two) holds all
+ * experts' weights as one [E, N_i, K] E4M3 array and their grids as one
+ * [E, ceil(N_i/128), ceil(K/128)] BF16 or F32 array (descriptors of rank 3).  The
+ * checks and their order are bsf8_validate's on the slice of one expert;
+ * WEIGHT_RANK when a weight is not rank 3, SCALE_RANK when its grid is not,
+ * SCALE_GRID / GROUP when a grid / a member has another E, DECL for a per-tensor
+ * declaration.  E <= 65535.  Host-only.  bsf8_experts_destroy releases it.
+ *
+ * bsf8_linear_w8a8_experts -- for expert e and row r in [offsets[e], offsets[e+1]):
+ *   y[r, R_i + n] = sum_kb (xs[t, kb] * S_i,e[n/128, kb]) * sum_{k in kb} xq[t, k] * W_i,e[n, k]
+ * with t = rows[r], or t = r when rows is NULL; products exact, F32 sums, as
+ * bsf8_linear_w8a8.
+ * xq, xs  : M tokens, as bsf8_quant_act or bsf8_quant_norm writes them.
+ * offsets : device int32 [E + 1], ascending (bsf8_expert_plan writes it); an entry
+ *           outside [0, R] counts as the nearer end.  Where they descend, runs
+ *           overlap and their rows are undefined; no access leaves the arrays.
+ * rows    : device int32 [R], the token of each row, or NULL (then M >= R is
+ *           needed); a row whose token is outside [0, M) is written as zeros.
+ * y       : [R, N] BF16 or F32; rows outside every expert's run keep what they hold.
+ * The host learns nothing about the runs, so a call can be captured into a graph
+ * and replayed with other offsets; R bounds them.  No workspace.  R == 0 is a
+ * no-op.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, DEVICE.
+ *
+ * bsf8_experts_describe -- as bsf8_describe, for a call of R rows.
+ */
+typedef struct bsf8_experts bsf8_experts;
+bsf8_status bsf8_experts_create(const bsf8_decl* decl, const bsf8_member_desc* members, int32_t n_members,
+                                bsf8_experts** out);
+void bsf8_experts_destroy(bsf8_experts* w);
+bsf8_status bsf8_experts_geometry(const bsf8_experts* w, int64_t* n_experts, int64_t* n_total, int64_t* k);
+bsf8_status bsf8_linear_w8a8_experts(const bsf8_experts* w, const uint8_t* xq, int64_t ldq, const float* xs,
+                                     int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
+                                     const int32_t* rows, int64_t R, void* y, int32_t y_dtype, int64_t ldy,
+                                     void* stream);
+const char* bsf8_experts_describe(const bsf8_experts* w, int64_t R);
 
 /*
  * bsf8_linear_w8a8_dynamic -- the W8A8 arm on unquantized activations: x is

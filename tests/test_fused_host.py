@@ -53,6 +53,102 @@ def test_expert_plan_refusals():
     assert call(M=1 << 30, top=2) == "UNSUPPORTED" and call(E=65536) == "UNSUPPORTED"
 
 
+def _weight(rows=(128,), K=256):
+    members = [dict(weight=dict(dtype="F8_E4M3", shape=(r, K), addr=FAKE),
+                    scale_inv=dict(dtype="BF16", shape=(-(-r // 128), -(-K // 128)), addr=FAKE)) for r in rows]
+    arr, keep = B._members_array(members)
+    h = ctypes.c_void_p()
+    assert B.lib().bsf8_weight_create(ctypes.byref(B._decl()), arr, len(rows), ctypes.byref(h)) == 0
+    return h
+
+
+def test_epilogue_refusals():
+    L, h = B.lib(), _weight()
+
+    def call(w=h, xq=FAKE, ldq=256, xs=FAKE, sm=2, sk=1, M=4, y=FAKE, dt=B.DT_BF16, ldy=128, e=True, **kw):
+        ep = B.Epilogue()
+        for k, v in kw.items():
+            setattr(ep, k, v)
+        return name(L.bsf8_linear_w8a8_epilogue(w, xq, ldq, xs, sm, sk, M, ctypes.byref(ep) if e else None, y, dt, ldy, None, 0, None))
+
+    try:
+        assert call(M=0) == "OK"
+        for bad in (dict(w=None), dict(e=False), dict(M=-1), dict(dt=B.DT_F16), dict(xq=None), dict(xs=None), dict(y=None),
+                    dict(ldq=255), dict(ldy=127), dict(sm=1, sk=3), dict(activation=5), dict(activation=-1),
+                    dict(bias=FAKE, bias_dtype=B.DT_F16), dict(residual=FAKE, residual_dtype=B.DT_U8, ldr=128),
+                    dict(residual=FAKE, residual_dtype=B.DT_F32, ldr=127)):
+            assert call(**bad) == "INVALID_ARG", bad
+        for bad in (dict(xs=FAKE + 2), dict(y=FAKE + 1), dict(bias=FAKE + 2, bias_dtype=B.DT_F32),
+                    dict(residual=FAKE + 1, residual_dtype=B.DT_BF16, ldr=128)):
+            assert call(**bad) == "ALIGNMENT", bad
+        assert call(M=1 << 31) == "UNSUPPORTED"
+        b = ctypes.c_size_t()
+        assert L.bsf8_workspace_size(h, B.ARM_W8A8_EPILOGUE, 8, ctypes.byref(b)) == 0
+        assert "arm=w8a8-epilogue" in L.bsf8_describe(h, B.ARM_W8A8_EPILOGUE, 8).decode()
+    finally:
+        L.bsf8_weight_destroy(h)
+
+
+def _experts(members, block=(128, 128), n=None):
+    arr, keep = B._members_array(members)
+    h = ctypes.c_void_p()
+    st = B.lib().bsf8_experts_create(ctypes.byref(B._decl("fp8", block)), arr, len(members) if n is None else n, ctypes.byref(h))
+    return name(st), h
+
+
+def _member(E=3, N=300, K=256, grid=None, wd="F8_E4M3", sd="BF16", leaf="scale_inv", addr=FAKE, shape=None):
+    return {"weight": dict(dtype=wd, shape=shape or (E, N, K), addr=addr),
+            leaf: dict(dtype=sd, shape=grid if grid is not None else (E, -(-N // 128), -(-K // 128)), addr=addr)}
+
+
+def test_experts_create():
+    ok, h = _experts([_member(), _member(N=77)])
+    assert ok == "OK"
+    L = B.lib()
+    e, n, k = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
+    assert L.bsf8_experts_geometry(h, ctypes.byref(e), ctypes.byref(n), ctypes.byref(k)) == 0
+    assert (e.value, n.value, k.value) == (3, 377, 256)
+    assert "E=3 N=377 K=256" in L.bsf8_experts_describe(h, 10).decode()
+    assert name(L.bsf8_experts_geometry(None, None, None, None)) == "INVALID_ARG"
+    L.bsf8_experts_destroy(h)
+    L.bsf8_experts_destroy(None)
+    for want, members, kw in [
+            ("GROUP", [], {}), ("GROUP", [_member()] * 9, {}), ("DECL", [_member()], dict(block=(64, 64))),
+            ("DECL", [_member()], dict(block=(0, 0))), ("WEIGHT_E5M2", [_member(wd="F8_E5M2")], {}),
+            ("WEIGHT_DTYPE", [_member(wd="BF16")], {}), ("WEIGHT_RANK", [_member(shape=(300, 256))], {}),
+            ("WEIGHT_RANK", [_member(shape=(1, 3, 300, 256))], {}), ("WEIGHT_EMPTY", [_member(N=0)], {}),
+            ("WEIGHT_EMPTY", [_member(E=0)], {}), ("SCALE_RANK", [_member(grid=(3, 2))], {}),
+            ("SCALE_RANK", [_member(grid=(3,))], {}), ("SCALE_GRID", [_member(grid=(3, 4, 2))], {}),
+            ("SCALE_GRID", [_member(grid=(2, 3, 2))], {}), ("SCALE_TRANSPOSED", [_member(grid=(3, 2, 3))], {}),
+            ("SCALE_DTYPE", [_member(sd="F16")], {}), ("SCALE_GRID", [_member(leaf="scale")], {}),
+            ("SCALE_MISSING", [dict(weight=_member()["weight"])], {}), ("GROUP", [_member(), _member(E=4)], {}),
+            ("GROUP", [_member(), _member(K=384)], {}), ("GROUP", [_member(), _member(sd="F32")], {}),
+            ("ALIGNMENT", [_member(addr=FAKE + 8)], {}), ("INVALID_ARG", [_member(addr=0)], {}),
+            ("UNSUPPORTED", [_member(E=65536)], {})]:
+        got, h = _experts(members, **kw)
+        assert got == want and not h.value, (want, got)
+
+
+def test_experts_refusals():
+    L = B.lib()
+    ok, h = _experts([_member()])
+    assert ok == "OK"
+
+    def call(w=h, xq=FAKE, ldq=256, xs=FAKE, sm=2, sk=1, M=4, off=FAKE, rows=FAKE, R=8, y=FAKE, dt=B.DT_BF16, ldy=300):
+        return name(L.bsf8_linear_w8a8_experts(w, xq, ldq, xs, sm, sk, M, off, rows, R, y, dt, ldy, None))
+
+    try:
+        assert call(R=0) == "OK"
+        for bad in (dict(w=None), dict(M=-1), dict(R=-1), dict(dt=B.DT_F16), dict(M=0), dict(xq=None), dict(xs=None),
+                    dict(off=None), dict(y=None), dict(rows=None), dict(ldq=255), dict(ldy=299), dict(sm=1, sk=2)):
+            assert call(**bad) == "INVALID_ARG", bad
+        for bad in (dict(off=FAKE + 2), dict(rows=FAKE + 1), dict(y=FAKE + 1), dict(xs=FAKE + 3)):
+            assert call(**bad) == "ALIGNMENT", bad
+        assert call(R=1 << 31) == "UNSUPPORTED"
+    finally:
+        L.bsf8_experts_destroy(h)
+
+
 def test_binding_refuses_host_tensors():
     import torch
     x, w = torch.zeros((4, 256)), torch.ones(256)
