@@ -48,4 +48,47 @@ __device__ __forceinline__ float epilogue(const EpilogueDev& e, float v, int64_t
   return v;
 }
 
+// four outputs of one row, columns that follow each other (nvalid of them
+// exist): bias values b, the residual from element `at` on
+typedef float bsf8_f4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ bsf8_f4 finish4(const EpilogueDev& e, bsf8_f4 v, const float (&b)[4], int64_t at, int nvalid) {
+  float r[4] = {0.f, 0.f, 0.f, 0.f};
+  if (e.res) {
+    if (e.res_bf16) {
+      const uint16_t* p = static_cast<const uint16_t*>(e.res) + at;
+      if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        r[0] = __uint_as_float(u.x << 16);
+        r[1] = __uint_as_float(u.x & 0xFFFF0000u);
+        r[2] = __uint_as_float(u.y << 16);
+        r[3] = __uint_as_float(u.y & 0xFFFF0000u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nvalid) r[i] = __uint_as_float(uint32_t(p[i]) << 16);
+      }
+    } else {
+      const float* p = static_cast<const float*>(e.res) + at;
+      if (nvalid == 4 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        r[0] = u.x;
+        r[1] = u.y;
+        r[2] = u.z;
+        r[3] = u.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (i < nvalid) r[i] = p[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = activate(v[i] + b[i], e.act);
+  if (e.res) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = fmaf(e.alpha, r[i], v[i]);
+  }
+  return v;
+}
+
 }  // namespace bsf8

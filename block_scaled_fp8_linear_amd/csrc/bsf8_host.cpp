@@ -412,7 +412,7 @@ bsf8_status bsf8_workspace_size(const bsf8_weight* w, int32_t arm, int64_t M, si
   else if (arm == BSF8_ARM_W8A8) *bytes = M ? w8a8_workspace_bytes(w->dev, M) : 0;
   else if (arm == BSF8_ARM_DENSE) *bytes = M ? dense_workspace_bytes(w->n_total, w->dev.K, M) : 0;
   else if (arm == BSF8_ARM_W8A8_DYNAMIC) *bytes = M ? dyn_layout(w->dev, M).total : 0;
-  else if (arm == BSF8_ARM_W8A8_EPILOGUE) *bytes = 0;
+  else if (arm == BSF8_ARM_W8A8_EPILOGUE) *bytes = M ? w8a8_epilogue_workspace_bytes(w->dev, M) : 0;
   else return fail(BSF8_E_INVALID_ARG, "arm %d", arm);
   return BSF8_OK;
 }
@@ -577,9 +577,14 @@ bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, i
   ep.bias_bf16 = e->bias_dtype == BSF8_DT_BF16;
   ep.res_bf16 = e->residual_dtype == BSF8_DT_BF16;
   ep.act = e->activation;
+  const size_t need = w8a8_epilogue_workspace_bytes(w->dev, M);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(BSF8_E_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if (workspace != nullptr && reinterpret_cast<uintptr_t>(workspace) % 256)
+    return fail(BSF8_E_ALIGNMENT, "workspace not 256-byte aligned");
   const bool aligned = w->aligned16 && (reinterpret_cast<uintptr_t>(xq) % 16 == 0) && (ldq % 16 == 0);
-  return launch_w8a8_rows(w->dev, aligned, xq, ldq, xs, xs_sm, xs_sk, M, ep, y, y_dtype == BSF8_DT_BF16, ldy,
-                          static_cast<hipStream_t>(stream));
+  return launch_w8a8_epilogue(w->dev, aligned, xq, ldq, xs, xs_sm, xs_sk, M, ep, y, y_dtype == BSF8_DT_BF16, ldy,
+                              workspace, workspace_bytes, static_cast<hipStream_t>(stream));
 }
 
 bsf8_status bsf8_experts_create(const bsf8_decl* decl, const bsf8_member_desc* members, int32_t n_members,

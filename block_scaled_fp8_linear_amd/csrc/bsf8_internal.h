@@ -118,10 +118,21 @@ struct EpilogueDev {
 bsf8_status launch_w8a8_rows(const WeightDev& w, bool aligned, const uint8_t* xq, int64_t ldq, const float* xs,
                              int64_t xs_sm, int64_t xs_sk, int64_t M, const EpilogueDev& ep, void* y, bool y_bf16,
                              int64_t ldy, hipStream_t stream);
+bsf8_status launch_w8a8_expert_rows(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
+                                    const float* xs, int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
+                                    const int32_t* rows, int64_t R, void* y, bool y_bf16, int64_t ldy,
+                                    hipStream_t stream);
+std::string describe_w8a8_rows(bool few, bool aligned);
+
+size_t w8a8_epilogue_workspace_bytes(const WeightDev& w, int64_t M);
+bsf8_status launch_w8a8_epilogue(const WeightDev& w, bool aligned, const uint8_t* xq, int64_t ldq, const float* xs,
+                                 int64_t xs_sm, int64_t xs_sk, int64_t M, const EpilogueDev& ep, void* y, bool y_bf16,
+                                 int64_t ldy, void* ws, size_t ws_bytes, hipStream_t stream);
+std::string describe_w8a8_epilogue(const WeightDev& w, bool aligned, int64_t M);
+
 bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
                                 const float* xs, int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
                                 const int32_t* rows, int64_t R, void* y, bool y_bf16, int64_t ldy, hipStream_t stream);
-std::string describe_w8a8_epilogue(const WeightDev& w, bool aligned, int64_t M);
 std::string describe_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, int64_t R);
 
 // Dense arm: the upcast copy and the BF16 GEMM over it (the fast W8A8 kernel's

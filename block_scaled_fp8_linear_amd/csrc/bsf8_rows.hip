@@ -303,7 +303,7 @@ bsf8_status launch_w8a8_rows(const WeightDev& w, bool aligned, const uint8_t* xq
   return launch_rows(a, aligned, (M + 15) / 16, (M + 63) / 64, M <= 16, stream);
 }
 
-bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
+bsf8_status launch_w8a8_expert_rows(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
                                 const float* xs, int64_t xs_sm, int64_t xs_sk, int64_t M, const int32_t* offsets,
                                 const int32_t* rows, int64_t R, void* y, bool y_bf16, int64_t ldy, hipStream_t stream) {
   RowsArgs a{};
@@ -325,17 +325,10 @@ bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, con
   return launch_rows(a, aligned, used + R / 16, used + R / 64, R <= 16 * E, stream);
 }
 
-std::string describe_w8a8_epilogue(const WeightDev& w, bool aligned, int64_t M) {
+std::string describe_w8a8_rows(bool few, bool aligned) {
   char buf[256];
-  snprintf(buf, sizeof(buf), "arm=w8a8-epilogue arithmetic=e4m3 codes decoded exactly to bf16, mfma_f32_16x16x32_bf16, f32 per-128-K epilogue | "
-           "kernel=w8a8_rows rows<=%d path=%s | M=%lld", M <= 16 ? 16 : 64, aligned ? "aligned16" : "bytewise", (long long)M);
-  return buf;
-}
-
-std::string describe_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, int64_t R) {
-  char buf[256];
-  snprintf(buf, sizeof(buf), "arm=w8a8-experts arithmetic=e4m3 codes decoded exactly to bf16, mfma_f32_16x16x32_bf16, f32 per-128-K epilogue | "
-           "kernel=w8a8_rows rows<=%d path=%s | R=%lld", R <= 16 * E ? 16 : 64, aligned ? "aligned16" : "bytewise", (long long)R);
+  snprintf(buf, sizeof(buf), "arithmetic=e4m3 codes decoded exactly to bf16, mfma_f32_16x16x32_bf16, f32 per-128-K epilogue | "
+           "kernel=w8a8_rows rows<=%d path=%s", few ? 16 : 64, aligned ? "aligned16" : "bytewise");
   return buf;
 }
 

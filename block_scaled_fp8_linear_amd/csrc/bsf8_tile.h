@@ -6,8 +6,10 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <type_traits>
 
+#include "bsf8_epilogue.h"
 #include "bsf8_internal.h"
 
 // buffer_load ... lds: each lane's 16 bytes land at lds + 16 * lane (the LLVM intrinsic).
@@ -184,6 +186,70 @@ struct FastArgs {
   int64_t ldws;
 };
 
+// What an instance of the tile kernel computes.
+enum TileMode {
+  kPlain,      // Y = Xq . W^T
+  kDense,      // BF16 operands without scales
+  kEpilogue,   // kPlain with bias, activation and residual at the store
+  kExperts     // row runs of experts: one weight each, rows gathered by number
+};
+
+struct FusedArgs : FastArgs {
+  EpilogueDev ep;          // kEpilogue
+  const int32_t* offsets;  // kExperts: the runs, [E + 1]
+  const int32_t* rows;     // kExperts: the token of each row, or null
+  int32_t E;
+  int32_t R;               // kExperts: rows of y (M counts the tokens)
+};
+template <int MODE>
+using ArgsOf = std::conditional_t<MODE == kEpilogue || MODE == kExperts, FusedArgs, FastArgs>;
+
+// Experts' runs as the tiles take them.  Each expert's rows are cut into tiles
+// of T; all tiles of all experts, times the weight's row tiles, are the blocks
+// that have work.  The runs lie in device memory, so each wave counts the tiles
+// of 64 experts at a time and sums across its lanes.
+__device__ __forceinline__ int run_tiles(const int32_t* offsets, int E, int R, int T, int e, int& lo, int& hi) {
+  const int i = min(e, E - 1);
+  lo = min(max(offsets[i], 0), R);
+  hi = min(max(offsets[i + 1], lo), R);
+  return e < E ? (hi - lo + T - 1) / T : 0;
+}
+__device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T) {
+  int sum = 0, lo, hi;
+  for (int e = threadIdx.x & 63; e < E; e += 64) sum += run_tiles(offsets, E, R, T, e, lo, hi);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+// The expert that holds tile `tile` (below their sum): its rows [lo, hi), its
+// tiles, and the tiles of the experts before it.
+__device__ __forceinline__ int find_run(const int32_t* offsets, int E, int R, int T, int tile, int& lo, int& hi,
+                                        int& tiles, int& before) {
+  const int lane = threadIdx.x & 63;
+  before = 0;
+  for (int base = 0; base < E; base += 64) {
+    int l, h;
+    const int n = run_tiles(offsets, E, R, T, base + lane, l, h);
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(before + sum > tile);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      lo = __builtin_amdgcn_readlane(l, at);
+      hi = __builtin_amdgcn_readlane(h, at);
+      tiles = __builtin_amdgcn_readlane(n, at);
+      before += __builtin_amdgcn_readlane(sum, at) - tiles;
+      return base + at;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return -1;
+}
+
 __device__ __forceinline__ v4i make_rsrc(const void* p, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
   v4i r;
@@ -256,11 +322,43 @@ __device__ __forceinline__ void store_tile_via_lds(const v4f (&acc)[STI][STJ], u
   }
 }
 
+// The same with an epilogue: the tile goes through LDS as F32, 32 columns at a
+// time, and each lane finishes four outputs of one token row.
+template <int STI, int STJ, bool YBF16>
+__device__ __forceinline__ void store_tile_epilogue(const v4f (&acc)[STI][STJ], uint8_t* buf, const FusedArgs& a,
+                                                    int64_t col0, int n_base, int n_end, int m_base, int M, int lane) {
+  const int l16 = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int i0 = 0; i0 < STI; i0 += 2) {
+#pragma unroll
+    for (int j = 0; j < STJ; ++j)
+#pragma unroll
+      for (int ii = 0; ii < 2; ++ii)
+        *reinterpret_cast<v4f*>(buf + (16 * j + l16) * F_OUT_PITCH + (ii * 16 + 4 * g) * 4) = acc[i0 + ii][j];
+    const int n = n_base + i0 * 16 + (lane & 7) * 4;
+    const int nvalid = min(4, n_end - n);
+    if (nvalid <= 0) continue;
+    float b[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.ep.bias) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < nvalid) b[e] = load_real(a.ep.bias, a.ep.bias_bf16, col0 + n + e);
+    }
+#pragma unroll 2
+    for (int t = 0; t < 2 * STJ; ++t) {
+      const int row = 8 * t + (lane >> 3), m = m_base + row;
+      if (m >= M) continue;
+      const v4f v = *reinterpret_cast<const v4f*>(buf + row * F_OUT_PITCH + (lane & 7) * 16);
+      store4(a.y, YBF16, int64_t(m) * a.ldy + col0 + n, nvalid,
+             finish4(a.ep, v, b, int64_t(m) * a.ep.ldr + col0 + n, nvalid));
+    }
+  }
+}
+
 // Dense arm: two BF16 MFMAs per 32-byte fragment pair.  A fragment holds 16
 // BF16 values of one row (chunks 2g and 2g + 1 of its 128-byte K block); the
 // first MFMA takes chunk 2g as its K group g and the second chunk 2g + 1, on
 // both operands alike, so the pair sums every K element of the block once.
-typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ void mfma_bf16_pair(v4f& c, const v8i& a, const v8i& b) {
   const v8bf a0 = __builtin_bit_cast(v8bf, __builtin_shufflevector(a, a, 0, 1, 2, 3));
   const v8bf a1 = __builtin_bit_cast(v8bf, __builtin_shufflevector(a, a, 4, 5, 6, 7));
@@ -270,12 +368,26 @@ __device__ __forceinline__ void mfma_bf16_pair(v4f& c, const v8i& a, const v8i& 
   c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, b1, c, 0, 0, 0);
 }
 
+// A fragment's 32 codes decoded to BF16, as four MFMA steps' operands.
+struct Decoded {
+  v8bf s[4];
+};
+__device__ __forceinline__ Decoded decode32(const v8i& f) {
+  return Decoded{{decode8(uint32_t(f[0]), uint32_t(f[1])), decode8(uint32_t(f[2]), uint32_t(f[3])),
+                  decode8(uint32_t(f[4]), uint32_t(f[5])), decode8(uint32_t(f[6]), uint32_t(f[7]))}};
+}
+
 // KFULL: K is a multiple of 128 bytes, so no copy needs the ragged-K test.
 // DENSE: BF16 operands without scales (the upcast weight of the resident=False
 // arm times BF16 activations): w.K counts bytes (2 per element), the MFMAs
 // accumulate in place, and there are no scales to stage or apply.
-template <int T, bool SBF16, bool KFULL, bool DENSE>
-__global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
+// EXACT: the codes of a fragment are decoded to BF16 and summed by BF16 MFMAs in
+// full F32, for F32 outputs: the FP8 MFMA's sum over a block is narrower than F32
+// (5e-5 of the result's norm on random codes, a hundredth of a BF16 output's
+// rounding but six hundred times an F32 output's).
+template <int T, bool SBF16, bool KFULL, int MODE, bool EXACT = false>
+__global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(ArgsOf<MODE> a) {
+  constexpr bool DENSE = MODE == kDense, EXPERTS = MODE == kExperts;
   using C = FTile<T>;
   constexpr int FBN = C::BN, FBM = C::BM, F_SA = C::SA, F_STAGE = C::STAGE;
   constexpr int F_A_LOADS = C::A_LOADS, F_B_LOADS = C::B_LOADS;
@@ -295,37 +407,59 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
   // tiles in groups of group_rows row tiles x all token tiles, so blocks that
   // run together share operands in that XCD's L2.  Split work walks
   // (split, row tile) pairs split-major: a group shares one K range.
-  const int nblk = gridDim.x;
   const int b = blockIdx.x;
   const int xcd = b % XCDS;
   const int l = b / XCDS;
-  const int split_rows = a.rt_total - a.rt_split0;
-  const int n_whole = a.rt_split0 * a.m_tiles;
-  int start_whole = 0, start_split = 0;
-  for (int y = 0; y < xcd; ++y) {
-    const int ny = (nblk - y + XCDS - 1) / XCDS, nwy = (n_whole - y + XCDS - 1) / XCDS;
-    start_whole += nwy;
-    start_split += ny - nwy;
+  int R, m0, m_end = a.M, split = 0, expert = 0;
+  bool whole = true;
+  if constexpr (EXPERTS) {
+    // Experts: the same dealing over the blocks that have work.  An expert's
+    // tiles of one weight row tile follow each other, so the weight is read from
+    // memory once and the expert's rows stay in the L2.
+    const int n_blocks = all_run_tiles(a.offsets, a.E, a.R, FBM) * a.rt_total;
+    int v = l;
+    for (int y = 0; y < xcd; ++y) v += (n_blocks - y + XCDS - 1) / XCDS;
+    if (b >= n_blocks) return;
+    int lo, hi, tiles, before;
+    expert = find_run(a.offsets, a.E, a.R, FBM, v / a.rt_total, lo, hi, tiles, before);
+    const int u = v - before * a.rt_total;
+    R = u / tiles;
+    m0 = lo + (u - R * tiles) * FBM;
+    m_end = hi;
+  } else {
+    const int nblk = gridDim.x;
+    const int split_rows = a.rt_total - a.rt_split0;
+    const int n_whole = a.rt_split0 * a.m_tiles;
+    int start_whole = 0, start_split = 0;
+    for (int y = 0; y < xcd; ++y) {
+      const int ny = (nblk - y + XCDS - 1) / XCDS, nwy = (n_whole - y + XCDS - 1) / XCDS;
+      start_whole += nwy;
+      start_split += ny - nwy;
+    }
+    const int n_whole_here = (n_whole - xcd + XCDS - 1) / XCDS;
+    whole = l < n_whole_here;
+    const int v = whole ? start_whole + l : start_split + (l - n_whole_here);
+    const int vr_total = whole ? a.rt_split0 : split_rows * a.splits;
+    const int GROUP_ROWS = a.group_rows;
+    const int gsz = GROUP_ROWS * a.m_tiles;
+    const int grp = v / gsz;
+    const int in_grp = v - grp * gsz;
+    const int g_rows = min(GROUP_ROWS, vr_total - grp * GROUP_ROWS);
+    const int VR = grp * GROUP_ROWS + in_grp % g_rows;
+    const int mt = in_grp / g_rows;
+    split = whole ? 0 : VR / split_rows;
+    R = whole ? VR : a.rt_split0 + (VR - split * split_rows);
+    m0 = mt * FBM;
   }
-  const int n_whole_here = (n_whole - xcd + XCDS - 1) / XCDS;
-  const bool whole = l < n_whole_here;
-  const int v = whole ? start_whole + l : start_split + (l - n_whole_here);
-  const int vr_total = whole ? a.rt_split0 : split_rows * a.splits;
-  const int GROUP_ROWS = a.group_rows;
-  const int gsz = GROUP_ROWS * a.m_tiles;
-  const int grp = v / gsz;
-  const int in_grp = v - grp * gsz;
-  const int g_rows = min(GROUP_ROWS, vr_total - grp * GROUP_ROWS);
-  const int VR = grp * GROUP_ROWS + in_grp % g_rows;
-  const int mt = in_grp / g_rows;
-  const int split = whole ? 0 : VR / split_rows;
-  const int R = whole ? VR : a.rt_split0 + (VR - split * split_rows);
   int mi = 0;
   while (mi + 1 < a.w.n_members && R >= a.rt0[mi + 1]) ++mi;
-  const MemberDev mem = a.w.m[mi];
+  MemberDev mem = a.w.m[mi];
   const int n0 = (R - a.rt0[mi]) * FBN;
-  const int m0 = mt * FBM;
   const int K = a.w.K, Kb = a.w.Kb, M = a.M;
+  if constexpr (EXPERTS) {
+    mem.w += int64_t(expert) * mem.rows * K;
+    mem.s = static_cast<const uint8_t*>(mem.s) + int64_t(expert) * ((mem.rows + 127) >> 7) * Kb * (SBF16 ? 2 : 4);
+  }
   const int kb_begin = whole ? 0 : split * a.kb_per_split;
   const int kb_end = whole ? Kb : min(Kb, kb_begin + a.kb_per_split);
 
@@ -350,8 +484,8 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
   // 256 contiguous bytes; token-major, 64 words a row pitch apart.
   const bool s_wave = wave < FBM / 64;
   const int s_tok = m0 + wave * 64 + 16 * (lane & 3) + (lane >> 2);
-  const bool s_ok = s_wave && s_tok < M;
-  const int s_off = s_ok ? s_tok * int(a.xs_sm) * 4 : 0;
+  bool s_ok = s_wave && s_tok < m_end;
+  int s_off = s_ok ? s_tok * int(a.xs_sm) * 4 : 0;
   const int s_kstep = int(a.xs_sk) * 4;
   // Lane L of a 1 KiB wave copy fills chunk position L & 7 of row L >> 3 of its
   // 8-row slab; since the swizzle depends on r & 7 only, the logical chunk it
@@ -370,6 +504,27 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
   // compiler from holding every copy's offset in its own vector register.
   const uint32_t a_lane = uint32_t(a_row0) * uint32_t(K);
   const uint32_t b_lane = uint32_t(b_row0) * uint32_t(a.ldq);
+  // Experts: a row's token is looked up once; the rows of a copying lane's slabs
+  // keep their byte offsets.  A row past the run or without a token reads zeros.
+  uint32_t b_row_off[EXPERTS ? F_B_LOADS : 1];
+  if constexpr (EXPERTS) {
+    auto token = [&](int r) {
+      const int tok = r < m_end ? (a.rows ? a.rows[r] : r) : -1;
+      return tok < M ? tok : -1;
+    };
+    if (copier) {
+#pragma unroll
+      for (int i = 0; i < F_B_LOADS; ++i) {
+        const int tok = token(b_row0 + 8 * i);
+        b_row_off[i] = tok >= 0 ? uint32_t(tok) * uint32_t(a.ldq) : b_bytes;
+      }
+    }
+    if (s_wave) {
+      const int tok = token(s_tok);
+      s_ok = tok >= 0;
+      s_off = s_ok ? tok * int(a.xs_sm) * 4 : 0;
+    }
+  }
   auto issue_one = [&](int kb, uint8_t* base, int c) {
     const uint32_t kbo = uint32_t(kb) * KBYTES;
     if (c < F_A_LOADS) {
@@ -382,7 +537,11 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
       const int i = c - F_A_LOADS;
       const uint32_t ch = ch_lane;
       const uint32_t sc = uint32_t(__builtin_amdgcn_readfirstlane(int(uint32_t(8 * i) * uint32_t(a.ldq) + kbo)));
-      const uint32_t off = KFULL || kbo + ch < uint32_t(K) ? b_lane + ch + sc : b_bytes;
+      uint32_t off;
+      if constexpr (EXPERTS)
+        off = KFULL || kbo + ch < uint32_t(K) ? b_row_off[i] + ch + kbo : b_bytes;
+      else
+        off = KFULL || kbo + ch < uint32_t(K) ? b_lane + ch + sc : b_bytes;
       bsf8_raw_buffer_load_lds(rb, (lds_u32_ptr)(base + FBN * KBYTES + (cw * F_B_LOADS + i) * 1024), 16, int(off), 0,
                                0, 0);
     }
@@ -498,6 +657,13 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
     // while tile i's MFMAs run.
     constexpr int LAG = 2;
     v4f part[LAG + 1];
+    // EXACT: the block's column operands decoded at once, a row tile's when its
+    // chain begins
+    Decoded bd[EXACT ? TJ : 1], ad;
+    if constexpr (EXACT) {
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) bd[j] = decode32(bf[j]);
+    }
 #pragma unroll
     for (int q = 0; q < TI * TJ + LAG; ++q) {
       if (q < TI * TJ) {
@@ -510,9 +676,15 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
           af[0] = read_a(nxt, 0);
         }
         if (j == 0 && i + 1 < TI) af[(i + 1) & 1] = read_a(cur, i + 1);
-        if constexpr (DENSE)
+        if constexpr (DENSE) {
           mfma_bf16_pair(acc[i][j], af[i & 1], bf[j]);
-        else
+        } else if constexpr (EXACT) {
+          if (j == 0) ad = decode32(af[i & 1]);
+          v4f c = v4f{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int u = 0; u < 4; ++u) c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ad.s[u], bd[j].s[u], c, 0, 0, 0);
+          part[q % (LAG + 1)] = c;
+        } else
           part[q % (LAG + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(af[i & 1], bf[j],
                                                                                v4f{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
         if (q >= BARQ) bf[j] = read_b(nxt, j);   // its last use in this block was the MFMA above
@@ -577,27 +749,42 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(FastArgs a) {
       if (!whole)
         store_tile_via_lds<TI, TJ, false>(acc, buf, a.ws + int64_t(split) * M * a.ldws, a.ldws,
                                   int64_t(R - a.rt_split0) * FBN - n0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
-      else if (a.y_bf16 && a.y_nt)
-        store_tile_via_lds<TI, TJ, true, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
+      else if constexpr (MODE == kEpilogue) {
+        if (a.y_bf16)
+          store_tile_epilogue<TI, TJ, true>(acc, buf, a, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
+        else
+          store_tile_epilogue<TI, TJ, false>(acc, buf, a, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
+      } else if (a.y_bf16 && a.y_nt)
+        store_tile_via_lds<TI, TJ, true, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       else if (a.y_bf16)
-        store_tile_via_lds<TI, TJ, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
+        store_tile_via_lds<TI, TJ, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       else if (a.y_nt)
-        store_tile_via_lds<TI, TJ, false, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
+        store_tile_via_lds<TI, TJ, false, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       else
-        store_tile_via_lds<TI, TJ, false>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
+        store_tile_via_lds<TI, TJ, false>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       return;
     }
     // unaligned output: lane holds rows 4*(lane/16)+r of each 16x16 tile, column lane%16
   #pragma unroll
     for (int j = 0; j < TJ; ++j) {
       const int m = m0 + wm * WM + 16 * j + l16;
-      if (m >= M) continue;
+      if (m >= m_end) continue;
   #pragma unroll
       for (int i = 0; i < TI; ++i) {
         const int n = n0 + wn * WN + 16 * i + 4 * g;
         const int nvalid = mem.rows - n;
         if (nvalid <= 0) continue;
-        store4(a.y, a.y_bf16, int64_t(m) * a.ldy + mem.col0 + n, nvalid, acc[i][j]);
+        v4f v = acc[i][j];
+        if constexpr (MODE == kEpilogue) {
+          float bias[4] = {0.f, 0.f, 0.f, 0.f};
+          if (a.ep.bias) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (e < nvalid) bias[e] = load_real(a.ep.bias, a.ep.bias_bf16, mem.col0 + n + e);
+          }
+          v = finish4(a.ep, v, bias, int64_t(m) * a.ep.ldr + mem.col0 + n, min(4, nvalid));
+        }
+        store4(a.y, a.y_bf16, int64_t(m) * a.ldy + mem.col0 + n, nvalid, v);
       }
     }
   };
@@ -625,7 +812,12 @@ struct ReduceArgs {
   int32_t col0[kMaxMembers];
 };
 
-__global__ __launch_bounds__(256) void splitk_reduce_kernel(ReduceArgs a) {
+struct FusedReduceArgs : ReduceArgs {
+  EpilogueDev ep;
+};
+
+template <bool EPILOGUE>
+__global__ __launch_bounds__(256) void splitk_reduce_kernel(std::conditional_t<EPILOGUE, FusedReduceArgs, ReduceArgs> a) {
   const int64_t c4_per_row = a.ldws / 4;
   const int64_t idx = int64_t(blockIdx.x) * 256 + threadIdx.x;
   if (idx >= int64_t(a.M) * c4_per_row) return;
@@ -646,7 +838,18 @@ __global__ __launch_bounds__(256) void splitk_reduce_kernel(ReduceArgs a) {
     t.z += u.z;
     t.w += u.w;
   }
-  store4(a.y, a.y_bf16, int64_t(m) * a.ldy + a.col0[i] + n, nvalid, v4f{t.x, t.y, t.z, t.w});
+  v4f v = v4f{t.x, t.y, t.z, t.w};
+  if constexpr (EPILOGUE) {
+    const int64_t col = a.col0[i] + n;
+    float bias[4] = {0.f, 0.f, 0.f, 0.f};
+    if (a.ep.bias) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < nvalid) bias[e] = load_real(a.ep.bias, a.ep.bias_bf16, col + e);
+    }
+    v = finish4(a.ep, v, bias, int64_t(m) * a.ep.ldr + col, min(4, nvalid));
+  }
+  store4(a.y, a.y_bf16, int64_t(m) * a.ldy + a.col0[i] + n, nvalid, v);
 }
 
 struct Plan {
@@ -722,7 +925,8 @@ SplitChoice choose_splits(int rt_total, int m_tiles, int Kb, int cus, double ste
 // its base, so every member, the activation block and its scales must stay
 // below 2^31 bytes.
 // (xs_extent: elements spanned by the activation scales; -1: M x Kb.)
-Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t xs_extent = -1) {
+// (exact: the EXACT instances, which exist for 128 x 128 tiles.)
+Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t xs_extent = -1, bool exact = false) {
   Plan p{};
   if (xs_extent < 0) xs_extent = M * w.Kb;
   bool fits = M * ldq < (int64_t(1) << 31) && xs_extent * 4 < (int64_t(1) << 31);
@@ -731,13 +935,15 @@ Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t
   if (p.fast) {
     // the tile (256 or 128) with the lower modelled cost, 256 on a tie
     SplitChoice sc{};
+    p.tile = 0;
     for (const int T : {256, 128}) {
+      if (exact && T == 256) continue;
       const int m_tiles = int((M + T - 1) / T);
       int r = 0;
       for (int i = 0; i < w.n_members; ++i) r += (w.m[i].rows + T - 1) / T;
       const SplitChoice c = T == 256 ? choose_splits(r, m_tiles, w.Kb, device_cus(), 1.0, 0.06)
                                      : choose_splits(r, m_tiles, w.Kb, device_cus(), 0.555, 0.015);
-      if (T == 256 || c.cost < sc.cost - 1e-9) {
+      if (p.tile == 0 || c.cost < sc.cost - 1e-9) {
         sc = c;
         p.tile = T;
       }
@@ -775,10 +981,22 @@ Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t
 
 
 // Fast-kernel launch (and the split-K reduction when the plan splits).
-bsf8_status launch_fast(const Plan& p, const WeightDev& w, bool dense, const uint8_t* xq, int64_t ldq,
-                        const float* xs, int64_t xs_sm, int64_t xs_sk, int64_t M, void* y, bool y_bf16, int64_t ldy,
-                        void* ws, size_t ws_bytes, hipStream_t stream) {
-  FastArgs a{};
+template <int MODE, bool EXACT>
+auto tile_kernel(int tile, bool scale_bf16, bool kfull) -> void (*)(ArgsOf<MODE>) {
+#define BSF8_TILE(T)                                                                                              \
+  (scale_bf16 ? (kfull ? w8a8_gemm_fast_kernel<T, true, true, MODE, EXACT> : w8a8_gemm_fast_kernel<T, true, false, MODE, EXACT>) \
+              : (kfull ? w8a8_gemm_fast_kernel<T, false, true, MODE, EXACT> : w8a8_gemm_fast_kernel<T, false, false, MODE, EXACT>))
+  if constexpr (EXACT) return BSF8_TILE(128);
+  else return tile == 256 ? BSF8_TILE(256) : BSF8_TILE(128);
+#undef BSF8_TILE
+}
+
+// (ep: kEpilogue; EXACT goes by the plan's `exact`.)
+template <int MODE, bool EXACT = false>
+bsf8_status launch_fast(const Plan& p, const WeightDev& w, const uint8_t* xq, int64_t ldq, const float* xs,
+                        int64_t xs_sm, int64_t xs_sk, int64_t M, void* y, bool y_bf16, int64_t ldy, void* ws,
+                        size_t ws_bytes, hipStream_t stream, const EpilogueDev* ep = nullptr) {
+  ArgsOf<MODE> a{};
   a.w = w;
   for (int i = 0; i <= kMaxMembers; ++i) a.rt0[i] = p.rt0[i];
   a.xq = xq;
@@ -809,19 +1027,19 @@ bsf8_status launch_fast(const Plan& p, const WeightDev& w, bool dense, const uin
     }
     a.ws = static_cast<float*>(ws);
   }
+  if constexpr (MODE == kEpilogue) a.ep = *ep;
   const bool kfull = w.K % KBYTES == 0;
-  using Kern = void (*)(FastArgs);
-  Kern kern;
-#define BSF8_FAST(T)                                                                                          \
-  (dense ? (kfull ? w8a8_gemm_fast_kernel<T, false, true, true> : w8a8_gemm_fast_kernel<T, false, false, true>) \
-   : w.scale_bf16 ? (kfull ? w8a8_gemm_fast_kernel<T, true, true, false> : w8a8_gemm_fast_kernel<T, true, false, false>) \
-                  : (kfull ? w8a8_gemm_fast_kernel<T, false, true, false> : w8a8_gemm_fast_kernel<T, false, false, false>))
-  kern = p.tile == 256 ? BSF8_FAST(256) : BSF8_FAST(128);
-#undef BSF8_FAST
+  void (*kern)(ArgsOf<MODE>);
+  if constexpr (MODE == kDense)   // (no scales: one type serves)
+    kern = p.tile == 256 ? (kfull ? w8a8_gemm_fast_kernel<256, false, true, MODE> : w8a8_gemm_fast_kernel<256, false, false, MODE>)
+                         : (kfull ? w8a8_gemm_fast_kernel<128, false, true, MODE> : w8a8_gemm_fast_kernel<128, false, false, MODE>);
+  else
+    kern = tile_kernel<MODE, EXACT>(p.tile, w.scale_bf16 != 0, kfull);
   hipLaunchKernelGGL(kern, dim3(p.blocks), dim3(FTHREADS), 0, stream, a);
-  bsf8_status st = device_status(hipGetLastError(), dense ? "dense_gemm launch" : "w8a8_gemm_fast launch");
+  bsf8_status st = device_status(hipGetLastError(), MODE == kDense ? "dense_gemm launch" : "w8a8_gemm_fast launch");
   if (st != BSF8_OK || p.splits == 1) return st;
-  ReduceArgs r{};
+  std::conditional_t<MODE == kEpilogue, FusedReduceArgs, ReduceArgs> r{};
+  if constexpr (MODE == kEpilogue) r.ep = *ep;
   r.ws = a.ws;
   r.ldws = p.ldws;
   r.split_stride = M * p.ldws;
@@ -839,7 +1057,7 @@ bsf8_status launch_fast(const Plan& p, const WeightDev& w, bool dense, const uin
     r.col0[i] = w.m[i].col0;
   }
   const int64_t threads = M * (p.ldws / 4);
-  hipLaunchKernelGGL(splitk_reduce_kernel, dim3(unsigned((threads + 255) / 256)), dim3(256), 0, stream, r);
+  hipLaunchKernelGGL(splitk_reduce_kernel<MODE == kEpilogue>, dim3(unsigned((threads + 255) / 256)), dim3(256), 0, stream, r);
   return device_status(hipGetLastError(), "splitk_reduce launch");
 }
 }  // namespace

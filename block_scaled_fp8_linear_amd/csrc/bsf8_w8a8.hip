@@ -287,7 +287,7 @@ bsf8_status launch_dense(const uint16_t* wd, int64_t N, int64_t K, const uint16_
     return BSF8_E_UNSUPPORTED;
   }
   if (p.blocks == 0) return BSF8_OK;
-  return launch_fast(p, w, true, reinterpret_cast<const uint8_t*>(x), 2 * ldx, nullptr, 0, 0, M, y, y_bf16, ldy,
+  return launch_fast<kDense>(p, w, reinterpret_cast<const uint8_t*>(x), 2 * ldx, nullptr, 0, 0, M, y, y_bf16, ldy,
                      ws, ws_bytes, stream);
 }
 
@@ -342,7 +342,7 @@ bsf8_status launch_w8a8(const WeightDev& w, bool aligned, const uint8_t* xq, int
     return launch_w8a8_stream(w, xq, ldq, xs, xs_sm, xs_sk, M, y, y_bf16, ldy, stream);
   const Plan p = make_plan(w, aligned, M, ldq, (M - 1) * xs_sm + (w.Kb - 1) * xs_sk + 1);
   if (p.blocks == 0) return BSF8_OK;
-  if (p.fast) return launch_fast(p, w, false, xq, ldq, xs, xs_sm, xs_sk, M, y, y_bf16, ldy, ws, ws_bytes, stream);
+  if (p.fast) return launch_fast<kPlain>(p, w, xq, ldq, xs, xs_sm, xs_sk, M, y, y_bf16, ldy, ws, ws_bytes, stream);
   GemmArgs a{};
   a.w = w;
   a.tm = p.tm;
