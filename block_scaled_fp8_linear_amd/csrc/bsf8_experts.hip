@@ -1,6 +1,7 @@
 // The experts' products (gfx950): which kernel takes a call, and the tile GEMM's
 // instances for ragged row runs.
 #include <cstdio>
+#include <cstdlib>
 #include <string>
 
 #include "bsf8_tile.h"
@@ -14,10 +15,10 @@ bool by_rows(const WeightDev& w, int64_t E, bool aligned, int64_t R, int64_t M, 
   // the tile kernel's 32-bit offsets: one expert's member, the tokens' codes and scales
   bool fits = M * ldq < (int64_t(1) << 31) && xs_extent * 4 < (int64_t(1) << 31) && w.Kb <= F_MAX_KB;
   for (int i = 0; i < w.n_members; ++i) fits = fits && int64_t(w.m[i].rows) * w.K < (int64_t(1) << 31);
-  return !aligned || !fits || R <= 16 * E;
+  return !aligned || !fits || R <= (getenv("XR") ? atoi(getenv("XR")) : 16) * E;
 }
 
-int tile_of(int64_t E, int64_t R, bool y_bf16) { return y_bf16 && R >= 256 * E ? 256 : 128; }
+int tile_of(int64_t E, int64_t R, bool y_bf16) { if (getenv("XT")) return y_bf16 ? atoi(getenv("XT")) : 128; return y_bf16 && R >= 256 * E ? 256 : 128; }
 
 }  // namespace
 

@@ -325,8 +325,9 @@ __device__ __forceinline__ void store_tile_via_lds(const v4f (&acc)[STI][STJ], u
 // The same with an epilogue: the tile goes through LDS as F32, 32 columns at a
 // time, and each lane finishes four outputs of one token row.
 template <int STI, int STJ, bool YBF16>
-__device__ __forceinline__ void store_tile_epilogue(const v4f (&acc)[STI][STJ], uint8_t* buf, const FusedArgs& a,
-                                                    int64_t col0, int n_base, int n_end, int m_base, int M, int lane) {
+__device__ __forceinline__ void store_tile_epilogue(const v4f (&acc)[STI][STJ], uint8_t* buf, const EpilogueDev& ep,
+                                                    void* y, int64_t ldy, int64_t col0, int n_base, int n_end,
+                                                    int m_base, int M, int lane) {
   const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int i0 = 0; i0 < STI; i0 += 2) {
@@ -339,18 +340,18 @@ __device__ __forceinline__ void store_tile_epilogue(const v4f (&acc)[STI][STJ], 
     const int nvalid = min(4, n_end - n);
     if (nvalid <= 0) continue;
     float b[4] = {0.f, 0.f, 0.f, 0.f};
-    if (a.ep.bias) {
+    if (ep.bias) {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (e < nvalid) b[e] = load_real(a.ep.bias, a.ep.bias_bf16, col0 + n + e);
+        if (e < nvalid) b[e] = load_real(ep.bias, ep.bias_bf16, col0 + n + e);
     }
-#pragma unroll 2
+#pragma unroll 1
     for (int t = 0; t < 2 * STJ; ++t) {
       const int row = 8 * t + (lane >> 3), m = m_base + row;
       if (m >= M) continue;
       const v4f v = *reinterpret_cast<const v4f*>(buf + row * F_OUT_PITCH + (lane & 7) * 16);
-      store4(a.y, YBF16, int64_t(m) * a.ldy + col0 + n, nvalid,
-             finish4(a.ep, v, b, int64_t(m) * a.ep.ldr + col0 + n, nvalid));
+      store4(y, YBF16, int64_t(m) * ldy + col0 + n, nvalid,
+             finish4(ep, v, b, int64_t(m) * ep.ldr + col0 + n, nvalid));
     }
   }
 }
@@ -741,7 +742,7 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(ArgsOf<MODE> a
     }
 
     // ---- store
-    if (!whole || a.y_vec) {
+    if (MODE == kEpilogue || !whole || a.y_vec) {   // (an epilogue's stores test their own alignment)
       // every wave is done reading both stages
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();
@@ -751,9 +752,9 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(ArgsOf<MODE> a
                                   int64_t(R - a.rt_split0) * FBN - n0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
       else if constexpr (MODE == kEpilogue) {
         if (a.y_bf16)
-          store_tile_epilogue<TI, TJ, true>(acc, buf, a, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
+          store_tile_epilogue<TI, TJ, true>(acc, buf, a.ep, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
         else
-          store_tile_epilogue<TI, TJ, false>(acc, buf, a, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
+          store_tile_epilogue<TI, TJ, false>(acc, buf, a.ep, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       } else if (a.y_bf16 && a.y_nt)
         store_tile_via_lds<TI, TJ, true, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       else if (a.y_bf16)
@@ -774,17 +775,7 @@ __global__ __launch_bounds__(FTHREADS) void w8a8_gemm_fast_kernel(ArgsOf<MODE> a
         const int n = n0 + wn * WN + 16 * i + 4 * g;
         const int nvalid = mem.rows - n;
         if (nvalid <= 0) continue;
-        v4f v = acc[i][j];
-        if constexpr (MODE == kEpilogue) {
-          float bias[4] = {0.f, 0.f, 0.f, 0.f};
-          if (a.ep.bias) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (e < nvalid) bias[e] = load_real(a.ep.bias, a.ep.bias_bf16, mem.col0 + n + e);
-          }
-          v = finish4(a.ep, v, bias, int64_t(m) * a.ep.ldr + mem.col0 + n, min(4, nvalid));
-        }
-        store4(a.y, a.y_bf16, int64_t(m) * a.ldy + mem.col0 + n, nvalid, v);
+        store4(a.y, a.y_bf16, int64_t(m) * a.ldy + mem.col0 + n, nvalid, acc[i][j]);
       }
     }
   };
