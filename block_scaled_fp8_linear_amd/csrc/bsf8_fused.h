@@ -1,6 +1,6 @@
 // Device code that the products with an epilogue and by expert share: the
-// epilogue, y = act(v + bias) + residual_scale * residual in F32, and the exact
-// decoding of codes.  Not part of the ABI.
+// epilogue, y = act(v + bias) + residual_scale * residual in F32, the exact
+// decoding of codes, and the experts' row runs.  Not part of the ABI.
 #pragma once
 
 #include "bsf8_internal.h"
@@ -35,17 +35,16 @@ __device__ __forceinline__ float activate(float v, int act) {
   }
 }
 
+// element i of a BF16 or F32 array as raw bits, and their value
+__device__ __forceinline__ uint32_t load_bits(const void* p, int bf16, int64_t i) {
+  if (bf16) return static_cast<const uint16_t*>(p)[i];
+  return static_cast<const uint32_t*>(p)[i];
+}
+__device__ __forceinline__ float widen(uint32_t bits, int bf16) { return __uint_as_float(bf16 ? bits << 16 : bits); }
+
 __device__ __forceinline__ float load_real(const void* p, int bf16, int64_t i) {
   if (bf16) return __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16);
   return static_cast<const float*>(p)[i];
-}
-
-// one output: row r, column n of y
-__device__ __forceinline__ float epilogue(const EpilogueDev& e, float v, int64_t r, int64_t n) {
-  if (e.bias) v += load_real(e.bias, e.bias_bf16, n);
-  v = activate(v, e.act);
-  if (e.res) v = fmaf(e.alpha, load_real(e.res, e.res_bf16, r * e.ldr + n), v);
-  return v;
 }
 
 // four outputs of one row, columns that follow each other (nvalid of them
@@ -89,6 +88,53 @@ __device__ __forceinline__ bsf8_f4 finish4(const EpilogueDev& e, bsf8_f4 v, cons
     for (int i = 0; i < 4; ++i) v[i] = fmaf(e.alpha, r[i], v[i]);
   }
   return v;
+}
+
+// Experts' row runs as the kernels take them.  Each expert's rows are cut into
+// tiles of T; all tiles of all experts, times the weight's row tiles, are the
+// blocks that have work.  The runs lie in device memory, so each wave counts the
+// tiles of 64 experts at a time and sums across its lanes.  Offsets are clamped
+// to [0, R], so nothing in device memory can lead an access out of bounds.
+__device__ __forceinline__ int run_tiles(const int32_t* offsets, int E, int R, int T, int e, int& lo, int& hi) {
+  const int i = min(e, E - 1);
+  lo = min(max(offsets[i], 0), R);
+  hi = min(max(offsets[i + 1], lo), R);
+  return e < E ? (hi - lo + T - 1) / T : 0;
+}
+__device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T) {
+  int sum = 0, lo, hi;
+  for (int e = threadIdx.x & 63; e < E; e += 64) sum += run_tiles(offsets, E, R, T, e, lo, hi);
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+// The expert that holds tile `tile`, -1 past the last: its rows [lo, hi), its
+// tiles, and the tiles of the experts before it.
+__device__ __forceinline__ int find_run(const int32_t* offsets, int E, int R, int T, int tile, int& lo, int& hi,
+                                        int& tiles, int& before) {
+  const int lane = threadIdx.x & 63;
+  before = 0;
+  for (int base = 0; base < E; base += 64) {
+    int l, h;
+    const int n = run_tiles(offsets, E, R, T, base + lane, l, h);
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d, 64);
+      if (lane >= d) sum += up;
+    }
+    const uint64_t past = __ballot(before + sum > tile);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      lo = __builtin_amdgcn_readlane(l, at);
+      hi = __builtin_amdgcn_readlane(h, at);
+      tiles = __builtin_amdgcn_readlane(n, at);
+      before += __builtin_amdgcn_readlane(sum, at) - tiles;
+      return base + at;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return -1;
 }
 
 }  // namespace bsf8

@@ -30,10 +30,11 @@
 // as zeros, so nothing in device memory can lead an access out of bounds.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cstdio>
 #include <string>
 
-#include "bsf8_epilogue.h"
+#include "bsf8_fused.h"
 
 namespace bsf8 {
 namespace {
@@ -41,9 +42,28 @@ namespace {
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 
-constexpr int WAVES = 8;
-constexpr int THREADS = WAVES * 64;
 constexpr int KB = 128;
+#ifndef RNT
+#define RNT true
+#endif
+#ifndef RD1
+#define RD1 1
+#endif
+#ifndef RD2
+#define RD2 1
+#endif
+#ifndef RFEW
+#define RFEW 16
+#endif
+#ifndef RKB4
+#define RKB4 16
+#endif
+#ifndef RTJ
+#define RTJ 4
+#endif
+#ifndef RRT
+#define RRT 2
+#endif
 
 struct RowsArgs {
   WeightDev w;                      // expert 0's members
@@ -60,36 +80,6 @@ struct RowsArgs {
   int32_t E;
   int32_t y_bf16;
 };
-
-// Run number `item` of the experts' runs of T rows: the expert and its rows
-// [first, end); false past the last run.  All lanes of a wave agree.
-__device__ __forceinline__ bool find_run(const int32_t* offsets, int E, int R, int T, int item, int& expert, int& first,
-                                         int& end) {
-  const int lane = threadIdx.x & 63;
-  for (int base = 0; base < E; base += 64) {
-    const int e = min(base + lane, E - 1);
-    const int lo = min(max(offsets[e], 0), R), hi = min(max(offsets[e + 1], lo), R);
-    const int runs = base + lane < E ? (hi - lo + T - 1) / T : 0;
-    int sum = runs;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += up;
-    }
-    const uint64_t past = __ballot(sum > item);
-    if (past) {
-      const int l = __builtin_ctzll(past);
-      const int run = item - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(runs, l));
-      expert = base + l;
-      end = __builtin_amdgcn_readlane(hi, l);
-      first = __builtin_amdgcn_readlane(lo, l) + run * T;
-      end = min(end, first + T);
-      return true;
-    }
-    item -= __builtin_amdgcn_readlane(sum, 63);
-  }
-  return false;
-}
 
 // 16 bytes at p + k of a row of K bytes.  ALIGNED: K and p are multiples of 16;
 // past the row's end the last 16 bytes (zeroed by the caller).  Else byte by
@@ -108,6 +98,13 @@ __device__ __forceinline__ uint4 load_piece(const uint8_t* p, int k, int K) {
   }
 }
 
+__device__ __forceinline__ void blank(uint4& v, bool all) {
+  v.x = all ? 0u : v.x;
+  v.y = all ? 0u : v.y;
+  v.z = all ? 0u : v.z;
+  v.w = all ? 0u : v.w;
+}
+
 // a lane's 32 codes of a K block as the four steps' operands
 struct Operand {
   v8bf s[4];
@@ -116,51 +113,55 @@ __device__ __forceinline__ Operand operand(const uint4 (&p)[2]) {
   return Operand{{decode8(p[0].x, p[0].y), decode8(p[0].z, p[0].w), decode8(p[1].x, p[1].y), decode8(p[1].z, p[1].w)}};
 }
 
-template <int RT, int TJ, int D, bool ALIGNED>
-__global__ __launch_bounds__(THREADS) void w8a8_rows_kernel(RowsArgs a) {
-  __shared__ float red[WAVES][RT * TJ][64][4];
-  const int rt_total = a.rt0[a.w.n_members];
-  const int item = blockIdx.x / rt_total, R_tile = blockIdx.x - item * rt_total;
-  int expert = 0, first, end;
-  if (a.offsets != nullptr) {
-    if (!find_run(a.offsets, a.E, a.R, 16 * TJ, item, expert, first, end)) return;
-  } else {
-    first = item * 16 * TJ;
-    end = min(a.R, first + 16 * TJ);
-  }
-  int mi = 0;
-  while (mi + 1 < a.w.n_members && R_tile >= a.rt0[mi + 1]) ++mi;
-  const MemberDev mem = a.w.m[mi];
+// A wave's LDS: its 16 RT weight rows and 16 TJ rows of codes of one K block.
+template <int RT, int TJ>
+constexpr int wave_lds() { return (RT + TJ) * 16 * KB; }
+
+// 16-byte piece p of row r sits at piece p ^ s(r), s a permutation of r & 7 that
+// sends even rows to {0, 1, 4, 5} and odd rows to {2, 3, 6, 7}: a fragment read's
+// 16 rows over two lane groups then hit all 64 banks once.
+__device__ __forceinline__ int at_piece(int row, int p) {
+  return row * KB + ((p ^ (((row & 1) << 1) | ((row >> 1) & 1) | (row & 4))) << 4);
+}
+
+// One block's tile: 16 RT weight rows from n0 of member `mem`, rows [first, end)
+// of codes, which fill TJ column tiles.  Straight-line inside a round of D K
+// blocks per wave: with a branch between loads the compiler waits for all of
+// them where it could wait for the oldest, so a round always runs D blocks, and
+// one past the last repeats the last with scale zero.
+template <int WAVES, int RT, int TJ, int D, bool ALIGNED, bool KFULL, bool SBF16>
+__device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, int expert, int n0, int first, int end,
+                                     uint8_t* lds) {
+  constexpr int THREADS = WAVES * 64;
   const int K = a.w.K, Kb = a.w.Kb;
-  const int n0 = (R_tile - a.rt0[mi]) * 16 * RT;
   const int nb = (mem.rows + 127) >> 7;
   const uint8_t* wbase = mem.w + int64_t(expert) * mem.rows * K;
-  const int64_t s_expert = int64_t(expert) * nb * a.w.Kb;
-
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
+  const int lr = lane >> 3, lp = lane & 7;   // row and piece of a load: 8 lanes read one row's 128 bytes
+  uint8_t* const wl = lds + wave * wave_lds<RT, TJ>();
+  uint8_t* const xl = wl + RT * 16 * KB;
 
-  // rows past the member's end repeat its last one and are not stored
-  const uint8_t* wrow[RT];
+  // rows past the member's end repeat its last one and are not stored; rows past
+  // the run repeat its first, and rows without a token read token 0
+  const uint8_t* wrow[2 * RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) wrow[i] = wbase + int64_t(min(n0 + 16 * i + l16, mem.rows - 1)) * K;
-  // the column's row of codes; rows past the run and rows without a token read
-  // token 0 and are not stored, or stored as zeros
-  const uint8_t* xrow[TJ];
+  for (int q = 0; q < 2 * RT; ++q) wrow[q] = wbase + int64_t(min(n0 + 8 * q + lr, mem.rows - 1)) * K;
+  auto token = [&](int i) {
+    const int r = first + i < end ? first + i : first;
+    const int tok = a.rows ? a.rows[r] : r;
+    return tok < 0 || tok >= a.M ? 0 : tok;
+  };
+  const uint8_t* xrow[2 * TJ];
+#pragma unroll
+  for (int q = 0; q < 2 * TJ; ++q) xrow[q] = a.xq + int64_t(token(8 * q + lr)) * a.ldq;
   const float* srow[TJ];
 #pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    const int r = first + 16 * j + l16;
-    int tok = r < end ? (a.rows ? a.rows[r] : r) : 0;
-    if (tok < 0 || tok >= a.M) tok = 0;
-    xrow[j] = a.xq + int64_t(tok) * a.ldq;
-    srow[j] = a.xs + int64_t(tok) * a.xs_sm;
-  }
-  const int tiles = (end - first + 15) / 16;      // column tiles that hold rows
-  // the scale row of each row tile (a tile lies in one: 16 RT divides 128)
-  const int64_t s_off = s_expert * (a.w.s_rs ? 1 : 0) + int64_t(n0 >> 7) * a.w.s_rs;
+  for (int j = 0; j < TJ; ++j) srow[j] = a.xs + int64_t(token(16 * j + l16)) * a.xs_sm;
+  // the scale row of the row tiles (16 RT divides 128, so they lie in one)
+  const int64_t s_off = (a.w.s_rs ? int64_t(expert) * nb * Kb : 0) + int64_t(n0 >> 7) * a.w.s_rs;
 
   v4f acc[RT][TJ];
 #pragma unroll
@@ -168,88 +169,123 @@ __global__ __launch_bounds__(THREADS) void w8a8_rows_kernel(RowsArgs a) {
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-  uint4 wr[D][RT][2], xr[D][TJ][2];
-  float sa[D][TJ], sw[D];
+  // What the store needs besides the sums is loaded before everything else, so
+  // that no memory latency follows the last sum: thread tid finishes outputs o =
+  // tid + THREADS u, row o % (16 RT) of the weight tile, row o / (16 RT) of codes.
+  constexpr int OUT = (RT * TJ * 256 + THREADS - 1) / THREADS;
+  // (Raw bits, widened at their use: a conversion here would wait for the load.)
+  uint32_t bias[OUT], res[OUT];
+  int out_tok[OUT];
+#pragma unroll
+  for (int u = 0; u < OUT; ++u) {
+    const int o = tid + THREADS * u;
+    const int n = min(n0 + o % (16 * RT), mem.rows - 1), r = min(first + o / (16 * RT), end - 1);
+    bias[u] = a.ep.bias ? load_bits(a.ep.bias, a.ep.bias_bf16, mem.col0 + n) : 0;
+    res[u] = a.ep.res ? load_bits(a.ep.res, a.ep.res_bf16, int64_t(r) * a.ep.ldr + mem.col0 + n) : 0;
+    out_tok[u] = a.rows ? a.rows[r] : 0;
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  uint4 wr[D][2 * RT], xr[D][2 * TJ];
+  float sa[D][TJ];
+  // The weight scales of the wave's K blocks, one per lane: block wave + WAVES
+  // (64 h + lane) for h-th 64 rounds.
+  uint32_t swr = 0;
+  auto load_scales = [&](int h) {
+    const int c = min(wave + WAVES * (64 * h + lane), Kb - 1);
+    swr = load_bits(mem.s, SBF16, s_off + int64_t(c) * a.w.s_cs);
+  };
+  load_scales(0);
+  __builtin_amdgcn_sched_barrier(0);
   auto issue = [&](int c, int d) __attribute__((always_inline)) {
     const int cc = min(c, Kb - 1);
-    const int k = cc * KB + 16 * g;
-    sw[d] = load_real(mem.s, a.w.scale_bf16, s_off + int64_t(cc) * a.w.s_cs);
+    const int k = cc * KB + 16 * lp;
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      if (j >= tiles) continue;
-      sa[d][j] = srow[j][int64_t(cc) * a.xs_sk];
-      xr[d][j][0] = load_piece<ALIGNED, false>(xrow[j], k, K);
-      xr[d][j][1] = load_piece<ALIGNED, false>(xrow[j], k + 64, K);
-    }
+    for (int j = 0; j < TJ; ++j) sa[d][j] = srow[j][int64_t(cc) * a.xs_sk];
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      wr[d][i][0] = load_piece<ALIGNED, TJ == 1>(wrow[i], k, K);
-      wr[d][i][1] = load_piece<ALIGNED, TJ == 1>(wrow[i], k + 64, K);
-    }
+    for (int q = 0; q < 2 * TJ; ++q) xr[d][q] = load_piece<ALIGNED, false>(xrow[q], k, K);
+#pragma unroll
+    for (int q = 0; q < 2 * RT; ++q) wr[d][q] = load_piece<ALIGNED, RNT>(wrow[q], k, K);
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) {
     issue(wave + WAVES * d, d);
     __builtin_amdgcn_sched_barrier(0);
   }
-  const bool ragged = ALIGNED && K % KB != 0;
+  int round = 0;
   for (int c0 = wave; c0 < Kb; c0 += WAVES * D) {
 #pragma unroll
-    for (int d = 0; d < D; ++d) {
+    for (int d = 0; d < D; ++d, ++round) {
       const int c = c0 + WAVES * d;
-      if (c >= Kb) break;
-      if (ragged && c == Kb - 1) {
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (c * KB + 64 * h + 16 * g >= K) {
-#pragma unroll
-            for (int i = 0; i < RT; ++i) wr[d][i][h] = zero;
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) xr[d][j][h] = zero;
-          }
+      if (round == 64) {   // (K beyond 65536)
+        load_scales(c / (WAVES * 64));
+        round = 0;
       }
+      const float sw = c < Kb ? widen(__builtin_amdgcn_readlane(swr, round), SBF16) : 0.f;
+      // bytes past K: zeros on both sides (a NaN code times zero is NaN)
+      const bool past = ALIGNED && !KFULL && min(c, Kb - 1) * KB + 16 * lp >= K;
+#pragma unroll
+      for (int q = 0; q < 2 * RT; ++q) {
+        if (ALIGNED && !KFULL) blank(wr[d][q], past);
+        *reinterpret_cast<uint4*>(wl + at_piece(8 * q + lr, lp)) = wr[d][q];
+      }
+#pragma unroll
+      for (int q = 0; q < 2 * TJ; ++q) {
+        if (ALIGNED && !KFULL) blank(xr[d][q], past);
+        *reinterpret_cast<uint4*>(xl + at_piece(8 * q + lr, lp)) = xr[d][q];
+      }
+      float s[TJ];
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) s[j] = sa[d][j] * sw;
+      // the slot's registers are free: its next loads go out before this block's arithmetic
+      __builtin_amdgcn_sched_barrier(0);
+      issue(c + WAVES * D, d);
+      __builtin_amdgcn_sched_barrier(0);
+      auto fragment = [&](const uint8_t* base, int row) {
+        const uint4 p[2] = {*reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g)),
+                            *reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g + 1))};
+        return operand(p);
+      };
       Operand w[RT];
 #pragma unroll
-      for (int i = 0; i < RT; ++i) w[i] = operand(wr[d][i]);
+      for (int i = 0; i < RT; ++i) w[i] = fragment(wl, 16 * i + l16);
 #pragma unroll
       for (int j = 0; j < TJ; ++j) {
-        if (j >= tiles) continue;
-        const Operand x = operand(xr[d][j]);
-        const float s = sa[d][j] * sw[d];
+        const Operand x = fragment(xl, 16 * j + l16);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           v4f p = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].s[q], x.s[q], p, 0, 0, 0);
-          acc[i][j] += p * s;
+          acc[i][j] += p * s[j];
         }
       }
-      issue(c + WAVES * D, d);
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
   // ---- the waves' partial tiles in wave order, the epilogue, the store
+  float(*red)[RT * TJ][64][4] = reinterpret_cast<float(*)[RT * TJ][64][4]>(lds);
+  static_assert(RT * TJ * 1024 <= wave_lds<RT, TJ>(), "partial tiles fit the waves' LDS");
+  __syncthreads();   // every wave is done with its rows
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < TJ; ++j) *reinterpret_cast<v4f*>(&red[wave][i * TJ + j][lane][0]) = acc[i][j];
   __syncthreads();
-  for (int o = tid; o < RT * TJ * 256; o += THREADS) {
-    const int row = o % (16 * RT), col = o / (16 * RT);   // weight row and row of codes of the block
+#pragma unroll
+  for (int u = 0; u < OUT; ++u) {
+    const int o = tid + THREADS * u;
+    const int row = o % (16 * RT), col = o / (16 * RT);
     const int n = n0 + row, r = first + col;
-    if (n >= mem.rows || r >= end) continue;
+    if (o >= RT * TJ * 256 || n >= mem.rows || r >= end) continue;
     const int t = (row >> 4) * TJ + (col >> 4), ln = 16 * ((row & 15) >> 2) + (col & 15);
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < WAVES; ++q) v += red[q][t][ln][row & 3];
-    if (a.rows) {
-      const int tok = a.rows[r];
-      if (tok < 0 || tok >= a.M) v = 0.f;
-    }
+    if (out_tok[u] < 0 || out_tok[u] >= a.M) v = 0.f;
+    v = activate(v + widen(bias[u], a.ep.bias_bf16), a.ep.act);
+    if (a.ep.res) v = fmaf(a.ep.alpha, widen(res[u], a.ep.res_bf16), v);
     const int64_t at = int64_t(r) * a.ldy + mem.col0 + n;
-    v = epilogue(a.ep, v, r, mem.col0 + n);
     if (a.y_bf16)
       static_cast<__bf16*>(a.y)[at] = static_cast<__bf16>(v);
     else
@@ -257,7 +293,38 @@ __global__ __launch_bounds__(THREADS) void w8a8_rows_kernel(RowsArgs a) {
   }
 }
 
-template <int RT, int TJ, int D>
+// Up to TJ column tiles; a block runs the code of as many as its rows fill.
+template <int WAVES, int RT, int TJ, bool ALIGNED, bool KFULL, bool SBF16>
+__global__ __launch_bounds__(WAVES * 64) void w8a8_rows_kernel(RowsArgs a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * wave_lds<RT, TJ>()];
+  const int rt_total = a.rt0[a.w.n_members];
+  const int item = blockIdx.x / rt_total;
+  int R_tile = blockIdx.x - item * rt_total, expert = 0, first = item * 16 * TJ, end = a.R;
+  if (a.offsets != nullptr) {
+    // an expert's runs of one weight tile follow each other
+    int lo, tiles, before;
+    expert = find_run(a.offsets, a.E, a.R, 16 * TJ, item, lo, end, tiles, before);
+    if (expert < 0) return;
+    const int u = blockIdx.x - before * rt_total;
+    R_tile = u / tiles;
+    first = lo + (u - R_tile * tiles) * 16 * TJ;
+  }
+  end = min(end, first + 16 * TJ);
+  int mi = 0;
+  while (mi + 1 < a.w.n_members && R_tile >= a.rt0[mi + 1]) ++mi;
+  const MemberDev mem = a.w.m[mi];
+  const int n0 = (R_tile - a.rt0[mi]) * 16 * RT;
+  const int tiles = (end - first + 15) / 16;
+  constexpr int D1 = ALIGNED ? RD1 : 1, D2 = ALIGNED ? RD2 : 1;
+  if (TJ == 1 || tiles == 1)
+    tile<WAVES, RT, 1, D1, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+  else if (TJ == 2 || tiles == 2)
+    tile<WAVES, RT, TJ < 2 ? TJ : 2, D2, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+  else
+    tile<WAVES, RT, TJ, D2, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+}
+
+template <int WAVES, int RT, int TJ>
 bsf8_status launch(const RowsArgs& base, bool aligned, int64_t items, hipStream_t stream) {
   RowsArgs a = base;
   int r = 0;
@@ -271,15 +338,23 @@ bsf8_status launch(const RowsArgs& base, bool aligned, int64_t items, hipStream_
     set_error("UNSUPPORTED: %lld blocks", (long long)grid);
     return BSF8_E_UNSUPPORTED;
   }
-  if (aligned)
-    hipLaunchKernelGGL((w8a8_rows_kernel<RT, TJ, D, true>), dim3(unsigned(grid)), dim3(THREADS), 0, stream, a);
-  else
-    hipLaunchKernelGGL((w8a8_rows_kernel<RT, TJ, 1, false>), dim3(unsigned(grid)), dim3(THREADS), 0, stream, a);
+  const bool kfull = a.w.K % KB == 0;
+  void (*kern)(RowsArgs) =
+      a.w.scale_bf16 ? (!aligned ? w8a8_rows_kernel<WAVES, RT, TJ, false, false, true>
+                        : kfull  ? w8a8_rows_kernel<WAVES, RT, TJ, true, true, true> : w8a8_rows_kernel<WAVES, RT, TJ, true, false, true>)
+                     : (!aligned ? w8a8_rows_kernel<WAVES, RT, TJ, false, false, false>
+                        : kfull  ? w8a8_rows_kernel<WAVES, RT, TJ, true, true, false> : w8a8_rows_kernel<WAVES, RT, TJ, true, false, false>);
+  hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(WAVES * 64), 0, stream, a);
   return device_status(hipGetLastError(), "w8a8_rows launch");
 }
 
-bsf8_status launch_rows(RowsArgs& a, bool aligned, int64_t items1, int64_t items4, bool few, hipStream_t stream) {
-  return few ? launch<1, 1, 4>(a, aligned, items1, stream) : launch<1, 4, 2>(a, aligned, items4, stream);
+// The kernel that takes R rows of E weights (E = 1: one weight).
+bsf8_status launch_rows(const RowsArgs& a, bool aligned, hipStream_t stream) {
+  const int64_t R = a.R, E = a.offsets ? a.E : 1;
+  const auto items = [&](int64_t T) { return a.offsets ? std::min(E, R) + R / T : (R + T - 1) / T; };
+  const bool few = R <= RFEW * E, w4 = a.w.Kb <= RKB4;
+  if (few) return w4 ? launch<4, RRT, 1>(a, aligned, items(16), stream) : launch<8, RRT, 1>(a, aligned, items(16), stream);
+  return w4 ? launch<4, RRT, RTJ>(a, aligned, items(16 * RTJ), stream) : launch<8, RRT, RTJ>(a, aligned, items(16 * RTJ), stream);
 }
 
 }  // namespace
@@ -300,7 +375,7 @@ bsf8_status launch_w8a8_rows(const WeightDev& w, bool aligned, const uint8_t* xq
   a.M = int32_t(M);
   a.R = int32_t(M);
   a.y_bf16 = y_bf16;
-  return launch_rows(a, aligned, (M + 15) / 16, (M + 63) / 64, M <= 16, stream);
+  return launch_rows(a, aligned, stream);
 }
 
 bsf8_status launch_w8a8_expert_rows(const WeightDev& w, int64_t E, bool aligned, const uint8_t* xq, int64_t ldq,
@@ -321,8 +396,7 @@ bsf8_status launch_w8a8_expert_rows(const WeightDev& w, int64_t E, bool aligned,
   a.R = int32_t(R);
   a.E = int32_t(E);
   a.y_bf16 = y_bf16;
-  const int64_t used = E < R ? E : R;
-  return launch_rows(a, aligned, used + R / 16, used + R / 64, R <= 16 * E, stream);
+  return launch_rows(a, aligned, stream);
 }
 
 std::string describe_w8a8_rows(bool few, bool aligned) {

@@ -9,7 +9,7 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "bsf8_epilogue.h"
+#include "bsf8_fused.h"
 #include "bsf8_internal.h"
 
 // buffer_load ... lds: each lane's 16 bytes land at lds + 16 * lane (the LLVM intrinsic).
@@ -203,52 +203,6 @@ struct FusedArgs : FastArgs {
 };
 template <int MODE>
 using ArgsOf = std::conditional_t<MODE == kEpilogue || MODE == kExperts, FusedArgs, FastArgs>;
-
-// Experts' runs as the tiles take them.  Each expert's rows are cut into tiles
-// of T; all tiles of all experts, times the weight's row tiles, are the blocks
-// that have work.  The runs lie in device memory, so each wave counts the tiles
-// of 64 experts at a time and sums across its lanes.
-__device__ __forceinline__ int run_tiles(const int32_t* offsets, int E, int R, int T, int e, int& lo, int& hi) {
-  const int i = min(e, E - 1);
-  lo = min(max(offsets[i], 0), R);
-  hi = min(max(offsets[i + 1], lo), R);
-  return e < E ? (hi - lo + T - 1) / T : 0;
-}
-__device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T) {
-  int sum = 0, lo, hi;
-  for (int e = threadIdx.x & 63; e < E; e += 64) sum += run_tiles(offsets, E, R, T, e, lo, hi);
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  return __builtin_amdgcn_readfirstlane(sum);
-}
-// The expert that holds tile `tile` (below their sum): its rows [lo, hi), its
-// tiles, and the tiles of the experts before it.
-__device__ __forceinline__ int find_run(const int32_t* offsets, int E, int R, int T, int tile, int& lo, int& hi,
-                                        int& tiles, int& before) {
-  const int lane = threadIdx.x & 63;
-  before = 0;
-  for (int base = 0; base < E; base += 64) {
-    int l, h;
-    const int n = run_tiles(offsets, E, R, T, base + lane, l, h);
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += up;
-    }
-    const uint64_t past = __ballot(before + sum > tile);
-    if (past) {
-      const int at = __builtin_ctzll(past);
-      lo = __builtin_amdgcn_readlane(l, at);
-      hi = __builtin_amdgcn_readlane(h, at);
-      tiles = __builtin_amdgcn_readlane(n, at);
-      before += __builtin_amdgcn_readlane(sum, at) - tiles;
-      return base + at;
-    }
-    before += __builtin_amdgcn_readlane(sum, 63);
-  }
-  return -1;
-}
 
 __device__ __forceinline__ v4i make_rsrc(const void* p, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(p);
