@@ -1,6 +1,7 @@
 // The W8A8 product with bias, activation and residual (gfx950): which kernel
 // takes a call, and the tile GEMM's instances with an epilogue.
 #include <cstdio>
+#include <cstdlib>
 #include <string>
 
 #include "bsf8_tile.h"
@@ -11,7 +12,7 @@ namespace {
 // Up to this many tokens the few-row kernel.
 constexpr int64_t kRowsMaxM = 48;
 
-bool by_rows(const Plan& p, int64_t M) { return !p.fast || M <= kRowsMaxM; }
+bool by_rows(const Plan& p, int64_t M) { return !p.fast || M <= (getenv("XM") ? atoi(getenv("XM")) : kRowsMaxM); }
 
 // F32 outputs sum the codes exactly (128 x 128 tiles); BF16 outputs take the FP8 MFMA.
 Plan plan_of(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t xs_extent, bool y_bf16) {

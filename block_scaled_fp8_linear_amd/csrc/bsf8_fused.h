@@ -101,38 +101,49 @@ __device__ __forceinline__ int run_tiles(const int32_t* offsets, int E, int R, i
   hi = min(max(offsets[i + 1], lo), R);
   return e < E ? (hi - lo + T - 1) / T : 0;
 }
-__device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T) {
-  int sum = 0, lo, hi;
-  for (int e = threadIdx.x & 63; e < E; e += 64) sum += run_tiles(offsets, E, R, T, e, lo, hi);
+// 64 experts' tiles, one expert per lane: rows, tiles, and the tiles up to and with it.
+struct Runs {
+  int lo, hi, n, sum;
+};
+__device__ __forceinline__ Runs runs_of(const int32_t* offsets, int E, int R, int T, int base) {
+  const int lane = threadIdx.x & 63;
+  Runs r;
+  r.n = run_tiles(offsets, E, R, T, base + lane, r.lo, r.hi);
+  r.sum = r.n;
 #pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  return __builtin_amdgcn_readfirstlane(sum);
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(r.sum, d, 64);
+    if (lane >= d) r.sum += up;
+  }
+  return r;
+}
+// Tiles of all experts; `first` keeps those of the first 64 experts.
+__device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T, Runs& first) {
+  first = runs_of(offsets, E, R, T, 0);
+  int sum = __builtin_amdgcn_readlane(first.sum, 63);
+  for (int base = 64; base < E; base += 64) {
+    const Runs r = runs_of(offsets, E, R, T, base);
+    sum += __builtin_amdgcn_readlane(r.sum, 63);
+  }
+  return sum;
 }
 // The expert that holds tile `tile`, -1 past the last: its rows [lo, hi), its
 // tiles, and the tiles of the experts before it.
-__device__ __forceinline__ int find_run(const int32_t* offsets, int E, int R, int T, int tile, int& lo, int& hi,
+__device__ __forceinline__ int find_run(const int32_t* offsets, int E, int R, int T, Runs r, int tile, int& lo, int& hi,
                                         int& tiles, int& before) {
-  const int lane = threadIdx.x & 63;
   before = 0;
   for (int base = 0; base < E; base += 64) {
-    int l, h;
-    const int n = run_tiles(offsets, E, R, T, base + lane, l, h);
-    int sum = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d, 64);
-      if (lane >= d) sum += up;
-    }
-    const uint64_t past = __ballot(before + sum > tile);
+    if (base) r = runs_of(offsets, E, R, T, base);
+    const uint64_t past = __ballot(before + r.sum > tile);
     if (past) {
       const int at = __builtin_ctzll(past);
-      lo = __builtin_amdgcn_readlane(l, at);
-      hi = __builtin_amdgcn_readlane(h, at);
-      tiles = __builtin_amdgcn_readlane(n, at);
-      before += __builtin_amdgcn_readlane(sum, at) - tiles;
+      lo = __builtin_amdgcn_readlane(r.lo, at);
+      hi = __builtin_amdgcn_readlane(r.hi, at);
+      tiles = __builtin_amdgcn_readlane(r.n, at);
+      before += __builtin_amdgcn_readlane(r.sum, at) - tiles;
       return base + at;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    before += __builtin_amdgcn_readlane(r.sum, 63);
   }
   return -1;
 }

@@ -303,7 +303,7 @@ __global__ __launch_bounds__(WAVES * 64) void w8a8_rows_kernel(RowsArgs a) {
   if (a.offsets != nullptr) {
     // an expert's runs of one weight tile follow each other
     int lo, tiles, before;
-    expert = find_run(a.offsets, a.E, a.R, 16 * TJ, item, lo, end, tiles, before);
+    expert = find_run(a.offsets, a.E, a.R, 16 * TJ, runs_of(a.offsets, a.E, a.R, 16 * TJ, 0), item, lo, end, tiles, before);
     if (expert < 0) return;
     const int u = blockIdx.x - before * rt_total;
     R_tile = u / tiles;

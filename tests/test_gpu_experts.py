@@ -83,7 +83,7 @@ def check(counts, rows, K, gather=True, M=None, y="bf16", f32_scales=False, toke
     B.linear_w8a8_experts(w, xq, xs, t.from_numpy(offsets).to(device()),
                           rows=t.from_numpy(idx).to(device()) if gather else None, out_dtype=out.dtype, out=out[:, :N])
     t.cuda.synchronize()
-    verify(to_np(out), q, s, om, offsets, idx, N, K, y == "bf16", fp8_mfma=y == "bf16" and "f8f6f4" in w.describe(R))
+    verify(to_np(out), q, s, om, offsets, idx, N, K, y == "bf16", fp8_mfma=y == "bf16" and "f8f6f4" in w.describe(R))   # (F32 outputs never use it)
 
 
 # run lengths around the tiles, experts without rows at both ends and between, one expert, more than 64 experts
