@@ -112,6 +112,7 @@ struct EpilogueDev {
   int64_t ldr;
   float alpha;
   int32_t bias_bf16, res_bf16, act;
+  int32_t res_vec;   // the residual's rows allow 16-byte loads
 };
 
 // The few-row kernel: one weight with an epilogue, and the experts' products.

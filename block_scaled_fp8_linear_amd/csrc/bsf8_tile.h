@@ -282,12 +282,114 @@ __device__ __forceinline__ void store_tile_via_lds(const v4f (&acc)[STI][STJ], u
   }
 }
 
-// The same with an epilogue: the tile goes through LDS as F32, 32 columns at a
-// time, and each lane finishes four outputs of one token row.
-template <int STI, int STJ, bool YBF16>
+// Bias of columns c + 16 i + e, raw (zeros without one).
+__device__ __forceinline__ void load_bias(const EpilogueDev& ep, int64_t c, uint32_t (&b)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) b[i >> 2][i & 3] = 0;
+  if (ep.bias && ep.bias_bf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(ep.bias) + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i >> 2][i & 3] = p[16 * (i >> 2) + (i & 3)];
+  } else if (ep.bias) {
+    const uint32_t* p = static_cast<const uint32_t*>(ep.bias) + c;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) b[i >> 2][i & 3] = p[16 * (i >> 2) + (i & 3)];
+  }
+}
+
+// The same with an epilogue.  The tile goes through LDS as F32, 64 columns of some
+// of the wave's tokens at a time, and a lane finishes eight outputs of a token
+// row: a 128-byte line of BF16 per eight lanes, as above.  Whole strips on aligned
+// rows only (the routine below takes the others): with the tests of those in it
+// the compiler spills the tile.  A round's residual loads go out together, before
+// its values are written to LDS: one by one behind each other's stores their
+// latency, some 32 times per block, took 5 us.
+// RES: the residual is absent (0), BF16 (4 words per lane and row) or F32 (8).
+constexpr int E_PITCH = 272;   // bytes per token row of the staging (64 F32 + 16: no bank conflicts)
+template <int STI, int STJ, bool YBF16, int RES>
 __device__ __forceinline__ void store_tile_epilogue(const v4f (&acc)[STI][STJ], uint8_t* buf, const EpilogueDev& ep,
-                                                    void* y, int64_t ldy, int64_t col0, int n_base, int n_end,
-                                                    int m_base, int M, int lane) {
+                                                    void* y, int64_t ldy, int64_t col0, int n_base, int m_base, int M,
+                                                    int lane) {
+  constexpr int HJ = RES == 8 ? 1 : STJ / 2, IT = 2 * HJ;   // token tiles per round; token rows per lane and round
+  constexpr int ESZ = YBF16 ? 2 : 4;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int n = n_base + (lane & 7) * 8;
+  const int m_lane = m_base + (lane >> 3);   // the lane's token rows are m_lane + 8 i
+  const uint8_t* rp = static_cast<const uint8_t*>(ep.res) + (int64_t(m_lane) * ep.ldr + col0 + n) * (RES / 2);
+  uint8_t* yp = static_cast<uint8_t*>(y) + (int64_t(m_lane) * ldy + col0 + n) * ESZ;
+  const int64_t r8 = ep.ldr * 8 * (RES / 2), y8 = ldy * 8 * ESZ;
+#pragma unroll
+  for (int i0 = 0; i0 < STI; i0 += 4) {
+    // bias in the MFMA layout: columns 4 g + e of the four row tiles
+    uint32_t bias[4][4];
+    load_bias(ep, col0 + n_base + i0 * 16 + 4 * g, bias);
+#pragma unroll
+    for (int j0 = 0; j0 < STJ; j0 += HJ) {
+      __builtin_amdgcn_sched_barrier(0);   // a round's loads stay in it (hoisted, they crowd out the tile)
+      uint4 res[IT][RES ? RES / 4 : 1];
+      if constexpr (RES != 0) {
+#pragma unroll
+        for (int t = 0; t < IT; ++t)
+#pragma unroll
+          for (int h = 0; h < RES / 4; ++h) {
+            res[t][h] = make_uint4(0, 0, 0, 0);
+            if (m_lane + 16 * j0 + 8 * t < M)
+              res[t][h] = reinterpret_cast<const uint4*>(rp + (2 * j0 + t) * r8 + i0 * 16 * (RES / 2))[h];
+          }
+      }
+      float x[HJ * 16];
+#pragma unroll
+      for (int j = 0; j < HJ; ++j)
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[16 * j + 4 * ii + e] = acc[i0 + ii][j0 + j][e] + widen(bias[ii][e], ep.bias_bf16);
+      __builtin_amdgcn_sched_barrier(0);
+      activate_all(x, ep.act);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < HJ; ++j)
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const float* v = x + 16 * j + 4 * ii;
+          *reinterpret_cast<v4f*>(buf + (16 * j + l16) * E_PITCH + (ii * 16 + 4 * g) * 4) = v4f{v[0], v[1], v[2], v[3]};
+        }
+#pragma unroll
+      for (int t = 0; t < IT; ++t) {
+        const v4f* p = reinterpret_cast<const v4f*>(buf + (8 * t + (lane >> 3)) * E_PITCH + (lane & 7) * 32);
+        const v4f lo = p[0], hi = p[1];
+        if (m_lane + 16 * j0 + 8 * t >= M) continue;
+        float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        if constexpr (RES == 4) {
+          const uint32_t w[4] = {res[t][0].x, res[t][0].y, res[t][0].z, res[t][0].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = fmaf(ep.alpha, __uint_as_float((e & 1) ? w[e >> 1] & 0xFFFF0000u : w[e >> 1] << 16), v[e]);
+        } else if constexpr (RES == 8) {
+          const uint32_t w[8] = {res[t][0].x, res[t][0].y, res[t][0].z, res[t][0].w,
+                                 res[t][RES / 8].x, res[t][RES / 8].y, res[t][RES / 8].z, res[t][RES / 8].w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = fmaf(ep.alpha, __uint_as_float(w[e]), v[e]);
+        }
+        uint8_t* o = yp + (2 * j0 + t) * y8 + i0 * 16 * ESZ;
+        if (YBF16) {
+          *reinterpret_cast<uint4*>(o) =
+              make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+        } else {
+          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      }
+    }
+  }
+}
+
+// Strips that end inside the wave's columns, or rows that are not 16-byte
+// aligned: 32 columns at a time, four outputs of a token row per lane.
+template <int STI, int STJ, bool YBF16>
+__device__ __forceinline__ void store_tile_epilogue_any(const v4f (&acc)[STI][STJ], uint8_t* buf, const EpilogueDev& ep,
+                                                        void* y, int64_t ldy, int64_t col0, int n_base, int n_end,
+                                                        int m_base, int M, int lane) {
   const int l16 = lane & 15, g = lane >> 4;
 #pragma unroll
   for (int i0 = 0; i0 < STI; i0 += 2) {
@@ -716,10 +818,17 @@ __global__ __launch_bounds__(FTHREADS, tile_waves(T, MODE, EXACT)) void w8a8_gem
         store_tile_via_lds<TI, TJ, false>(acc, buf, a.ws + int64_t(split) * M * a.ldws, a.ldws,
                                   int64_t(R - a.rt_split0) * FBN - n0, n0 + wn * WN, mem.rows, m0 + wm * WM, M, lane);
       else if constexpr (MODE == kEpilogue) {
-        if (a.y_bf16)
-          store_tile_epilogue<TI, TJ, true>(acc, buf, a.ep, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
-        else
-          store_tile_epilogue<TI, TJ, false>(acc, buf, a.ep, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
+        // (EXACT instances serve F32 outputs, the others BF16)
+        const int nw = n0 + wn * WN, mw = m0 + wm * WM;
+        auto store = [&](auto res) __attribute__((always_inline)) {
+          store_tile_epilogue<TI, TJ, !EXACT, decltype(res)::value>(acc, buf, a.ep, a.y, a.ldy, mem.col0, nw, mw, m_end,
+                                                                    lane);
+        };
+        if (!a.y_vec || !a.ep.res_vec || nw + WN > mem.rows)
+          store_tile_epilogue_any<TI, TJ, !EXACT>(acc, buf, a.ep, a.y, a.ldy, mem.col0, nw, mem.rows, mw, m_end, lane);
+        else if (!a.ep.res) store(std::integral_constant<int, 0>{});
+        else if (a.ep.res_bf16) store(std::integral_constant<int, 4>{});
+        else store(std::integral_constant<int, 8>{});
       } else if (a.y_bf16 && a.y_nt)
         store_tile_via_lds<TI, TJ, true, true>(acc, buf, a.y, a.ldy, mem.col0, n0 + wn * WN, mem.rows, m0 + wm * WM, m_end, lane);
       else if (a.y_bf16)
@@ -1012,7 +1121,13 @@ bsf8_status launch_fast(const Plan& p, const WeightDev& w, const uint8_t* xq, in
     }
     a.ws = static_cast<float*>(ws);
   }
-  if constexpr (MODE == kEpilogue) a.ep = *ep;
+  if constexpr (MODE == kEpilogue) {
+    a.ep = *ep;
+    const int64_t rsz = ep->res_bf16 ? 2 : 4;
+    bool rvec = (reinterpret_cast<uintptr_t>(ep->res) & 15) == 0 && (ep->ldr * rsz) % 16 == 0;
+    for (int i = 0; i < w.n_members; ++i) rvec = rvec && (w.m[i].col0 * rsz) % 16 == 0;
+    a.ep.res_vec = rvec ? 1 : 0;
+  }
   const bool kfull = w.K % KBYTES == 0;
   void (*kern)(ArgsOf<MODE>);
   if constexpr (MODE == kDense)   // (no scales: one type serves)
@@ -1024,7 +1139,7 @@ bsf8_status launch_fast(const Plan& p, const WeightDev& w, const uint8_t* xq, in
   bsf8_status st = device_status(hipGetLastError(), MODE == kDense ? "dense_gemm launch" : "w8a8_gemm_fast launch");
   if (st != BSF8_OK || p.splits == 1) return st;
   std::conditional_t<MODE == kEpilogue, FusedReduceArgs, ReduceArgs> r{};
-  if constexpr (MODE == kEpilogue) r.ep = *ep;
+  if constexpr (MODE == kEpilogue) r.ep = a.ep;
   r.ws = a.ws;
   r.ldws = p.ldws;
   r.split_stride = M * p.ldws;
