@@ -41,29 +41,9 @@ namespace {
 
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+typedef u4v __attribute__((aligned(1))) u4v_any;   // (the hardware loads 16 bytes from any address)
 
 constexpr int KB = 128;
-#ifndef RNT
-#define RNT true
-#endif
-#ifndef RD1
-#define RD1 1
-#endif
-#ifndef RD2
-#define RD2 1
-#endif
-#ifndef RFEW
-#define RFEW 16
-#endif
-#ifndef RKB4
-#define RKB4 16
-#endif
-#ifndef RTJ
-#define RTJ 4
-#endif
-#ifndef RRT
-#define RRT 2
-#endif
 
 struct RowsArgs {
   WeightDev w;                      // expert 0's members
@@ -81,28 +61,58 @@ struct RowsArgs {
   int32_t y_bf16;
 };
 
-// 16 bytes at p + k of a row of K bytes.  ALIGNED: K and p are multiples of 16;
-// past the row's end the last 16 bytes (zeroed by the caller).  Else byte by
-// byte, zeros past the end.
-template <bool ALIGNED, bool NT>
-__device__ __forceinline__ uint4 load_piece(const uint8_t* p, int k, int K) {
-  if constexpr (ALIGNED) {
-    const u4v* q = reinterpret_cast<const u4v*>(p + min(k, K - 16));
-    const u4v v = NT ? __builtin_nontemporal_load(q) : *q;
-    return make_uint4(v.x, v.y, v.z, v.w);
-  } else {
-    uint32_t b[4] = {0, 0, 0, 0};
-    const int n = min(16, K - k);
-    for (int i = 0; i < n; ++i) b[i >> 2] |= uint32_t(p[k + i]) << (8 * (i & 3));
-    return make_uint4(b[0], b[1], b[2], b[3]);
-  }
-}
-
 __device__ __forceinline__ void blank(uint4& v, bool all) {
   v.x = all ? 0u : v.x;
   v.y = all ? 0u : v.y;
   v.z = all ? 0u : v.z;
   v.w = all ? 0u : v.w;
+}
+
+// How a row's 16-byte pieces are read.
+enum Access {
+  kAligned,     // K and every row a multiple of 16
+  kUnaligned,   // K >= 16: loads at any byte address, the last piece ending at K
+  kBytes        // K < 16
+};
+
+// 16 bytes at p + k of a row of K bytes; a piece that does not lie in the row is
+// read as the row's last 16 bytes and put right by clip().
+template <Access ACCESS, bool NT>
+__device__ __forceinline__ uint4 load_piece(const uint8_t* p, int k, int K) {
+  if constexpr (ACCESS == kAligned) {
+    const u4v* q = reinterpret_cast<const u4v*>(p + min(k, K - 16));
+    const u4v v = NT ? __builtin_nontemporal_load(q) : *q;
+    return make_uint4(v.x, v.y, v.z, v.w);
+  } else if constexpr (ACCESS == kUnaligned) {
+    const u4v v = *reinterpret_cast<const u4v_any*>(p + min(k, K - 16));
+    return make_uint4(v.x, v.y, v.z, v.w);
+  } else {
+    uint32_t b[4] = {0, 0, 0, 0};
+    for (int i = 0; i < K; ++i)
+      if (k == 0) b[i >> 2] |= uint32_t(p[i]) << (8 * (i & 3));
+    return make_uint4(b[0], b[1], b[2], b[3]);
+  }
+}
+// The piece at k of what load_piece read: bytes past K become zeros.
+template <Access ACCESS>
+__device__ __forceinline__ void clip(uint4& v, int k, int K) {
+  if constexpr (ACCESS == kAligned) {
+    blank(v, k >= K);
+  } else if constexpr (ACCESS == kUnaligned) {
+    const int d = k - min(k, K - 16);   // the piece starts d bytes into what was read
+    const int s = 8 * (d & 7);
+    uint64_t lo = uint64_t(v.x) | uint64_t(v.y) << 32, hi = uint64_t(v.z) | uint64_t(v.w) << 32;
+    if (d & 8) {
+      lo = hi;
+      hi = 0;
+    }
+    if (s) {
+      lo = lo >> s | hi << (64 - s);
+      hi >>= s;
+    }
+    v = make_uint4(uint32_t(lo), uint32_t(lo >> 32), uint32_t(hi), uint32_t(hi >> 32));
+    blank(v, d >= 16);
+  }
 }
 
 // a lane's 32 codes of a K block as the four steps' operands
@@ -129,7 +139,7 @@ __device__ __forceinline__ int at_piece(int row, int p) {
 // blocks per wave: with a branch between loads the compiler waits for all of
 // them where it could wait for the oldest, so a round always runs D blocks, and
 // one past the last repeats the last with scale zero.
-template <int WAVES, int RT, int TJ, int D, bool ALIGNED, bool KFULL, bool SBF16>
+template <int WAVES, int RT, int TJ, int D, Access ACCESS, bool KFULL, bool SBF16>
 __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, int expert, int n0, int first, int end,
                                      uint8_t* lds) {
   constexpr int THREADS = WAVES * 64;
@@ -203,9 +213,9 @@ __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, in
 #pragma unroll
     for (int j = 0; j < TJ; ++j) sa[d][j] = srow[j][int64_t(cc) * a.xs_sk];
 #pragma unroll
-    for (int q = 0; q < 2 * TJ; ++q) xr[d][q] = load_piece<ALIGNED, false>(xrow[q], k, K);
+    for (int q = 0; q < 2 * TJ; ++q) xr[d][q] = load_piece<ACCESS, false>(xrow[q], k, K);
 #pragma unroll
-    for (int q = 0; q < 2 * RT; ++q) wr[d][q] = load_piece<ALIGNED, RNT>(wrow[q], k, K);
+    for (int q = 0; q < 2 * RT; ++q) wr[d][q] = load_piece<ACCESS, true>(wrow[q], k, K);
   };
 #pragma unroll
   for (int d = 0; d < D; ++d) {
@@ -223,17 +233,17 @@ __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, in
       }
       const float sw = c < Kb ? widen(__builtin_amdgcn_readlane(swr, round), SBF16) : 0.f;
       // bytes past K: zeros on both sides (a NaN code times zero is NaN)
-      const bool past = ALIGNED && !KFULL && min(c, Kb - 1) * KB + 16 * lp >= K;
+      if (!KFULL && ACCESS != kBytes && c >= Kb - 1) {
+        const int k = (Kb - 1) * KB + 16 * lp;
 #pragma unroll
-      for (int q = 0; q < 2 * RT; ++q) {
-        if (ALIGNED && !KFULL) blank(wr[d][q], past);
-        *reinterpret_cast<uint4*>(wl + at_piece(8 * q + lr, lp)) = wr[d][q];
+        for (int q = 0; q < 2 * RT; ++q) clip<ACCESS>(wr[d][q], k, K);
+#pragma unroll
+        for (int q = 0; q < 2 * TJ; ++q) clip<ACCESS>(xr[d][q], k, K);
       }
 #pragma unroll
-      for (int q = 0; q < 2 * TJ; ++q) {
-        if (ALIGNED && !KFULL) blank(xr[d][q], past);
-        *reinterpret_cast<uint4*>(xl + at_piece(8 * q + lr, lp)) = xr[d][q];
-      }
+      for (int q = 0; q < 2 * RT; ++q) *reinterpret_cast<uint4*>(wl + at_piece(8 * q + lr, lp)) = wr[d][q];
+#pragma unroll
+      for (int q = 0; q < 2 * TJ; ++q) *reinterpret_cast<uint4*>(xl + at_piece(8 * q + lr, lp)) = xr[d][q];
       float s[TJ];
 #pragma unroll
       for (int j = 0; j < TJ; ++j) s[j] = sa[d][j] * sw;
@@ -294,7 +304,7 @@ __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, in
 }
 
 // Up to TJ column tiles; a block runs the code of as many as its rows fill.
-template <int WAVES, int RT, int TJ, bool ALIGNED, bool KFULL, bool SBF16>
+template <int WAVES, int RT, int TJ, Access ACCESS, bool KFULL, bool SBF16>
 __global__ __launch_bounds__(WAVES * 64) void w8a8_rows_kernel(RowsArgs a) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * wave_lds<RT, TJ>()];
   const int rt_total = a.rt0[a.w.n_members];
@@ -315,13 +325,23 @@ __global__ __launch_bounds__(WAVES * 64) void w8a8_rows_kernel(RowsArgs a) {
   const MemberDev mem = a.w.m[mi];
   const int n0 = (R_tile - a.rt0[mi]) * 16 * RT;
   const int tiles = (end - first + 15) / 16;
-  constexpr int D1 = ALIGNED ? RD1 : 1, D2 = ALIGNED ? RD2 : 1;
   if (TJ == 1 || tiles == 1)
-    tile<WAVES, RT, 1, D1, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, 1, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
   else if (TJ == 2 || tiles == 2)
-    tile<WAVES, RT, TJ < 2 ? TJ : 2, D2, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, TJ < 2 ? TJ : 2, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
   else
-    tile<WAVES, RT, TJ, D2, ALIGNED, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, TJ, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+}
+
+template <int WAVES, int RT, int TJ, bool SBF16>
+auto pick(bool aligned, int K) -> void (*)(RowsArgs) {
+  const bool kfull = K % KB == 0;
+  if (aligned)
+    return kfull ? w8a8_rows_kernel<WAVES, RT, TJ, kAligned, true, SBF16> : w8a8_rows_kernel<WAVES, RT, TJ, kAligned, false, SBF16>;
+  if constexpr (WAVES == 4)
+    if (K < 16) return w8a8_rows_kernel<WAVES, RT, TJ, kBytes, false, SBF16>;
+  // (any K: unaligned rows with K a multiple of 128 take it too)
+  return w8a8_rows_kernel<WAVES, RT, TJ, kUnaligned, false, SBF16>;
 }
 
 template <int WAVES, int RT, int TJ>
@@ -338,12 +358,7 @@ bsf8_status launch(const RowsArgs& base, bool aligned, int64_t items, hipStream_
     set_error("UNSUPPORTED: %lld blocks", (long long)grid);
     return BSF8_E_UNSUPPORTED;
   }
-  const bool kfull = a.w.K % KB == 0;
-  void (*kern)(RowsArgs) =
-      a.w.scale_bf16 ? (!aligned ? w8a8_rows_kernel<WAVES, RT, TJ, false, false, true>
-                        : kfull  ? w8a8_rows_kernel<WAVES, RT, TJ, true, true, true> : w8a8_rows_kernel<WAVES, RT, TJ, true, false, true>)
-                     : (!aligned ? w8a8_rows_kernel<WAVES, RT, TJ, false, false, false>
-                        : kfull  ? w8a8_rows_kernel<WAVES, RT, TJ, true, true, false> : w8a8_rows_kernel<WAVES, RT, TJ, true, false, false>);
+  void (*kern)(RowsArgs) = a.w.scale_bf16 ? pick<WAVES, RT, TJ, true>(aligned, a.w.K) : pick<WAVES, RT, TJ, false>(aligned, a.w.K);
   hipLaunchKernelGGL(kern, dim3(unsigned(grid)), dim3(WAVES * 64), 0, stream, a);
   return device_status(hipGetLastError(), "w8a8_rows launch");
 }
@@ -352,9 +367,9 @@ bsf8_status launch(const RowsArgs& base, bool aligned, int64_t items, hipStream_
 bsf8_status launch_rows(const RowsArgs& a, bool aligned, hipStream_t stream) {
   const int64_t R = a.R, E = a.offsets ? a.E : 1;
   const auto items = [&](int64_t T) { return a.offsets ? std::min(E, R) + R / T : (R + T - 1) / T; };
-  const bool few = R <= RFEW * E, w4 = a.w.Kb <= RKB4;
-  if (few) return w4 ? launch<4, RRT, 1>(a, aligned, items(16), stream) : launch<8, RRT, 1>(a, aligned, items(16), stream);
-  return w4 ? launch<4, RRT, RTJ>(a, aligned, items(16 * RTJ), stream) : launch<8, RRT, RTJ>(a, aligned, items(16 * RTJ), stream);
+  const bool few = R <= 16 * E, w4 = a.w.Kb <= 16;
+  if (few) return w4 ? launch<4, 2, 1>(a, aligned, items(16), stream) : launch<8, 2, 1>(a, aligned, items(16), stream);
+  return w4 ? launch<4, 2, 4>(a, aligned, items(64), stream) : launch<8, 2, 4>(a, aligned, items(64), stream);
 }
 
 }  // namespace
@@ -402,7 +417,7 @@ bsf8_status launch_w8a8_expert_rows(const WeightDev& w, int64_t E, bool aligned,
 std::string describe_w8a8_rows(bool few, bool aligned) {
   char buf[256];
   snprintf(buf, sizeof(buf), "arithmetic=e4m3 codes decoded exactly to bf16, mfma_f32_16x16x32_bf16, f32 per-128-K epilogue | "
-           "kernel=w8a8_rows rows<=%d path=%s", few ? 16 : 64, aligned ? "aligned16" : "bytewise");
+           "kernel=w8a8_rows rows<=%d path=%s", few ? 16 : 64, aligned ? "aligned16" : "unaligned");
   return buf;
 }
 
