@@ -708,7 +708,9 @@ def linear_w8a8_epilogue(w: BlockFP8Weight, xq, xs, *, bias=None, activation=Non
     """linear_w8a8 and what follows it in one call: y = activation(x . W^T + bias) + residual_scale * residual.
 
     bias: [N]; residual: [M, N], which may be ``out`` itself (float32 or bfloat16 both); activation: None, "relu",
-    "silu", "gelu" or "gelu_tanh".  y is bfloat16 unless out_dtype says float32."""
+    "silu", "gelu" or "gelu_tanh".  y is bfloat16 unless out_dtype says float32.  workspace: (tensor, bytes) as
+    workspace_size(ARM_W8A8_EPILOGUE, M) says; without it a call that needs one takes its own from the allocator, so
+    that graphs captured on one stream may be replayed at the same time."""
     torch = _torch()
     real = (torch.float32, torch.bfloat16)
     out_dtype = out_dtype or torch.bfloat16
@@ -727,7 +729,11 @@ def linear_w8a8_epilogue(w: BlockFP8Weight, xq, xs, *, bias=None, activation=Non
         e.residual, e.ldr = residual.data_ptr(), _pitch("residual", residual, M, N, real)
         e.residual_dtype, e.residual_scale = _dt_of(residual), residual_scale
     y, ldy = _output(out, M, N, out_dtype, w.device)
-    ws, wsb = workspace if workspace is not None else w.workspace(ARM_W8A8_EPILOGUE, M)
+    if workspace is not None:
+        ws, wsb = workspace
+    else:
+        wsb = w.workspace_size(ARM_W8A8_EPILOGUE, M)
+        ws = torch.empty(wsb, dtype=torch.uint8, device=w.device) if wsb else None
     _launch("linear_w8a8_epilogue", idx, lib().bsf8_linear_w8a8_epilogue, w.handle, xq.data_ptr(), ldq, xs.data_ptr(),
             sm, sk, M, ctypes.byref(e), y.data_ptr(), _dt_of(y), ldy, ws.data_ptr() if ws is not None else None, wsb)
     return y

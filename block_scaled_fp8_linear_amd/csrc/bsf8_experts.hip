@@ -80,7 +80,7 @@ bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, con
   a.R = int32_t(R);
   // the most tiles that R rows of E experts can make; blocks past the last one leave
   const int64_t grid = ((E < R ? E : R) + R / T) * r;
-  if (grid > INT32_MAX) {
+  if (grid * FTHREADS > UINT32_MAX) {
     set_error("UNSUPPORTED: %lld blocks", (long long)grid);
     return BSF8_E_UNSUPPORTED;
   }

@@ -156,15 +156,18 @@ __device__ __forceinline__ Runs runs_of(const int32_t* offsets, int E, int R, in
   }
   return r;
 }
-// Tiles of all experts; `first` keeps those of the first 64 experts.
+// Tiles of all experts; `first` keeps those of the first 64 experts.  Ascending
+// offsets make at most min(E, R) + R / T of them, and the count ends there, so
+// that overlapping runs (descending offsets) cannot pass 32 bits.
 __device__ __forceinline__ int all_run_tiles(const int32_t* offsets, int E, int R, int T, Runs& first) {
   first = runs_of(offsets, E, R, T, 0);
   int sum = __builtin_amdgcn_readlane(first.sum, 63);
-  for (int base = 64; base < E; base += 64) {
+  const int most = min(E, R) + R / T;
+  for (int base = 64; base < E && sum < most; base += 64) {
     const Runs r = runs_of(offsets, E, R, T, base);
     sum += __builtin_amdgcn_readlane(r.sum, 63);
   }
-  return sum;
+  return min(sum, most);
 }
 // The expert that holds tile `tile`, -1 past the last: its rows [lo, hi), its
 // tiles, and the tiles of the experts before it.

@@ -62,6 +62,7 @@ struct NormDev {
   int32_t post_bf16, gate_bf16, w_bf16, n_bf16;
   int32_t x_vec, res_vec, h_vec, n_vec, q_vec, post_vec, gate_vec, w_vec;   // wide accesses allowed
   int32_t wide;    // all of them, K % 8 == 0 and one type of weights
+  int64_t m0;      // first row of the launch
   double eps, alpha;
   const void* x;
   const int32_t* slots;

@@ -217,7 +217,7 @@ template <int T, int V, bool XBF16, bool HBF16>
 __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(NormDev a) {
   __shared__ double lds[T / 64];
   const int t = threadIdx.x & (T - 1);
-  const int64_t m = T == 64 ? int64_t(blockIdx.x) * (kSmallBlock / 64) + (threadIdx.x >> 6) : int64_t(blockIdx.x);
+  const int64_t m = T == 64 ? a.m0 + int64_t(blockIdx.x) * (kSmallBlock / 64) + (threadIdx.x >> 6) : a.m0 + int64_t(blockIdx.x);
   if (T == 64 && m >= a.M) return;   // whole waves; a wave-wide row meets no barrier
   const int K = a.K;
   int k[V], valid[V];
@@ -466,7 +466,7 @@ __global__ __launch_bounds__(V == 1 ? 128 : 1024) void quant_norm_wide_kernel(No
   const bool on = k[V - 1] < K;
   if (!on) k[V - 1] = 0;
   const double inv_k = 1.0 / double(K);
-  const int64_t m = blockIdx.x;
+  const int64_t m = a.m0 + int64_t(blockIdx.x);
 
   // ---- the block's output; the residual's loads go out with it
   Raw<HBF16> res[V];
@@ -641,7 +641,8 @@ Kern pick_wide(bool x_bf16, bool h_bf16, bool w_bf16) {
 
 }  // namespace
 
-bsf8_status launch_quant_norm(const NormDev& a, bool x_bf16, bool h_bf16, hipStream_t stream) {
+bsf8_status launch_quant_norm(const NormDev& args, bool x_bf16, bool h_bf16, hipStream_t stream) {
+  NormDev a = args;
   const int vecs = (a.K + EPL - 1) / EPL;
   Kern kern;
   int threads, rows;
@@ -662,8 +663,14 @@ bsf8_status launch_quant_norm(const NormDev& a, bool x_bf16, bool h_bf16, hipStr
     rows = 1;
     kern = vecs <= 1024 ? pick<256, 4>(x_bf16, h_bf16) : pick<1024, 4>(x_bf16, h_bf16);
   }
-  hipLaunchKernelGGL(kern, dim3(unsigned((int64_t(a.M) + rows - 1) / rows)), dim3(threads), 0, stream, a);
-  return device_status(hipGetLastError(), "quant_norm launch");
+  // a launch holds fewer than 2^32 threads, so rows go out by 2^22 blocks (four rows each in the short rows' kernel)
+  bsf8_status st = BSF8_OK;
+  for (int64_t step = (int64_t(1) << 22) * rows - rows; a.m0 < a.M && st == BSF8_OK; a.m0 += step) {
+    const int64_t here = a.M - a.m0 < step ? a.M - a.m0 : step;
+    hipLaunchKernelGGL(kern, dim3(unsigned((here + rows - 1) / rows)), dim3(threads), 0, stream, a);
+    st = device_status(hipGetLastError(), "quant_norm launch");
+  }
+  return st;
 }
 
 }  // namespace bsf8

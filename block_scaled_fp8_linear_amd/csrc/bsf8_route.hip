@@ -64,7 +64,7 @@ __global__ __launch_bounds__(THREADS) void expert_plan_kernel(PlanArgs a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const T* ids = static_cast<const T*>(a.ids);
   // a wave's part: whole steps; only the choices' last step can be short
-  const int steps_all = (a.n + STEP - 1) / STEP, part = (steps_all + WAVES - 1) / WAVES;
+  const int steps_all = a.n / STEP + (a.n % STEP != 0), part = (steps_all + WAVES - 1) / WAVES;
   const int s_begin = min(steps_all, wave * part), s_end = min(steps_all, s_begin + part);
   const int s_full = min(s_end, a.n / STEP);
   const bool has_short = s_begin <= a.n / STEP && a.n / STEP < s_end;

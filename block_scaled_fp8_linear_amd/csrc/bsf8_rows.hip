@@ -9,18 +9,24 @@
 // codes: 5.1e-5 of the result's norm, up to 2^-12 of the sum of magnitudes,
 // against 7.7e-8 and 2^-22), and here, where the weight's bytes set the time,
 // twice the matrix instructions cost nothing.
-// Nothing goes through LDS on the way in: a lane's 32 bytes of a K block are two
-// 16-byte loads straight into the registers that are decoded.  The sum over K
-// does not care which K a register holds so long as both operands agree, so lane
-// group g takes bytes [16 g, 16 g + 16) of each half of the block instead of [32
-// g, 32 g + 32): four lanes then read 64 contiguous bytes per instruction.  The
-// weight is what there is to read, and every byte of it is read once per 16 TJ
-// rows of codes.
 //
-// A block takes 16 RT weight rows and up to 16 TJ rows of codes; its eight waves
-// take K blocks wave, wave + 8, ... (neighbouring waves read neighbouring 128
-// bytes of a row) with D blocks in flight each, and their partial tiles are
-// added through LDS in wave order, so results do not depend on timing.
+// A block takes 16 RT weight rows and up to 16 TJ rows of codes; its waves take K
+// blocks wave, wave + WAVES, ..., each on its own, and their partial tiles are
+// added through LDS in wave order, so results do not depend on timing.  Eight
+// lanes load one row's 128 bytes of a K block: what bounds the kernel is the
+// weight's bytes, and the memory system streams whole 128-byte lines of few rows
+// faster than the fragments' own layout (16 bytes of each of 16 rows, four lanes
+// to 64 bytes).  The rows pass through the wave's own part of LDS into the
+// fragments' layout, without a barrier; the next K block's loads go out as soon
+// as the registers of this one are in LDS, before its arithmetic.  Sixteen waves
+// of a compute unit then have 96 KiB in flight (up to 16 rows of codes; 114 registers).
+//
+// W [5120, 5120] with bias and residual takes 7.8 / 9.7 / 16.3 / 17.6 us at 1 / 16 / 48
+// / 64 tokens (26 MB: 3.4 TB/s at one token, launch and ramp included; fragments
+// loaded straight into registers took 11.4 us); 8 of 64 experts [1536, 2048] at one
+// token 9.3 us.  Four waves where K has at most 16 blocks, eight beyond: 4 tokens
+// of 8 of 64 experts at K = 2048 12.4 against 17.2 us, [5120, 17408] at one token 28.7
+// against 18.7 us.
 //
 // Experts: the row runs lie in device memory, so every wave finds the (expert,
 // run of 16 TJ rows) of its block itself: 64 experts' runs are counted at a time
@@ -135,11 +141,10 @@ __device__ __forceinline__ int at_piece(int row, int p) {
 }
 
 // One block's tile: 16 RT weight rows from n0 of member `mem`, rows [first, end)
-// of codes, which fill TJ column tiles.  Straight-line inside a round of D K
-// blocks per wave: with a branch between loads the compiler waits for all of
-// them where it could wait for the oldest, so a round always runs D blocks, and
-// one past the last repeats the last with scale zero.
-template <int WAVES, int RT, int TJ, int D, Access ACCESS, bool KFULL, bool SBF16>
+// of codes, which fill TJ column tiles.  No branch around a load: the compiler
+// would wait for all of them there.  The loads issued in the last round repeat
+// the last K block and are not used.
+template <int WAVES, int RT, int TJ, Access ACCESS, bool KFULL, bool SBF16>
 __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, int expert, int n0, int first, int end,
                                      uint8_t* lds) {
   constexpr int THREADS = WAVES * 64;
@@ -196,8 +201,8 @@ __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, in
   }
   __builtin_amdgcn_sched_barrier(0);
 
-  uint4 wr[D][2 * RT], xr[D][2 * TJ];
-  float sa[D][TJ];
+  uint4 wr[2 * RT], xr[2 * TJ];
+  float sa[TJ];
   // The weight scales of the wave's K blocks, one per lane: block wave + WAVES
   // (64 h + lane) for h-th 64 rounds.
   uint32_t swr = 0;
@@ -207,68 +212,61 @@ __device__ __forceinline__ void tile(const RowsArgs& a, const MemberDev& mem, in
   };
   load_scales(0);
   __builtin_amdgcn_sched_barrier(0);
-  auto issue = [&](int c, int d) __attribute__((always_inline)) {
+  auto issue = [&](int c) __attribute__((always_inline)) {
     const int cc = min(c, Kb - 1);
     const int k = cc * KB + 16 * lp;
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) sa[d][j] = srow[j][int64_t(cc) * a.xs_sk];
+    for (int j = 0; j < TJ; ++j) sa[j] = srow[j][int64_t(cc) * a.xs_sk];
 #pragma unroll
-    for (int q = 0; q < 2 * TJ; ++q) xr[d][q] = load_piece<ACCESS, false>(xrow[q], k, K);
+    for (int q = 0; q < 2 * TJ; ++q) xr[q] = load_piece<ACCESS, false>(xrow[q], k, K);
 #pragma unroll
-    for (int q = 0; q < 2 * RT; ++q) wr[d][q] = load_piece<ACCESS, true>(wrow[q], k, K);
+    for (int q = 0; q < 2 * RT; ++q) wr[q] = load_piece<ACCESS, true>(wrow[q], k, K);
   };
-#pragma unroll
-  for (int d = 0; d < D; ++d) {
-    issue(wave + WAVES * d, d);
-    __builtin_amdgcn_sched_barrier(0);
-  }
+  issue(wave);
+  __builtin_amdgcn_sched_barrier(0);
   int round = 0;
-  for (int c0 = wave; c0 < Kb; c0 += WAVES * D) {
+  for (int c = wave; c < Kb; c += WAVES, ++round) {
+    if (round == 64) {   // (K beyond 65536)
+      load_scales(c / (WAVES * 64));
+      round = 0;
+    }
+    const float sw = widen(__builtin_amdgcn_readlane(swr, round), SBF16);
+    // bytes past K: zeros on both sides (a NaN code times zero is NaN)
+    if (!KFULL && ACCESS != kBytes && c == Kb - 1) {
+      const int k = c * KB + 16 * lp;
 #pragma unroll
-    for (int d = 0; d < D; ++d, ++round) {
-      const int c = c0 + WAVES * d;
-      if (round == 64) {   // (K beyond 65536)
-        load_scales(c / (WAVES * 64));
-        round = 0;
-      }
-      const float sw = c < Kb ? widen(__builtin_amdgcn_readlane(swr, round), SBF16) : 0.f;
-      // bytes past K: zeros on both sides (a NaN code times zero is NaN)
-      if (!KFULL && ACCESS != kBytes && c >= Kb - 1) {
-        const int k = (Kb - 1) * KB + 16 * lp;
+      for (int q = 0; q < 2 * RT; ++q) clip<ACCESS>(wr[q], k, K);
 #pragma unroll
-        for (int q = 0; q < 2 * RT; ++q) clip<ACCESS>(wr[d][q], k, K);
+      for (int q = 0; q < 2 * TJ; ++q) clip<ACCESS>(xr[q], k, K);
+    }
 #pragma unroll
-        for (int q = 0; q < 2 * TJ; ++q) clip<ACCESS>(xr[d][q], k, K);
-      }
+    for (int q = 0; q < 2 * RT; ++q) *reinterpret_cast<uint4*>(wl + at_piece(8 * q + lr, lp)) = wr[q];
 #pragma unroll
-      for (int q = 0; q < 2 * RT; ++q) *reinterpret_cast<uint4*>(wl + at_piece(8 * q + lr, lp)) = wr[d][q];
+    for (int q = 0; q < 2 * TJ; ++q) *reinterpret_cast<uint4*>(xl + at_piece(8 * q + lr, lp)) = xr[q];
+    float s[TJ];
 #pragma unroll
-      for (int q = 0; q < 2 * TJ; ++q) *reinterpret_cast<uint4*>(xl + at_piece(8 * q + lr, lp)) = xr[d][q];
-      float s[TJ];
+    for (int j = 0; j < TJ; ++j) s[j] = sa[j] * sw;
+    // the registers are free: the next loads go out before this block's arithmetic
+    __builtin_amdgcn_sched_barrier(0);
+    issue(c + WAVES);
+    __builtin_amdgcn_sched_barrier(0);
+    auto fragment = [&](const uint8_t* base, int row) {
+      const uint4 p[2] = {*reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g)),
+                          *reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g + 1))};
+      return operand(p);
+    };
+    Operand w[RT];
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) s[j] = sa[d][j] * sw;
-      // the slot's registers are free: its next loads go out before this block's arithmetic
-      __builtin_amdgcn_sched_barrier(0);
-      issue(c + WAVES * D, d);
-      __builtin_amdgcn_sched_barrier(0);
-      auto fragment = [&](const uint8_t* base, int row) {
-        const uint4 p[2] = {*reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g)),
-                            *reinterpret_cast<const uint4*>(base + at_piece(row, 2 * g + 1))};
-        return operand(p);
-      };
-      Operand w[RT];
+    for (int i = 0; i < RT; ++i) w[i] = fragment(wl, 16 * i + l16);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) w[i] = fragment(wl, 16 * i + l16);
+    for (int j = 0; j < TJ; ++j) {
+      const Operand x = fragment(xl, 16 * j + l16);
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const Operand x = fragment(xl, 16 * j + l16);
+      for (int i = 0; i < RT; ++i) {
+        v4f p = v4f{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          v4f p = v4f{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].s[q], x.s[q], p, 0, 0, 0);
-          acc[i][j] += p * s[j];
-        }
+        for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[i].s[q], x.s[q], p, 0, 0, 0);
+        acc[i][j] += p * s[j];
       }
     }
   }
@@ -326,11 +324,11 @@ __global__ __launch_bounds__(WAVES * 64) void w8a8_rows_kernel(RowsArgs a) {
   const int n0 = (R_tile - a.rt0[mi]) * 16 * RT;
   const int tiles = (end - first + 15) / 16;
   if (TJ == 1 || tiles == 1)
-    tile<WAVES, RT, 1, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
   else if (TJ == 2 || tiles == 2)
-    tile<WAVES, RT, TJ < 2 ? TJ : 2, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, TJ < 2 ? TJ : 2, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
   else
-    tile<WAVES, RT, TJ, 1, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
+    tile<WAVES, RT, TJ, ACCESS, KFULL, SBF16>(a, mem, expert, n0, first, end, lds);
 }
 
 template <int WAVES, int RT, int TJ, bool SBF16>
@@ -354,7 +352,7 @@ bsf8_status launch(const RowsArgs& base, bool aligned, int64_t items, hipStream_
   }
   a.rt0[kMaxMembers] = r;
   const int64_t grid = items * r;
-  if (grid > INT32_MAX) {
+  if (grid * WAVES * 64 > UINT32_MAX) {
     set_error("UNSUPPORTED: %lld blocks", (long long)grid);
     return BSF8_E_UNSUPPORTED;
   }

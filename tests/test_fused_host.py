@@ -156,3 +156,37 @@ def test_binding_refuses_host_tensors():
         B.quant_norm(x, w)
     with pytest.raises(ValueError, match="GPU tensor"):
         B.expert_plan(torch.zeros((4, 2), dtype=torch.int32), 4)
+
+
+def test_sizes_beyond_one_launch_and_workspaces():
+    """Refused before any launch: more blocks than a launch holds, a workspace that is missing or too small."""
+    L = B.lib()
+    ok, h = _experts([_member(K=24)])
+    assert ok == "OK"
+    try:
+        assert name(L.bsf8_linear_w8a8_experts(h, FAKE, 24, FAKE, 1, 1, 2 ** 30 - 1, FAKE, FAKE, 2 ** 30 - 1, FAKE,
+                                               B.DT_F32, 300, None)) == "UNSUPPORTED"
+    finally:
+        L.bsf8_experts_destroy(h)
+
+    def weight(N, K):
+        arr, keep = B._members_array([{k: dict(d, shape=d["shape"][1:]) for k, d in _member(E=1, N=N, K=K).items()}])
+        w = ctypes.c_void_p()
+        assert L.bsf8_weight_create(ctypes.byref(B._decl("fp8", (128, 128))), arr, 1, ctypes.byref(w)) == 0
+        return w
+
+    def call(w, M, K, N, ws, nbytes):
+        return name(L.bsf8_linear_w8a8_epilogue(w, FAKE, K, FAKE, -(-K // 128), 1, M, ctypes.byref(B.Epilogue()), FAKE,
+                                                B.DT_F32, N, ws, nbytes, None))
+
+    w = weight(300, 24)
+    assert call(w, 2 ** 30 - 1, 24, 300, None, 0) == "UNSUPPORTED"
+    L.bsf8_weight_destroy(w)
+    w = weight(640, 4096)
+    need = ctypes.c_size_t()
+    assert L.bsf8_workspace_size(w, B.ARM_W8A8_EPILOGUE, 200, ctypes.byref(need)) == 0 and need.value > 0
+    assert call(w, 200, 4096, 640, None, 0) == "WORKSPACE"
+    assert call(w, 200, 4096, 640, FAKE, need.value - 1) == "WORKSPACE"
+    assert call(w, 200, 4096, 640, FAKE + 128, need.value) == "ALIGNMENT"
+    assert L.bsf8_workspace_size(w, B.ARM_W8A8_EPILOGUE, 64, ctypes.byref(need)) == 0 and need.value == 0
+    L.bsf8_weight_destroy(w)
