@@ -27,6 +27,7 @@ __device__ __forceinline__ v8bf decode8(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ float times_sigmoid(float v, float u) {   // v / (1 + exp(-u))
   return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.4426950408889634f));
 }
+__device__ __forceinline__ float relu(float v) { return v < 0.f ? 0.f : v; }   // (NaN stays NaN)
 __device__ __forceinline__ float silu(float v) { return times_sigmoid(v, v); }
 __device__ __forceinline__ float gelu_tanh(float v) {   // u = 2 sqrt(2 / pi) (v + 0.044715 v^3)
   return times_sigmoid(v, v * fmaf(v * v, 0.071354816272600248f, 1.5957691216057308f));
@@ -47,7 +48,7 @@ __device__ __forceinline__ float gelu(float v) {
 }
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
-    case BSF8_ACT_RELU: return fmaxf(v, 0.f);
+    case BSF8_ACT_RELU: return relu(v);
     case BSF8_ACT_SILU: return silu(v);
     case BSF8_ACT_GELU: return gelu(v);
     case BSF8_ACT_GELU_TANH: return gelu_tanh(v);
@@ -68,7 +69,7 @@ __device__ __forceinline__ void by_fours(float (&v)[N], F f) {
 }
 template <int N>
 __device__ __forceinline__ void activate_all(float (&v)[N], int act) {
-  if (act == BSF8_ACT_RELU) by_fours(v, [](float x) { return fmaxf(x, 0.f); });
+  if (act == BSF8_ACT_RELU) by_fours(v, relu);
   else if (act == BSF8_ACT_SILU) by_fours(v, silu);
   else if (act == BSF8_ACT_GELU) by_fours(v, gelu);
   else if (act == BSF8_ACT_GELU_TANH) by_fours(v, gelu_tanh);

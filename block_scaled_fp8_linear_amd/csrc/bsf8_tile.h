@@ -574,7 +574,10 @@ __global__ __launch_bounds__(FTHREADS, tile_waves(T, MODE, EXACT)) void w8a8_gem
   const uint32_t b_lane = uint32_t(b_row0) * uint32_t(a.ldq);
   // Experts: a row's token is looked up once; the rows of a copying lane's slabs
   // keep their byte offsets.  A row past the run or without a token reads zeros.
+  // Bit l of token_ok: row l of the wave's WM has a token (the others are zeros at
+  // the store: a zero code times a NaN code or scale of the weight is NaN).
   uint32_t b_row_off[EXPERTS ? F_B_LOADS : 1];
+  uint64_t token_ok = ~uint64_t(0);
   if constexpr (EXPERTS) {
     auto token = [&](int r) {
       const int tok = r < m_end ? (a.rows ? a.rows[r] : r) : -1;
@@ -587,6 +590,9 @@ __global__ __launch_bounds__(FTHREADS, tile_waves(T, MODE, EXACT)) void w8a8_gem
         b_row_off[i] = tok >= 0 ? uint32_t(tok) * uint32_t(a.ldq) : b_bytes;
       }
     }
+    static_assert(WM <= 64, "a wave's rows fit a ballot");
+    const int r_lane = m0 + wm * WM + lane;
+    token_ok = __ballot(lane >= WM || r_lane >= m_end || token(r_lane) >= 0);
     if (s_wave) {
       const int tok = token(s_tok);
       s_ok = tok >= 0;
@@ -807,6 +813,18 @@ __global__ __launch_bounds__(FTHREADS, tile_waves(T, MODE, EXACT)) void w8a8_gem
       step(kb, stage0, stage1, bf, af, copy_tag);
       if (kb + 1 < kb_end) step(kb + 1, stage1, stage0, bf, af, copy_tag);
     }
+
+    if constexpr (EXPERTS)
+      if (token_ok != ~uint64_t(0)) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+          const bool ok = token_ok >> (16 * j + l16) & 1;
+#pragma unroll
+          for (int i = 0; i < TI; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = ok ? acc[i][j][e] : 0.f;
+        }
+      }
 
     // ---- store
     if (MODE == kEpilogue || !whole || a.y_vec) {   // (an epilogue's stores test their own alignment)

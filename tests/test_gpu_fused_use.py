@@ -172,3 +172,57 @@ def test_offsets_of_many_experts_that_descend():
         B.linear_w8a8_experts(w, xq, xs, off, out_dtype=dt, out=buf[10:10 + R])
         t.cuda.synchronize()
         assert bool((buf[:10] == 5.0).all()) and bool((buf[10 + R:] == 5.0).all())
+
+
+@pytest.mark.parametrize("M", [1, 20, 64, 130, 300])
+@pytest.mark.parametrize("act", [None, "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_nan_codes_reach_their_outputs_only(M, act, out):
+    """A NaN code of a weight row makes that column NaN, one of a token that row, whatever the activation."""
+    t = torch()
+    N, K = 260, 2048
+    m = synth.random_code_weight(822, "nan_w", N, K)
+    codes, scales = member_to_device(m)
+    codes = codes.clone()
+    codes[137, 300] = 0x7F
+    codes[259, K - 1] = 0xFF
+    w = B.BlockFP8Weight([(codes, scales)])
+    xq, xs = B.quant_act(t.randn(M, K, device=device()))
+    banner(f"NaN codes M={M} {act} {out}")
+    dt = t.bfloat16 if out == "bf16" else t.float32
+    args = dict(bias=t.randn(N, device=device()), activation=act, residual=t.randn(M, N, device=device()), out_dtype=dt)
+    want = t.zeros((M, N), dtype=t.bool, device=device())
+    want[:, [137, 259]] = True
+    assert t.equal(B.linear_w8a8_epilogue(w, xq, xs, **args).isnan(), want)
+    xq[M // 2, 5] = 0xFF
+    want[M // 2] = True
+    assert t.equal(B.linear_w8a8_epilogue(w, xq, xs, **args).isnan(), want)
+
+
+@pytest.mark.parametrize("counts", [(1, 0, 2), (3, 20, 40), (200, 0, 300), (1500, 1500, 1500)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_nan_codes_by_expert(counts, out):
+    """NaN codes of one expert's weight row and of token 0, which every fifth row gathers; rows without a token are
+    zero all the same."""
+    t = torch()
+    E, N, K = len(counts), 260, 1024
+    g = t.Generator(device=device())
+    g.manual_seed(6)
+    w = t.randint(0, 0x70, (E, N, K), dtype=t.uint8, device=device(), generator=g)
+    w[2, 100, 1000] = 0x7F
+    we = B.ExpertsFP8Weight([(w, t.full((E, 3, 8), 0.01, device=device()))])
+    R, M = sum(counts), 50
+    xq, xs = B.quant_act(t.randn((M, K), device=device(), generator=g))
+    xq[0] = 0xFF
+    rows = t.randint(1, M, (R,), device=device(), generator=g, dtype=t.int32)
+    rows[::5] = 0
+    rows[1::7] = -1
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    banner(f"NaN codes by expert {counts} {out}: {we.describe(R)}")
+    dt = t.bfloat16 if out == "bf16" else t.float32
+    y = B.linear_w8a8_experts(we, xq, xs, t.from_numpy(off).to(device()), rows=rows, out_dtype=dt)
+    want = (rows == 0)[:, None].repeat(1, N)
+    want[off[2]:, 100] = True
+    want &= (rows >= 0)[:, None]
+    assert t.equal(y.isnan(), want)
+    assert bool((y[rows < 0] == 0).all())
