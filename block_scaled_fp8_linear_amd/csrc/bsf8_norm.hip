@@ -346,8 +346,8 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
 // close to the time of the memory traffic, so the two must overlap, and waves
 // in flight are what overlaps them: the test-free form at 128 registers (four
 // waves per SIMD) takes [8192, 7168] BF16 with residual, post norm and gate in
-// 118 us and with the residual alone in 87 us (410 MB; a copy of as much takes
-// 84 us), [8192, 5120] in 78 and 58 us.  Tried and slower: the general kernel
+// 115 us and with the residual alone in 85 us (410 MB; a copy of as much takes
+// 84 us), [8192, 5120] in 80 and 58 us.  Tried and slower: the general kernel
 // above for these rows (205 us; two waves per SIMD and a branch around every
 // load), blocks that stay and prefetch their next row (175 us; the registers of
 // the second row halve the waves), two rows per block sharing the weights'
@@ -356,16 +356,21 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
 // rsqrt64().  One row takes 3.5 us.
 // ---------------------------------------------------------------------------
 
-template <bool BF16>
+// NT: non-temporal, for rows that are read once and then dead (the block's output and the old stream): they leave the
+// caches to what the next call reads (rows from memory, [1024, 5120] 16.2 -> 14.2 us, [8192, 7168] 117.4 -> 115 us).  The
+// new stream is stored as usual: the next step reads it.  Experts' rows are loaded as usual too: behind the product that
+// wrote them both forms take 18.4 us (1024 tokens, 8 rows of 4096 each), from the cache 17.8 against 19.0 us.
+template <bool BF16, bool NT = false>
 __device__ __forceinline__ void load_wide(const void* p, int64_t off, Raw<BF16>& r) {
-  const uint4* q = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + off * (BF16 ? 2 : 4));
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  const u4* q = reinterpret_cast<const u4*>(static_cast<const uint8_t*>(p) + off * (BF16 ? 2 : 4));
 #pragma unroll
   for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
-    const uint4 u = q[i];
-    r.w[4 * i] = u.x;
-    r.w[4 * i + 1] = u.y;
-    r.w[4 * i + 2] = u.z;
-    r.w[4 * i + 3] = u.w;
+    const u4 u = NT ? __builtin_nontemporal_load(q + i) : q[i];
+    r.w[4 * i] = u[0];
+    r.w[4 * i + 1] = u[1];
+    r.w[4 * i + 2] = u[2];
+    r.w[4 * i + 3] = u[3];
   }
 }
 
@@ -474,10 +479,10 @@ __global__ __launch_bounds__(V == 1 ? 128 : 1024) void quant_norm_wide_kernel(No
   if constexpr (!COMBINE) {
     Raw<XBF16> x[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) load_wide<XBF16>(a.x, m * a.ldx + k[i], x[i]);
+    for (int i = 0; i < V; ++i) load_wide<XBF16, true>(a.x, m * a.ldx + k[i], x[i]);
     if (a.res != nullptr) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) load_wide<HBF16>(a.res, m * a.ldr + k[i], res[i]);
+      for (int i = 0; i < V; ++i) load_wide<HBF16, true>(a.res, m * a.ldr + k[i], res[i]);
     }
     if (!on) clear(x[V - 1]);
 #pragma unroll
@@ -487,7 +492,7 @@ __global__ __launch_bounds__(V == 1 ? 128 : 1024) void quant_norm_wide_kernel(No
   } else {
     if (a.res != nullptr) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) load_wide<HBF16>(a.res, m * a.ldr + k[i], res[i]);
+      for (int i = 0; i < V; ++i) load_wide<HBF16, true>(a.res, m * a.ldr + k[i], res[i]);
     }
 #pragma unroll
     for (int i = 0; i < V; ++i)
