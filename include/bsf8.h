@@ -351,8 +351,8 @@ bsf8_status bsf8_quant_norm(const bsf8_norm_args* args, void* stream);
  * rows    [M * top] : the token of each row, by expert and within an expert in
  *       the order of ids; entries from offsets[n_experts] on keep what they hold.
  * slots   [M, top] : the row of each choice, -1 for one without an expert.
- * One launch, no workspace; the result does not depend on timing.  M == 0
- * writes the offsets, all zero.
+ * One launch, no workspace; the result does not depend on timing.  No output may
+ * overlap ids or another output.  M == 0 writes the offsets, all zero.
  * Errors: INVALID_ARG, ALIGNMENT (ids not element aligned, an output not 4-byte
  * aligned), UNSUPPORTED (M * top > 2^31 - 1, n_experts > 65535), DEVICE.
  */
@@ -488,6 +488,7 @@ bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, i
  * rows    : device int32 [R], the token of each row, or NULL (then M >= R is
  *           needed); a row whose token is outside [0, M) is written as zeros.
  * y       : [R, N] BF16 or F32; rows outside every expert's run keep what they hold.
+ *           It may not overlap an input.
  * The host learns nothing about the runs, so a call can be captured into a graph
  * and replayed with other offsets; R bounds them.  No workspace.  R == 0 is a
  * no-op.

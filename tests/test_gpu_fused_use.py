@@ -226,3 +226,43 @@ def test_nan_codes_by_expert(counts, out):
     want &= (rows >= 0)[:, None]
     assert t.equal(y.isnan(), want)
     assert bool((y[rows < 0] == 0).all())
+
+
+@pytest.mark.parametrize("K", [40, 129, 1024, 2047, 5120, 12000, 16400, 20001])
+@pytest.mark.parametrize("kind", ["rms", "layer"])
+def test_norm_in_place(K, kind):
+    """The new stream written over the old one, or over the block's output: the bits of the call that does not."""
+    t = torch()
+    M = 37
+    x = t.randn(M, K, device=device()).bfloat16()
+    r = t.randn(M, K + 8, device=device()).bfloat16()[:, :K]
+    weight, post = t.rand(K, device=device()) + 0.5, t.rand(K, device=device()) + 0.5
+    banner(f"quant_norm in place K={K} {kind}")
+    call = lambda **kw: B.quant_norm(kw.pop("x", x), weight, kind=kind, post_weight=post, **kw)
+    q, s, h, _ = call(residual=r)
+    old = r.clone()
+    pitched = t.zeros((M, K + 8), dtype=t.bfloat16, device=device())[:, :K]
+    pitched.copy_(old)
+    got = call(residual=pitched, h=pitched)
+    assert got[2].data_ptr() == pitched.data_ptr()
+    assert t.equal(got[0], q) and t.equal(got[1], s) and t.equal(pitched, h)
+    over = x.clone()
+    got = call(x=over, residual=r, h=over)
+    assert t.equal(got[0], q) and t.equal(got[1], s) and t.equal(over, h) and t.equal(r, old)
+
+
+@pytest.mark.parametrize("K", [5, 100, 1024, 5120, 20000])
+def test_norm_of_constant_rows(K):
+    """Rows of zeros and of one value: a norm of exactly zero (layer norm, zeros) gives codes zero and the floor's scale."""
+    t = torch()
+    banner(f"quant_norm constant rows K={K}")
+    for value in (0.0, 3.0, -2.0 ** -100):
+        x = t.full((3, K), value, device=device())
+        for kind in ("rms", "layer"):
+            q, s, _, n = B.quant_norm(x, t.ones(K, device=device()), kind=kind, out_dtype=t.float32)
+            want = 0.0 if kind == "layer" else value / (value * value + 1e-6) ** 0.5
+            # the layer norm's mean of K equal values is off by at most K roundings, times 1 / sqrt(eps)
+            tol = 2.0 ** -24 * abs(want) + (K * 2.0 ** -53 * abs(value) * 1000 if kind == "layer" else 0.0) + 2.0 ** -149
+            assert bool(((n.double() - want).abs() <= tol).all())
+            yq, ys = O.quant_act(n.cpu().numpy())
+            assert np.array_equal(q.cpu().numpy(), yq) and np.array_equal(s.cpu().numpy(), ys)
