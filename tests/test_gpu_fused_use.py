@@ -8,6 +8,7 @@ import oracle as O
 import synth
 from fused_util import expect
 from gpu_util import banner, device, member_to_device, oracle_members, to_np, torch
+from test_gpu_route import plan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -266,3 +267,16 @@ def test_norm_of_constant_rows(K):
             assert bool(((n.double() - want).abs() <= tol).all())
             yq, ys = O.quant_act(n.cpu().numpy())
             assert np.array_equal(q.cpu().numpy(), yq) and np.array_equal(s.cpu().numpy(), ys)
+
+
+@pytest.mark.parametrize("top", [1, 2, 3, 5, 6, 7, 9, 10, 12, 17, 33, 100, 1000, 65537, 1 << 20, (1 << 20) + 1])
+def test_plan_divides_by_any_top(top):
+    t = torch()
+    M = max(2, 3_000_000 // top)
+    banner(f"expert_plan M={M} top={top}")
+    g = np.random.default_rng(top)
+    ids = g.integers(-1, 5, (M, top)).astype(np.int32)
+    off, rows, slots = B.expert_plan(t.from_numpy(ids).to(device()), 5)
+    ro, rr, rs = plan_ref(ids, 5)
+    assert np.array_equal(off.cpu().numpy(), ro) and np.array_equal(slots.cpu().numpy(), rs)
+    assert np.array_equal(rows.cpu().numpy()[:ro[-1]], rr[:ro[-1]])
