@@ -40,17 +40,22 @@ bsf8_status launch_w8a8_epilogue(const WeightDev& w, bool aligned, const uint8_t
                 : launch_fast<kEpilogue, true>(p, w, xq, ldq, xs, xs_sm, xs_sk, M, y, y_bf16, ldy, ws, ws_bytes, stream, &ep);
 }
 
+// (Both output types' plans, for tokens packed at a pitch of K.)
 std::string describe_w8a8_epilogue(const WeightDev& w, bool aligned, int64_t M) {
-  const Plan p = plan_of(w, aligned, M, w.K, -1, true);
   char m[64];
   snprintf(m, sizeof(m), " | M=%lld", (long long)M);
-  if (by_rows(p, M)) return "arm=w8a8-epilogue " + describe_w8a8_rows(M <= 16, aligned) + m;
-  char buf[320];
-  snprintf(buf, sizeof(buf),
-           "arm=w8a8-epilogue arithmetic=bf16 outputs e4m3xe4m3 mfma_f32_16x16x128_f8f6f4, f32 outputs codes decoded "
-           "exactly to bf16, f32 per-128-K epilogue | kernel=w8a8_gemm_fast tile=%dx%d (f32 outputs 128x128) split_k=%d",
-           p.tile, p.tile, p.splits);
-  return std::string(buf) + m;
+  if (by_rows(plan_of(w, aligned, M, w.K, -1, true), M)) return "arm=w8a8-epilogue " + describe_w8a8_rows(M <= 16, aligned) + m;
+  std::string out = "arm=w8a8-epilogue";
+  for (const bool bf16 : {true, false}) {
+    const Plan p = plan_of(w, aligned, M, w.K, -1, bf16);
+    char buf[320];
+    snprintf(buf, sizeof(buf),
+             "arithmetic=%s, f32 per-128-K epilogue | kernel=w8a8_gemm_fast tile=%dx%d split_k=%d split_row_tiles=%d",
+             bf16 ? "e4m3xe4m3 mfma_f32_16x16x128_f8f6f4" : "e4m3 codes decoded exactly to bf16, mfma_f32_16x16x32_bf16",
+             p.tile, p.tile, p.splits, p.rt_total - p.rt_split0);
+    out += std::string(bf16 ? " | bf16 outputs: " : " | f32 outputs: ") + buf;
+  }
+  return out + m;
 }
 
 }  // namespace bsf8

@@ -91,6 +91,7 @@ bsf8_status launch_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, con
   return device_status(hipGetLastError(), "w8a8_experts launch");
 }
 
+// (For packed tokens whose codes and scales stay below 2 GiB: farther ones take the few-row kernel.)
 std::string describe_w8a8_experts(const WeightDev& w, int64_t E, bool aligned, int64_t R) {
   char n[64];
   snprintf(n, sizeof(n), " | R=%lld", (long long)R);
