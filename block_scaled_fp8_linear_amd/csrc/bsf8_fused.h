@@ -44,7 +44,8 @@ __device__ __forceinline__ float gelu(float v) {
   p = fmaf(t, p, -0.284496736f);
   p = fmaf(t, p, 0.254829592f);
   const float tail = 0.5f * v * t * p * __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
-  return v >= 0.f ? v - tail : tail;
+  // (at +inf the tail is inf * 0: the smaller of v - NaN and v is v)
+  return v >= 0.f ? fminf(v - tail, v) : tail;
 }
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {

@@ -435,7 +435,8 @@ bsf8_status bsf8_linear_w8a8(const bsf8_weight* w, const uint8_t* xq, int64_t ld
  * e->bias     : [N] F32 or BF16, or NULL.
  * e->activation : bsf8_activation: none, relu, silu = v / (1 + exp(-v)), gelu =
  *               v * Phi(v), gelu_tanh (its usual approximation
- *               v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))).
+ *               v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))).  At +inf all of
+ *               them are +inf; at -inf relu is 0, silu and the gelus are NaN (-inf * 0).
  * e->residual : [M, N] F32 or BF16, leading dimension ldr, or NULL.  It may be y
  *               itself (same address, pitch and type); no other overlap.
  * workspace   : bsf8_workspace_size with arm W8A8_EPILOGUE.
