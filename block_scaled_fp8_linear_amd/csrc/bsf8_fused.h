@@ -32,18 +32,26 @@ __device__ __forceinline__ float silu(float v) { return times_sigmoid(v, v); }
 __device__ __forceinline__ float gelu_tanh(float v) {   // u = 2 sqrt(2 / pi) (v + 0.044715 v^3)
   return times_sigmoid(v, v * fmaf(v * v, 0.071354816272600248f, 1.5957691216057308f));
 }
-// v Phi(v) with Phi(-|v|) = erfc(x) / 2, x = |v| / sqrt(2), by the rational
-// approximation 7.1.26 of Abramowitz and Stegun, "Handbook of Mathematical
-// Functions" (error below 1.5e-7, and shrinking with exp(-x^2) where the result
-// does): at most 1.3 * 2^-24 |v| of the result.
+// v Phi(v) with the tail |v| Phi(-|v|) = |v| / 2 * erfc(|v| / sqrt(2)), and
+// erfc(|v| / sqrt(2)) = exp(-v^2 / 2) t P(t - 1/2), t = 1 / (1 + 0.35 |v|).  P is a
+// polynomial of degree eight, fitted to the least relative error over 0 <= |v| <= 14
+// (2^-24.9; the result is below 2^-126 beyond).  The error is relative to the tail, so
+// it shrinks with the result where v is negative: below (19 + 1.25 v^2) 2^-24 of it,
+// v^2 from the roundings of the exponent, 9 from those of t (the tail's slope in t is
+// 2.3 at 0), the rest from the polynomial and the products.  (A form with an absolute
+// bound on erfc was wrong by 1e-2 of the result at -7, three bits of a BF16 output.)
 __device__ __forceinline__ float gelu(float v) {
-  const float x = fabsf(v) * 0.70710678118654752f;
-  const float t = __builtin_amdgcn_rcpf(fmaf(x, 0.3275911f, 1.f));
-  float p = fmaf(t, 1.061405429f, -1.453152027f);
-  p = fmaf(t, p, 1.421413741f);
-  p = fmaf(t, p, -0.284496736f);
-  p = fmaf(t, p, 0.254829592f);
-  const float tail = 0.5f * v * t * p * __builtin_amdgcn_exp2f(x * x * -1.4426950408889634f);
+  const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(v), 0.35f, 1.f));
+  const float s = t - 0.5f;
+  float p = fmaf(s, -0.0582918764f, 0.0547759776f);
+  p = fmaf(s, p, 0.0883303399f);
+  p = fmaf(s, p, -0.112277419f);
+  p = fmaf(s, p, -0.163480295f);
+  p = fmaf(s, p, 0.16374165f);
+  p = fmaf(s, p, 0.568791597f);
+  p = fmaf(s, p, 0.685983216f);
+  p = fmaf(s, p, 0.506488546f);
+  const float tail = 0.5f * v * t * p * __builtin_amdgcn_exp2f(v * v * -0.72134752044448170f);
   // (at +inf the tail is inf * 0: the smaller of v - NaN and v is v)
   return v >= 0.f ? fminf(v - tail, v) : tail;
 }

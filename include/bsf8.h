@@ -437,6 +437,9 @@ bsf8_status bsf8_linear_w8a8(const bsf8_weight* w, const uint8_t* xq, int64_t ld
  *               v * Phi(v), gelu_tanh (its usual approximation
  *               v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3)))).  At +inf all of
  *               them are +inf; at -inf relu is 0, silu and the gelus are NaN (-inf * 0).
+ *               Evaluated in F32, off by at most, relative to the value, (6 + 1.5 |v|)
+ *               2^-24 (silu), (19 + 1.25 v^2) 2^-24 (gelu), (6 + 5.5 u) 2^-24 with u = 1.6
+ *               (|v| + 0.045 |v|^3) (gelu_tanh); values below 2^-118 may be zero.
  * e->residual : [M, N] F32 or BF16, leading dimension ldr, or NULL.  It may be y
  *               itself (same address, pitch and type); no other overlap.
  * workspace   : bsf8_workspace_size with arm W8A8_EPILOGUE.

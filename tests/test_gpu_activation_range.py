@@ -51,3 +51,38 @@ def test_infinities_and_huge_values(M, N, K, out, act):
     ok = ~np.isnan(want) & np.isfinite(want)
     assert np.array_equal(y[np.isinf(want)], want[np.isinf(want)])
     assert np.all(np.abs(y[ok] - want[ok]) <= (2.0 ** -8 if out == BF16 else 2.0 ** -24) * np.abs(want[ok]))
+
+
+# How far an output may be off, relative to itself, in units of 2^-24.  The hardware's exp2 and reciprocal are within one
+# unit in the last place, 2 units of 2^-24 here; every F32 operation adds one.
+#  silu: exp2's argument carries its product's rounding and the constant's, 1.5 |v| 2^-24 of its natural exponent, and
+#  exp2, the sum, the reciprocal and the product add 2 + 1 + 2 + 1.
+#  gelu_tanh: the same with u, |u| <= 2 sqrt(2 / pi) (|v| + 0.045 |v|^3), whose own four roundings and constants make 4 |u|.
+#  gelu: tail = |v| / 2 * t P(t) * exp2(-v^2 / (2 ln 2)).  exp2's argument has the square's and the product's rounding and
+#  the constant's, 2.5 * v^2 / 2; t = 1 / (1 + p |v|) is off by 1 + 2 and acts on t P(t) with a slope below 3 (at v = 0),
+#  the polynomial's own error is below 1, its evaluation below 4, exp2 and the products add 2 + 3.  The result is the
+#  tail where v < 0 and at least as large as it where v >= 0.
+def _units(v, act):
+    a = np.abs(v)
+    if act == "silu":
+        return 6 + 1.5 * a
+    if act == "gelu_tanh":
+        return 6 + 5.5 * 2 * np.sqrt(2 / np.pi) * (a + 0.045 * a ** 3)
+    return 19 + 1.25 * v ** 2
+
+
+@pytest.mark.parametrize("M,N,K,out", [(3, 60000, 128, F32), (130, 60000, 128, F32), (200, 640, 4096, F32),
+                                       (1000, 8200, 512, BF16)])
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+def test_relative_error(M, N, K, out, act):
+    """Outputs far below the argument, where the activation vanishes, are as accurate as those near it."""
+    v = np.concatenate([np.linspace(-13, 13, N // 2), -np.logspace(-12, np.log10(80.0), N // 4), np.logspace(-12, 2, N // 4)])
+    v, y = activate(v, M, N, K, out, act)
+    want = act64(v, act)
+    rel = _units(v, act) * 2.0 ** -24
+    if out == BF16:
+        rel = rel + 2.0 ** -8 * (1 + rel)
+    # exp2 and the reciprocal know no denormals: what is below 2^-118 may be zero
+    err = np.abs(y - want) - 2.0 ** -118
+    bad = ~(err <= rel * np.abs(want))
+    assert not bad.any(), (act, v[bad][:5], y[bad][:5], want[bad][:5])
