@@ -448,6 +448,7 @@ bsf8_status bsf8_linear_dense(const uint16_t* wd, int64_t N, int64_t K, const ui
   if (K % 8 || ldx % 8 || reinterpret_cast<uintptr_t>(wd) % 16 || reinterpret_cast<uintptr_t>(x) % 16)
     return fail(BSF8_E_ALIGNMENT, "dense GEMM needs K and ldx multiples of 8 and 16-byte aligned wd and x");
   if (reinterpret_cast<uintptr_t>(y) % ye) return fail(BSF8_E_ALIGNMENT, "y not element aligned");
+  if (M == 1) ldx = K;   // one row has no pitch
   if (!dense_supported(N, K, M, ldx))
     return fail(BSF8_E_UNSUPPORTED, "dense GEMM shape N=%lld K=%lld M=%lld ldx=%lld (K <= 65536 and operands "
                 "below 2 GiB)", (long long)N, (long long)K, (long long)M, (long long)ldx);

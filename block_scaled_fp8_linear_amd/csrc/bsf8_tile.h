@@ -1035,7 +1035,10 @@ SplitChoice choose_splits(int rt_total, int m_tiles, int Kb, int cus, double ste
 
 // The direct-copy kernel addresses each operand with 32-bit byte offsets from
 // its base, so every member, the activation block and its scales must stay
-// below 2^31 bytes.
+// below 2^31 bytes.  A tile's rows past the last token are read at offsets past
+// the block's end, which the buffer unit answers with zeros; those offsets must
+// not wrap either (few tokens at a pitch of 16 MiB and more), or they would be
+// reads of whatever lies between and behind the rows.
 // (xs_extent: elements spanned by the activation scales; -1: M x Kb.)
 // (exact: the EXACT instances, which exist for 128 x 128 tiles.)
 Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t xs_extent = -1, bool exact = false) {
@@ -1076,7 +1079,8 @@ Plan make_plan(const WeightDev& w, bool aligned, int64_t M, int64_t ldq, int64_t
     p.ldws = int64_t(split_rows) * T;
     p.blocks = p.rt_split0 * p.m_tiles + split_rows * p.m_tiles * p.splits;
     p.ws_bytes = p.splits > 1 ? size_t(p.splits) * size_t(M) * size_t(p.ldws) * sizeof(float) : 0;
-    return p;
+    if ((int64_t(p.m_tiles) * T - 1) * ldq + w.K <= (int64_t(1) << 32)) return p;
+    p = Plan{};
   }
   p.splits = 1;
   p.m_tiles = int((M + BM - 1) / BM);

@@ -593,8 +593,8 @@ const char* bsf8_describe(const bsf8_weight* w, int32_t arm, int64_t M);
  * (row-major, row pitch K: bsf8_upcast's output with ldo = K) and BF16 x [M, K]
  * with row pitch ldx; BF16 x BF16 products accumulated in F32 on the BF16
  * matrix cores; y F32 or BF16 (RNE) [M, ldy].  Needs K and ldx multiples of 8,
- * wd and x 16-byte aligned (ALIGNMENT otherwise), K <= 65536 and each operand
- * below 2 GiB (UNSUPPORTED otherwise).  A workspace of
+ * wd and x 16-byte aligned (ALIGNMENT otherwise), K <= 65536, each operand
+ * below 2 GiB and 128 or 256 rows of x (a tile) below 4 GiB (UNSUPPORTED otherwise).  A workspace of
  * bsf8_dense_workspace_size bytes (256-byte aligned) is needed when the tile
  * grid is split over K, as for the W8A8 arm; M == 0 is a no-op.
  */
