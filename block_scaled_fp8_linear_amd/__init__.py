@@ -369,8 +369,15 @@ class BlockFP8Weight:
         return mi.value, lr.value, sr.value
 
     def workspace_size(self, arm: int, M: int) -> int:
+        """Workspace bytes of a call of M tokens on this weight's device (they go by its compute units)."""
         b = ctypes.c_size_t()
-        _check(lib().bsf8_workspace_size(self._h, arm, M, ctypes.byref(b)), "workspace_size")
+        idx = self.device.index
+        if idx is None or _current()[0]() == idx:
+            st = lib().bsf8_workspace_size(self._h, arm, M, ctypes.byref(b))
+        else:
+            with _torch().cuda.device(idx):
+                st = lib().bsf8_workspace_size(self._h, arm, M, ctypes.byref(b))
+        _check(st, "workspace_size")
         return b.value
 
     def workspace(self, arm: int, M: int):
