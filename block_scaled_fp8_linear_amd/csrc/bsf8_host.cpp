@@ -5,6 +5,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <new>
 #include <string>
 
@@ -12,16 +13,15 @@
 
 namespace bsf8 {
 
-static thread_local std::string g_last_error;
-static thread_local std::string g_describe;
+// fixed buffers: reporting a failure allocates nothing, so it cannot throw
+static thread_local char g_last_error[560];
+static thread_local char g_describe[1536];
 
 void set_error(const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
+  vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
-  g_last_error = buf;
 }
 
 bsf8_status device_status(hipError_t e, const char* what) {
@@ -38,7 +38,7 @@ static bsf8_status fail(bsf8_status s, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(buf, sizeof(buf), fmt, ap);
   va_end(ap);
-  g_last_error = std::string(bsf8_status_name(s)) + ": " + buf;
+  snprintf(g_last_error, sizeof(g_last_error), "%s: %s", bsf8_status_name(s), buf);
   return s;
 }
 
@@ -114,6 +114,19 @@ static bsf8_status validate_impl(const bsf8_decl* decl, const bsf8_member_desc* 
   return BSF8_OK;
 }
 
+// A describe line, `text()` followed by the handle's geometry, in the thread's
+// buffer; the geometry alone where the host's memory ends.
+template <typename F>
+static const char* described(const char* geo, const F& text) {
+  try {
+    const std::string s = text();
+    snprintf(g_describe, sizeof(g_describe), "%s%s", s.c_str(), geo);
+  } catch (const std::exception&) {
+    snprintf(g_describe, sizeof(g_describe), "out of host memory%s", geo);
+  }
+  return g_describe;
+}
+
 static bool dtype_ok(int32_t dt, bool f32, bool bf16) {
   return (f32 && dt == BSF8_DT_F32) || (bf16 && dt == BSF8_DT_BF16);
 }
@@ -152,7 +165,7 @@ const char* bsf8_status_name(bsf8_status s) {
   return "UNKNOWN";
 }
 
-const char* bsf8_last_error(void) { return g_last_error.c_str(); }
+const char* bsf8_last_error(void) { return g_last_error; }
 
 bsf8_status bsf8_validate(const bsf8_decl* decl, const bsf8_member_desc* members, int32_t n_members) {
   return validate_impl(decl, members, n_members);
@@ -173,7 +186,8 @@ bsf8_status bsf8_weight_create(const bsf8_decl* decl, const bsf8_member_desc* me
   }
   if (K > INT32_MAX / 2 || total > INT32_MAX / 2)
     return fail(BSF8_E_UNSUPPORTED, "N or K beyond 2^30");
-  bsf8_weight* h = new bsf8_weight();
+  bsf8_weight* h = new (std::nothrow) bsf8_weight();
+  if (h == nullptr) return fail(BSF8_E_UNSUPPORTED, "out of host memory");
   std::memset(&h->dev, 0, sizeof(h->dev));
   h->dev.n_members = n_members;
   h->dev.K = static_cast<int32_t>(K);
@@ -699,8 +713,7 @@ const char* bsf8_experts_describe(const bsf8_experts* w, int64_t R) {
   char geo[256];
   snprintf(geo, sizeof(geo), " | experts E=%lld N=%lld K=%d members=%d scales=%s", (long long)w->n_experts,
            (long long)w->n_total, w->dev.K, w->dev.n_members, w->dev.scale_bf16 ? "bf16" : "f32");
-  g_describe = describe_w8a8_experts(w->dev, w->n_experts, w->aligned16, R > 0 ? R : 1) + geo;
-  return g_describe.c_str();
+  return described(geo, [&] { return describe_w8a8_experts(w->dev, w->n_experts, w->aligned16, R > 0 ? R : 1); });
 }
 
 bsf8_status bsf8_linear_w8a8_noalloc(const bsf8_weight* w, const uint8_t* xq, int64_t ldq, const float* xs,
@@ -737,17 +750,19 @@ const char* bsf8_describe(const bsf8_weight* w, int32_t arm, int64_t M) {
   char geo[256];
   snprintf(geo, sizeof(geo), " | weight N=%lld K=%d members=%d scales=%s%s", (long long)w->n_total, w->dev.K,
            w->dev.n_members, w->dev.scale_bf16 ? "bf16" : "f32", w->per_tensor ? " per-tensor" : "");
-  if (arm == BSF8_ARM_W8A16) g_describe = describe_w8a16(w->dev, w->aligned16, M) + geo;
-  else if (arm == BSF8_ARM_W8A8) g_describe = describe_w8a8(w->dev, w->aligned16, M) + geo;
-  else if (arm == BSF8_ARM_DENSE) g_describe = describe_dense(w->n_total, w->dev.K, M) + geo;
-  else if (arm == BSF8_ARM_W8A8_DYNAMIC)
-    g_describe = (w8a8_dyn_stream_applies(w->dev, w->aligned16, M > 0 ? M : 1, int64_t(w->dev.K) * 4)
-                      ? describe_w8a8_dyn_stream(w->dev, M > 0 ? M : 1)
-                      : "quant_act into the workspace (K-major scales), then " + describe_w8a8(w->dev, w->aligned16, M)) +
-                  geo;
-  else if (arm == BSF8_ARM_W8A8_EPILOGUE) g_describe = describe_w8a8_epilogue(w->dev, w->aligned16, M > 0 ? M : 1) + geo;
-  else g_describe = "unknown arm";
-  return g_describe.c_str();
+  return described(geo, [&]() -> std::string {
+    switch (arm) {
+      case BSF8_ARM_W8A16: return describe_w8a16(w->dev, w->aligned16, M);
+      case BSF8_ARM_W8A8: return describe_w8a8(w->dev, w->aligned16, M);
+      case BSF8_ARM_DENSE: return describe_dense(w->n_total, w->dev.K, M);
+      case BSF8_ARM_W8A8_DYNAMIC:
+        return w8a8_dyn_stream_applies(w->dev, w->aligned16, M > 0 ? M : 1, int64_t(w->dev.K) * 4)
+                   ? describe_w8a8_dyn_stream(w->dev, M > 0 ? M : 1)
+                   : "quant_act into the workspace (K-major scales), then " + describe_w8a8(w->dev, w->aligned16, M);
+      case BSF8_ARM_W8A8_EPILOGUE: return describe_w8a8_epilogue(w->dev, w->aligned16, M > 0 ? M : 1);
+      default: geo[0] = 0; return "unknown arm";
+    }
+  });
 }
 
 }  // extern "C"

@@ -19,6 +19,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <memory>
 #include <string>
@@ -304,9 +305,7 @@ using namespace bsf8;
 
 static_assert(sizeof(bsf8_unit) == 432, "bsf8_unit layout is part of the ABI");
 
-extern "C" {
-
-bsf8_status bsf8_parse_quant_config(const char* json_text, bsf8_decl* out) {
+static bsf8_status parse_quant_config(const char* json_text, bsf8_decl* out) {
   if (json_text == nullptr || out == nullptr) return ifail(BSF8_E_INVALID_ARG, "null argument");
   Json root;
   Parser ps(json_text, std::strlen(json_text));
@@ -330,8 +329,8 @@ bsf8_status bsf8_parse_quant_config(const char* json_text, bsf8_decl* out) {
   return BSF8_OK;
 }
 
-bsf8_status bsf8_inspect_safetensors(const char* path, const bsf8_decl* decl, bsf8_unit* units, int32_t capacity,
-                                     int32_t* n_units) {
+static bsf8_status inspect_safetensors(const char* path, const bsf8_decl* decl, bsf8_unit* units, int32_t capacity,
+                                       int32_t* n_units) {
   if (path == nullptr || decl == nullptr || n_units == nullptr || capacity < 0 || (units == nullptr && capacity > 0))
     return ifail(BSF8_E_INVALID_ARG, "null argument or negative capacity");
   *n_units = 0;
@@ -446,6 +445,26 @@ bsf8_status bsf8_inspect_safetensors(const char* path, const bsf8_decl* decl, bs
   if (count == 0 && dense_2d > 0)
     return ifail(BSF8_E_WEIGHT_DTYPE, "%s: a dense tree (no FP8 weight) under an fp8 declaration", path);
   return BSF8_OK;
+}
+
+// (strings and maps throw where the host's memory ends)
+extern "C" {
+
+bsf8_status bsf8_parse_quant_config(const char* json_text, bsf8_decl* out) {
+  try {
+    return parse_quant_config(json_text, out);
+  } catch (const std::exception&) {
+    return ifail(BSF8_E_UNSUPPORTED, "out of host memory");
+  }
+}
+
+bsf8_status bsf8_inspect_safetensors(const char* path, const bsf8_decl* decl, bsf8_unit* units, int32_t capacity,
+                                     int32_t* n_units) {
+  try {
+    return inspect_safetensors(path, decl, units, capacity, n_units);
+  } catch (const std::exception&) {
+    return ifail(BSF8_E_UNSUPPORTED, "out of host memory");
+  }
 }
 
 }  // extern "C"

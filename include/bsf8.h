@@ -71,7 +71,8 @@ typedef enum bsf8_status {
   BSF8_E_SCALE_GRID = 15,       /* any other grid shape (mis-blocked, floor-divided, ...) */
   BSF8_E_ALIGNMENT = 16,        /* weight address not 16-byte aligned, scale not element aligned,
                                    or an activation/output address or ld not aligned as a call needs */
-  BSF8_E_UNSUPPORTED = 17,      /* a dtype combination this build does not implement */
+  BSF8_E_UNSUPPORTED = 17,      /* a dtype combination or size this build does not implement, or no host
+                                   memory for a handle or a header */
   BSF8_E_WORKSPACE = 18,        /* workspace missing or smaller than bsf8_workspace_size reports */
   BSF8_E_DEVICE = 19            /* HIP error at launch; see bsf8_last_error() */
 } bsf8_status;
