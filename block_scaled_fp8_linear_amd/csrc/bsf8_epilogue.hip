@@ -10,9 +10,10 @@ namespace {
 
 // Up to this many tokens the few-row kernel, which has four 16-token tiles.  At 64
 // tokens with a residual it takes 17.6 us against the tile GEMM's 19.3 on [5120,
-// 5120], 17.7 against 19.0 on [5000, 4000], 11.8 / 11.9 on [1000, 2000], 48.3 / 47.5 on
-// [17408, 5120], 39.7 / 35.7 on [5120, 17408]; at 100 tokens, where it reads the weight
-// twice, 26.9 against 20.6 on [5120, 5120].
+// 5120], 17.7 against 19.0 on [5000, 4000], 11.8 / 11.9 on [1000, 2000]; the tile GEMM is
+// ahead on wide and on long weights, 47.5 against 48.3 on [17408, 5120] and 35.7 against
+// 39.7 on [5120, 17408], which this rule does not see.  At 100 tokens, where the few-row
+// kernel reads the weight twice, it takes 26.9 against 20.6 on [5120, 5120].
 constexpr int64_t kRowsMaxM = 64;
 
 bool by_rows(const Plan& p, int64_t M) { return !p.fast || M <= kRowsMaxM; }

@@ -24,6 +24,8 @@ __device__ __forceinline__ v8bf decode8(uint32_t lo, uint32_t hi) {
 // the IEEE division a 256 x 256 tile's activations took 8 us, a tenth of it.  The
 // error is below 4 * 2^-24 |v|: the exponent's rounding, |u| 2^-24 relative, meets
 // sigma(u) <= 1 / (1 + |u|) where u is negative and 1 - sigma where it is positive.
+// Relative to the result it is below (6 + 1.5 |u|) 2^-24, and u's own error for a u
+// that is computed, down to 2^-118 (exp2 and the reciprocal know no denormals).
 __device__ __forceinline__ float times_sigmoid(float v, float u) {   // v / (1 + exp(-u))
   return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.4426950408889634f));
 }

@@ -346,8 +346,8 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
 // close to the time of the memory traffic, so the two must overlap, and waves
 // in flight are what overlaps them: the test-free form at 128 registers (four
 // waves per SIMD) takes [8192, 7168] BF16 with residual, post norm and gate in
-// 115 us and with the residual alone in 85 us (410 MB; a copy of as much takes
-// 84 us), [8192, 5120] in 80 and 58 us.  Tried and slower: the general kernel
+// 111 us and with the residual alone in 82-85 us (410 MB; a copy of as much takes
+// 84 us), [8192, 5120] in 76 and 60 us.  Tried and slower: the general kernel
 // above for these rows (205 us; two waves per SIMD and a branch around every
 // load), blocks that stay and prefetch their next row (175 us; the registers of
 // the second row halve the waves), two rows per block sharing the weights'
@@ -357,7 +357,7 @@ __global__ __launch_bounds__(T == 64 ? kSmallBlock : T) void quant_norm_kernel(N
 // ---------------------------------------------------------------------------
 
 // NT: non-temporal, for rows that are read once and then dead (the block's output and the old stream): they leave the
-// caches to what the next call reads (rows from memory, [1024, 5120] 16.2 -> 14.2 us, [8192, 7168] 117.4 -> 115 us).  The
+// caches to what the next call reads (rows from memory, [1024, 5120] 16.2 -> 14.2 us, [8192, 7168] 113 -> 111 us).  The
 // new stream is stored as usual: the next step reads it.  Experts' rows are loaded as usual too: behind the product that
 // wrote them both forms take 18.4 us (1024 tokens, 8 rows of 4096 each), from the cache 17.8 against 19.0 us.
 template <bool BF16, bool NT = false>
@@ -471,8 +471,9 @@ __device__ __forceinline__ void wide_stats(const double (&v)[V][EPL], bool on, c
 }
 
 // COMBINE: x holds the experts' rows.  LAYER: the layer norm; a kernel that tests
-// for it holds 96 registers where one for the RMS norm holds 80, and five waves
-// per SIMD in place of six ([8192, 7168] with post norm and gate 127 against 116 us).
+// for it held 96 to 107 registers, four or five waves per SIMD, where one for the
+// RMS norm holds 78 and six waves ([8192, 7168] with post norm and gate 127 us at
+// 107 registers against 111).
 template <int V, bool COMBINE, bool XBF16, bool HBF16, bool WBF16, bool LAYER>
 __global__ __launch_bounds__(V == 1 ? 128 : 1024) void quant_norm_wide_kernel(NormDev a) {
   __shared__ double lds[2][16];

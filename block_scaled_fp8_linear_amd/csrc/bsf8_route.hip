@@ -12,7 +12,7 @@
 // The operator moves 12 bytes per choice; what bounds it is the launch (2.5 us up
 // to some thousand choices) and then the two sweeps' instructions, two comparisons
 // per choice and block with the counts on the scalar unit, and the places: 65536
-// choices of 128 experts 11.5 us (24 us with a test around every load, 17.5 us with
+// choices of 128 experts 11.5-13.6 us (24 us with a test around every load, 17.5 us with
 // the counts on the vector unit, 13.8 us with a division by top).  Groups of 8 or
 // 16 steps' loads in place of 4 take as long or longer.
 #include <hip/hip_runtime.h>

@@ -300,8 +300,10 @@ __device__ __forceinline__ void load_bias(const EpilogueDev& ep, int64_t c, uint
 // The same with an epilogue.  The tile goes through LDS as F32, 64 columns of some
 // of the wave's tokens at a time, and a lane finishes eight outputs of a token
 // row: a 128-byte line of BF16 per eight lanes, as above.  Whole strips on aligned
-// rows only (the routine below takes the others): with the tests of those in it
-// the compiler spills the tile.  A round's residual loads go out together, before
+// rows only; the routine below takes the others, so that no strip tests for them.
+// The 256 x 256 instances still keep 137 to 247 registers of the tile in scratch
+// while they store (252 to 264 bytes a lane; their K loops keep none), the 128 x
+// 128 instances none.  A round's residual loads go out together, before
 // its values are written to LDS: one by one behind each other's stores their
 // latency, some 32 times per block, took 5 us.
 // RES: the residual is absent (0), BF16 (4 words per lane and row) or F32 (8).

@@ -432,6 +432,11 @@ bsf8_status bsf8_linear_w8a8(const bsf8_weight* w, const uint8_t* xq, int64_t ld
  * acc the F32 product of bsf8_linear_w8a8, everything F32, rounded once to
  * y_dtype.  (The sums behind acc may be ordered otherwise than in
  * bsf8_linear_w8a8, so the two agree within its bound, not bit for bit.)
+ * F32 outputs, and BF16 outputs of up to 64 tokens, sum the products in F32.  BF16
+ * outputs of more tokens (operands 16-byte aligned) sum each 128-wide slice in the
+ * FP8 matrix instruction, which holds fewer bits: off by up to 2^-12 of the slice's
+ * sum of magnitudes (5e-5 of the result's norm on random codes), so a token's
+ * result can differ in its last bits with the number of tokens in the call.
  *
  * e->bias     : [N] F32 or BF16, or NULL.
  * e->activation : bsf8_activation: none, relu, silu = v / (1 + exp(-v)), gelu =
@@ -444,7 +449,9 @@ bsf8_status bsf8_linear_w8a8(const bsf8_weight* w, const uint8_t* xq, int64_t ld
  * e->residual : [M, N] F32 or BF16, leading dimension ldr, or NULL.  It may be y
  *               itself (same address, pitch and type); no other overlap.
  * workspace   : bsf8_workspace_size with arm W8A8_EPILOGUE.
- * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, WORKSPACE, DEVICE.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (M >= 2^30, or more than the 2^32 threads
+ * of one launch: calls off 16-byte alignment from about M * N = 17 * 10^9 on), WORKSPACE,
+ * DEVICE.
  */
 typedef enum bsf8_activation {
   BSF8_ACT_NONE = 0,
@@ -485,8 +492,11 @@ bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, i
  * bsf8_linear_w8a8_experts -- for expert e and row r in [offsets[e], offsets[e+1]):
  *   y[r, R_i + n] = sum_kb (xs[t, kb] * S_i,e[n/128, kb]) * sum_{k in kb} xq[t, k] * W_i,e[n, k]
  * with t = rows[r], or t = r when rows is NULL; products exact, F32 sums, as
- * bsf8_linear_w8a8.
- * xq, xs  : M tokens, as bsf8_quant_act or bsf8_quant_norm writes them.
+ * bsf8_linear_w8a8.  Where bsf8_experts_describe names the FP8 matrix instruction
+ * (BF16 outputs of many rows per expert) it sums each slice, as in
+ * bsf8_linear_w8a8_epilogue.
+ * xq, xs  : M tokens, as bsf8_quant_act or bsf8_quant_norm writes them (M == 0 with
+ *           R > 0 is INVALID_ARG: rows of no tokens).
  * offsets : device int32 [E + 1], ascending (bsf8_expert_plan writes it); an entry
  *           outside [0, R] counts as the nearer end.  Where they descend, runs
  *           overlap and their rows are undefined; no access leaves the arrays.
@@ -497,7 +507,8 @@ bsf8_status bsf8_linear_w8a8_epilogue(const bsf8_weight* w, const uint8_t* xq, i
  * The host learns nothing about the runs, so a call can be captured into a graph
  * and replayed with other offsets; R bounds them.  No workspace.  R == 0 is a
  * no-op.
- * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, DEVICE.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (M or R >= 2^30, or more than the 2^32
+ * threads of one launch, about (min(E, R) + R / 16) * N / 32 * 512), DEVICE.
  *
  * bsf8_experts_describe -- as bsf8_describe, for a call of R rows.
  */
