@@ -761,6 +761,8 @@ def linear_w8a8_epilogue(w: BlockFP8Weight, xq, xs, *, bias=None, activation=Non
     y, ldy = _output(out, M, N, out_dtype, w.device)
     if workspace is not None:
         ws, wsb = workspace
+        if wsb > (ws.numel() * ws.element_size() if ws is not None and ws.is_contiguous() else 0):
+            raise ValueError(f"the workspace must be a contiguous tensor of at least the {wsb} bytes given")
     else:
         wsb = w.workspace_size(ARM_W8A8_EPILOGUE, M)
         ws = torch.empty(wsb, dtype=torch.uint8, device=w.device) if wsb else None

@@ -35,3 +35,24 @@ def test_workspace_is_asked_on_the_weights_device(monkeypatch, current, owner):
     w._h, w.device = None, types.SimpleNamespace(index=owner)
     assert w.workspace_size(B.ARM_W8A8_EPILOGUE, 200) == 0
     assert seen == [owner] and state == [current]
+
+
+@pytest.mark.parametrize("shape,strides,given", [(100, None, 101), (0, None, 1), (None, None, 256), ((8, 64), (128, 1), 512)])
+def test_a_workspace_shorter_than_it_says_is_refused(monkeypatch, shape, strides, given):
+    """The library is told the bytes of the workspace, so they must be there."""
+    import torch
+    called = []
+    w = types.SimpleNamespace(device=types.SimpleNamespace(index=-1), K=256, n_total=64, handle=None)
+    xq, xs = torch.zeros((4, 256), dtype=torch.uint8), torch.zeros((4, 2))
+    out = torch.zeros((4, 64), dtype=torch.bfloat16)
+    monkeypatch.setattr(B, "_CURRENT", (lambda: -1, lambda idx: 0))
+    monkeypatch.setattr(B, "lib", lambda: types.SimpleNamespace(bsf8_linear_w8a8_epilogue=lambda *a: called.append(a) or 0))
+    ws = None if shape is None else torch.zeros(shape, dtype=torch.uint8)
+    if strides:
+        ws = torch.zeros(1024, dtype=torch.uint8).as_strided(shape, strides)
+    with pytest.raises(ValueError, match="workspace"):
+        B.linear_w8a8_epilogue(w, xq, xs, out=out, workspace=(ws, given))
+    assert not called
+    B.linear_w8a8_epilogue(w, xq, xs, out=out, workspace=(torch.zeros(512, dtype=torch.uint8), 512))
+    B.linear_w8a8_epilogue(w, xq, xs, out=out, workspace=(None, 0))
+    assert len(called) == 2

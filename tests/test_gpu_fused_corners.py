@@ -160,3 +160,12 @@ def test_dropped_choices_hold_anything(K):
         got = call(probs.masked_fill(dropped, bad), x.masked_fill(~named[:, None], bad))
         assert all(t.equal(a, b) for a, b in zip(got, want))
     assert t.equal(want[2][2], res[2])
+
+
+@pytest.mark.parametrize("K", [65536, 65664, 70001, 131072, 131088])
+def test_the_longest_sums(K):
+    """K whose blocks outnumber a wave's scales held at a time, and beyond what the tile kernel takes."""
+    for M in (2, 70):
+        epilogue.check(M, (40,), K, act="relu", residual="f32", y="f32", seed=1)
+        epilogue.check(M, (40,), K, act="relu", seed=1)
+    experts.check((1, 0, 40), (33,), K, y="f32", seed=1)
