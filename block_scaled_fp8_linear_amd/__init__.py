@@ -16,6 +16,10 @@ Entry points mirror ``include/bsf8.h``:
 * ``linear_w8a8_epilogue(w, xq, xs, ...)``  linear_w8a8 with bias, activation and residual in the same call
 * ``ExpertsFP8Weight(members)``, ``linear_w8a8_experts(w, xq, xs, offsets, rows)``  products grouped by expert
 * ``linear_w8a8(w, xq, xs)``            FP8 x FP8 arm with F32 epilogue
+* ``rope(q, positions, inv_freq, ...)``  rotary positions with any number of axes, with the head norm
+* ``PagedKVCache(k, v, ...)``           a paged cache of keys and values: E4M3 codes with 1x128 scales, or bfloat16
+* ``cache_write(cache, k, v, slots, ...)``  keys (rotated on the way) and values into the cache
+* ``cache_read(cache, table, offsets, R)``  ranges of cached sequences back as plain rows
 """
 from __future__ import annotations
 
@@ -74,6 +78,26 @@ class Epilogue(ctypes.Structure):
     """bsf8_epilogue."""
     _fields_ = [("bias", _ptr), ("bias_dtype", _i32), ("activation", _i32), ("residual", _ptr),
                 ("residual_dtype", _i32), ("ldr", _i64), ("residual_scale", ctypes.c_float)]
+
+
+class Heads(ctypes.Structure):
+    """bsf8_heads."""
+    _fields_ = [("data", _ptr), ("dtype", _i32), ("heads", _i32), ("token", _i64), ("head", _i64)]
+
+
+class Cache(ctypes.Structure):
+    """bsf8_cache."""
+    _fields_ = [("dtype", _i32), ("heads", _i32), ("head_dim", _i32), ("page_size", _i32), ("n_pages", _i64),
+                ("k", _ptr), ("v", _ptr), ("page", _i64), ("row", _i64), ("head", _i64), ("k_scale", _ptr),
+                ("v_scale", _ptr), ("s_page", _i64), ("s_row", _i64), ("s_head", _i64), ("s_group", _i64)]
+
+
+class RopeArgs(ctypes.Structure):
+    """bsf8_rope_args."""
+    _fields_ = [("M", _i64), ("head_dim", _i32), ("rotary_dim", _i32), ("pairing", _i32), ("n_axes", _i32),
+                ("positions", _ptr), ("position_bytes", _i32), ("ld_axis", _i64), ("axis", ctypes.c_char_p),
+                ("inv_freq", _ptr), ("scale", _f64), ("eps", _f64), ("q", Heads), ("q_out", Heads), ("k", Heads),
+                ("k_out", Heads), ("q_weight", _ptr), ("k_weight", _ptr), ("weight_dtype", _i32)]
 
 
 class Unit(ctypes.Structure):
@@ -139,6 +163,12 @@ EXPORTS = [
     ("bsf8_expert_plan", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_int64,
                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p]),
+    ("bsf8_cache_validate", ctypes.c_int, [ctypes.POINTER(Cache)]),
+    ("bsf8_rope", ctypes.c_int, [ctypes.POINTER(RopeArgs), _ptr]),
+    ("bsf8_cache_write", ctypes.c_int, [ctypes.POINTER(Cache), _i64, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _ptr,
+                                        _i32, ctypes.POINTER(RopeArgs), _ptr]),
+    ("bsf8_cache_read", ctypes.c_int, [ctypes.POINTER(Cache), _i64, _ptr, _i64, _i64, _ptr, _ptr, _i64,
+                                       ctypes.POINTER(Heads), ctypes.POINTER(Heads), _ptr]),
     ("bsf8_upcast", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_dense_workspace_size", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(ctypes.c_size_t)]),
@@ -932,12 +962,252 @@ def linear_dense(wd, x, out_dtype=None, out=None, workspace=None):
     return y
 
 
+# ---------------------------------------------------- rotary positions and the paged cache
+
+def _heads(name, t, M, heads, D, dtypes, out=None) -> Heads:
+    """bsf8_heads of ``t``, which must be [M, heads, D] of one of ``dtypes`` with unit channel stride."""
+    dt = t.dtype
+    if t.shape == (M, heads, D) and dt in dtypes:
+        s0, s1, s2 = t.stride()
+        if s2 == 1:
+            return Heads(t.data_ptr(), DT_BF16 if dt is _T.bfloat16 else DT_F32, heads, s0, s1)
+    raise ValueError(f"{name} must be [{M}, {heads}, {D}] with unit channel stride, of one of {dtypes}")
+
+
+class PagedKVCache:
+    """A paged cache of one layer's keys and values on the GPU: borrowed tensors [pages, page_size, heads, head_dim].
+
+    ``k``, ``v``: bfloat16, or uint8 / float8_e4m3fn codes with ``k_scale``, ``v_scale`` float32 [pages, page_size, heads,
+    ceil(head_dim / 128)]: each row of a head quantized as quant_act quantizes a token, in groups of 128 channels.  k and v
+    have one shape and one set of strides, the scales too; any strides with adjacent channels will do, so token-major and
+    head-major pages and pages that hold keys and values side by side are all views of this form.  ``new`` makes the
+    layout that paged_attention reads fastest.  Slot p * page_size + r is row r of page p."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        idx = _gpu_index("k", k)
+        _same_device(idx, v=v, k_scale=k_scale, v_scale=v_scale)
+        if k.dim() != 4 or v.shape != k.shape or v.dtype != k.dtype or v.stride() != k.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must be [pages, page_size, heads, head_dim] of one type, shape and strides with unit "
+                             "channel stride")
+        dt = _dt_of(k)
+        codes = dt in (DT_U8, DT_F8_E4M3)
+        if (k_scale is None) != (v_scale is None) or codes != (k_scale is not None):
+            raise ValueError("a cache of codes needs k_scale and v_scale, a bfloat16 cache has neither")
+        c = Cache()
+        c.dtype = DT_F8_E4M3 if codes else dt
+        c.n_pages, c.page_size, c.heads, c.head_dim = k.shape
+        c.k, c.v = k.data_ptr(), v.data_ptr()
+        c.page, c.row, c.head, _ = k.stride()
+        if codes:
+            f32 = _torch().float32
+            shape = tuple(k.shape[:3]) + (-(-k.shape[3] // BLOCK),)
+            if k_scale.shape != shape or v_scale.shape != shape or k_scale.dtype != f32 or v_scale.dtype != f32 or \
+                    k_scale.stride() != v_scale.stride():
+                raise ValueError(f"k_scale and v_scale must be float32 {list(shape)} of one set of strides")
+            c.k_scale, c.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+            c.s_page, c.s_row, c.s_head, c.s_group = k_scale.stride()
+        _check(lib().bsf8_cache_validate(ctypes.byref(c)), "PagedKVCache")
+        self._c, self._ref = c, ctypes.byref(c)
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self._idx = k.device, idx
+        self.n_pages, self.page_size, self.heads, self.head_dim = k.shape
+
+    @classmethod
+    def new(cls, n_pages: int, page_size: int, heads: int, head_dim: int, dtype=None, device="cuda"):
+        """A zeroed cache of ``dtype`` (torch.uint8, the default, for E4M3 codes; or torch.bfloat16): head-major pages, a
+        page's scales of a head next to each other."""
+        torch = _torch()
+        dtype = dtype or torch.uint8
+        kv = [torch.zeros(n_pages, heads, page_size, head_dim, dtype=dtype, device=device).transpose(1, 2) for _ in "kv"]
+        if dtype == torch.bfloat16:
+            return cls(*kv)
+        groups = -(-head_dim // BLOCK)
+        sc = [torch.zeros(n_pages, heads, groups, page_size, dtype=torch.float32, device=device).permute(0, 3, 1, 2)
+              for _ in "kv"]
+        return cls(*kv, *sc)
+
+
+PAIRINGS = {"half": 0, "adjacent": 1}
+
+
+def rope_axes(sections: Sequence[int], interleaved: bool = False) -> bytes:
+    """The axis of each rotated pair, for ``axes`` of rope and cache_write: ``sections`` pairs of each axis one after the
+    other, or, interleaved, pair i on axis i % A while i < A * sections[i % A] and on axis 0 otherwise (axis 0 takes what
+    the others leave)."""
+    sections = [int(n) for n in sections]
+    if not 1 <= len(sections) <= 16 or min(sections) < 0:
+        raise ValueError("1 to 16 sections of 0 or more pairs")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+    A = len(sections)
+    axes = bytes(i % A if i < A * sections[i % A] else 0 for i in range(sum(sections)))
+    if [axes.count(a) for a in range(A)] != sections:
+        raise ValueError(f"sections {sections} cannot be taken in turns")
+    return axes
+
+
+def _rotation(a: RopeArgs, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight):
+    """Fill the rotation and the head norms of ``a``."""
+    torch = _torch()
+    if pairing not in PAIRINGS:
+        raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
+    a.M, a.head_dim, a.pairing, a.scale, a.eps = M, D, PAIRINGS[pairing], scale, eps
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq: both or neither")
+    if inv_freq is not None:
+        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous float32 [rotary_dim / 2] tensor")
+        half = inv_freq.shape[0]
+        a.rotary_dim, a.inv_freq = 2 * half, inv_freq.data_ptr()
+        dt = positions.dtype
+        if dt is torch.int32:
+            a.position_bytes = 4
+        elif dt is torch.int64:
+            a.position_bytes = 8
+        else:
+            raise ValueError("positions must be int32 or int64")
+        dims = positions.dim()
+        if dims not in (1, 2) or positions.shape[-1] != M or (M > 1 and positions.stride(-1) != 1):
+            raise ValueError(f"positions must be [M] or [axes, M] with M = {M} and unit token stride")
+        a.positions = positions.data_ptr()
+        a.n_axes, a.ld_axis = (1, 0) if dims == 1 else (positions.shape[0], positions.stride(0))
+        if axes is not None:
+            if len(axes) != half:
+                raise ValueError(f"axes must name one axis for each of the {half} pairs")
+            a.axis = axes if type(axes) is bytes else bytes(axes)
+        elif a.n_axes != 1:
+            raise ValueError("positions of several axes need axes (see rope_axes)")
+    elif axes is not None:
+        raise ValueError("axes without positions")
+    if q_weight is not None:
+        a.q_weight, a.weight_dtype = _vector("q_weight", q_weight, D, (torch.float32, torch.bfloat16)), _dt_of(q_weight)
+    if k_weight is not None:
+        a.k_weight, a.weight_dtype = _vector("k_weight", k_weight, D, (torch.float32, torch.bfloat16)), _dt_of(k_weight)
+        if q_weight is not None and q_weight.dtype != k_weight.dtype:
+            raise ValueError("q_weight and k_weight must have one type")
+
+
+def _turned(name, t, M, heads, D, out, out_dtype, real):
+    """(output, its bsf8_heads) of rotated heads ``t``."""
+    if out is None:
+        out = _T.empty((M, heads, D), dtype=out_dtype or t.dtype, device=t.device)
+        if out.dtype not in real:
+            raise ValueError("out_dtype must be float32 or bfloat16")
+        return out, Heads(out.data_ptr(), DT_BF16 if out.dtype is _T.bfloat16 else DT_F32, heads, heads * D, D)
+    return out, _heads(name, out, M, heads, D, real if out_dtype is None else (out_dtype,))
+
+
+def rope(q, positions, inv_freq, *, k=None, axes=None, pairing="half", scale=1.0, q_weight=None, k_weight=None, eps=1e-6,
+         out=None, k_out=None, out_dtype=None):
+    """Rotary positions of queries q [M, heads, D] and, in the same launch, keys k [M, kv_heads, D] (float32 or bfloat16;
+    views of a grouped projection's output will do) -> (q', k'), k' None without k.
+
+    positions: int32 or int64 [M], or [axes, M] with ``axes`` naming the axis of each pair (rope_axes).  inv_freq: float32
+    [R / 2]; the first R channels of a head turn, pair i by positions * inv_freq[i]: channels (i, i + R/2) with
+    ``pairing`` "half", (2i, 2i + 1) with "adjacent"; ``scale`` multiplies the turned channels.  q_weight, k_weight [D]:
+    the RMS norm of each head before it turns.  Computed in 64 bits, rounded to float32 and to the output's type (the
+    input's unless out_dtype or the outputs say otherwise); an output may be its input."""
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    idx = _gpu_index("q", q)
+    _same_device(idx, positions=positions, inv_freq=inv_freq, k=k, q_weight=q_weight, k_weight=k_weight, out=out, k_out=k_out)
+    if q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be [M, heads, head_dim]")
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight or k_out without k")
+    M, H, D = q.shape
+    a = RopeArgs()
+    _rotation(a, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight)
+    a.q = _heads("q", q, M, H, D, real)
+    out, a.q_out = _turned("out", q, M, H, D, out, out_dtype, real)
+    if k is not None:
+        kv = k.shape[1]
+        a.k = _heads("k", k, M, kv, D, real)
+        k_out, a.k_out = _turned("k_out", k, M, kv, D, k_out, out_dtype, real)
+    _launch("rope", idx, lib().bsf8_rope, ctypes.byref(a))
+    return out, k_out
+
+
+def cache_write(cache: PagedKVCache, k, v, slots, *, positions=None, inv_freq=None, axes=None, pairing="half", scale=1.0,
+                k_weight=None, eps=1e-6, q=None, q_weight=None, out=None, out_dtype=None):
+    """Keys and values [M, heads, D] (float32 or bfloat16) of M tokens into the cache's slots (int32 or int64 [M], page *
+    page_size + row; a slot outside the cache drops the token).  With positions and inv_freq (and k_weight) the keys are
+    rotated (and normed) on the way as rope does, and queries ``q`` in the same launch; returns rope's q', None without q.
+    Slots of one call must differ."""
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    idx = cache._idx
+    _same_device(idx, k=k, v=v, slots=slots, positions=positions, inv_freq=inv_freq, k_weight=k_weight, q=q,
+                 q_weight=q_weight, out=out)
+    D = cache.head_dim
+    if slots.dim() != 1 or slots.dtype not in (torch.int32, torch.int64) or not slots.is_contiguous():
+        raise ValueError("slots must be a contiguous int32 or int64 [M] tensor")
+    M = slots.shape[0]
+    kh = _heads("k", k, M, cache.heads, D, real)
+    vh = _heads("v", v, M, cache.heads, D, real)
+    if q is None and (out is not None or out_dtype is not None or q_weight is not None):
+        raise ValueError("out, out_dtype or q_weight without q")
+    a = None
+    if inv_freq is not None or positions is not None or axes is not None or k_weight is not None or q is not None:
+        r = RopeArgs()
+        _rotation(r, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight)
+        if q is not None:
+            if q.dim() != 3:
+                raise ValueError("q must be [M, heads, head_dim]")
+            H = q.shape[1]
+            r.q = _heads("q", q, M, H, D, real)
+            out, r.q_out = _turned("out", q, M, H, D, out, out_dtype, real)
+        a = ctypes.byref(r)
+    _launch("cache_write", idx, lib().bsf8_cache_write, cache._ref, M, ctypes.byref(kh), ctypes.byref(vh), slots.data_ptr(),
+            slots.element_size(), a)
+    return out
+
+
+def _table(name, table, B) -> Tuple[int, int]:
+    """(columns, pitch) of an int32 [B, pages] tensor with unit column stride."""
+    if table.dim() != 2 or table.shape[0] != B or table.dtype != _T.int32 or (table.shape[1] > 1 and table.stride(1) != 1):
+        raise ValueError(f"{name} must be int32 [{B}, pages] with unit column stride")
+    return table.shape[1], table.stride(0)
+
+
+def cache_read(cache: PagedKVCache, table, offsets, R: int, *, starts=None, out_dtype=None, k_out=None, v_out=None):
+    """Ranges of cached sequences back as rows -> (k, v) [R, heads, D]: rows offsets[b] .. offsets[b+1] - 1 are positions
+    starts[b] (0) on of sequence b, whose pages are table[b] (int32 [B, pages]).  offsets: int32 [B + 1] on the GPU; R bounds
+    them.  bfloat16 unless out_dtype or the outputs say float32; a position without a page reads as zeros, rows outside
+    every range keep what the outputs hold (new outputs: undefined)."""
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    idx = cache._idx
+    _same_device(idx, table=table, offsets=offsets, starts=starts, k_out=k_out, v_out=v_out)
+    B = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
+    if B < 0 or R < 0:
+        raise ValueError("offsets must be int32 [B + 1] and R at least 0")
+    off = _vector("offsets", offsets, B + 1, (torch.int32,))
+    at = _vector("starts", starts, B, (torch.int32,)) if starts is not None else None
+    pages, ld = _table("table", table, B)
+    H, D = cache.heads, cache.head_dim
+    new = out_dtype or (k_out if k_out is not None else v_out).dtype if k_out is not None or v_out is not None else \
+        out_dtype or torch.bfloat16
+    if new not in real:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    if k_out is None:
+        k_out = torch.empty((R, H, D), dtype=new, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty((R, H, D), dtype=new, device=cache.device)
+    kh, vh = _heads("k_out", k_out, R, H, D, (new,)), _heads("v_out", v_out, R, H, D, (new,))
+    _launch("cache_read", idx, lib().bsf8_cache_read, cache._ref, B, table.data_ptr(), ld, pages, at, off, R,
+            ctypes.byref(kh), ctypes.byref(vh))
+    return k_out, v_out
+
+
+
 __all__ = ["BSF8Error", "BlockFP8Weight", "validate", "quant_act", "quant_glu", "glu_act", "quant_norm", "expert_plan", "linear_w8a16", "linear_w8a8",
            "linear_w8a8_dynamic", "linear_w8a8_noalloc", "linear_w8a8_epilogue", "linear_w8a8_experts",
            "ExpertsFP8Weight", "ARM_W8A8_EPILOGUE", "NOALLOC_SCRATCH_BYTES", "upcast",
            "linear_dense", "dense_workspace_size", "lib", "status_name", "ARM_W8A16", "ARM_W8A8", "ARM_DENSE",
            "ARM_W8A8_DYNAMIC",
-           "EXPORTS", "LIB_PATH", "MAX_MEMBERS", "scales_kmajor"]
+           "EXPORTS", "LIB_PATH", "MAX_MEMBERS", "scales_kmajor", "PagedKVCache", "rope", "rope_axes", "cache_write",
+           "cache_read"]
 
 
 READ_STREAM_SINK_WORDS = 2048  # BSF8_READ_STREAM_SINK_WORDS in include/bsf8.h

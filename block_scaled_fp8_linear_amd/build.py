@@ -27,7 +27,8 @@ SOURCES = ["bsf8_host.cpp", "bsf8_inspect.cpp", "bsf8_quant.hip", "bsf8_w8a16.hi
 # Sources compiled apart (in parallel) and joined into the object of the source
 # they belong to: what links the kernels' objects by name (the host-sanitized
 # build of the tests) knows the objects of SOURCES.
-JOINED = {"bsf8_quant.hip": ["bsf8_norm.hip", "bsf8_route.hip"], "bsf8_w8a8.hip": ["bsf8_rows.hip", "bsf8_epilogue.hip", "bsf8_experts.hip"]}
+JOINED = {"bsf8_quant.hip": ["bsf8_norm.hip", "bsf8_route.hip", "bsf8_cache.hip"],
+          "bsf8_w8a8.hip": ["bsf8_rows.hip", "bsf8_epilogue.hip", "bsf8_experts.hip"]}
 ARCH = "gfx950"
 
 

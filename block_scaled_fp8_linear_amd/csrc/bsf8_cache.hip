@@ -1,0 +1,382 @@
+// Rotary positions, and a paged cache of keys and values written and read back (gfx950).
+//
+// heads_kernel: rows of head_dim channels (queries, keys, values of a token's heads) with
+// the head norm, the rotation and, for the cache, the E4M3 quantization.
+//   x' = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+// Everything is F64 up to one rounding to F32, as in the norm step: a code next to a border
+// changes by a whole step with the last bit of an F32 sum, and F64 FMAs run at the F32 rate
+// here.  It bounds nothing: a channel costs some 15 vector instructions against 3 to 6 bytes.
+//
+// A row is LPR = 8, 16 or 32 lanes of 8 channels (head_dim up to 64, 128, 256), so that a
+// 128-channel scale group is 16 lanes, and a wave holds 64 / LPR rows, all of one token:
+// a lane has the same channels in every row it takes, so its angles' sines and cosines are
+// made once for all the heads of the wave.  The pair's other channel is loaded a second time
+// rather than exchanged between lanes: it is in the cache line that the row's own lanes ask
+// for.  An output may be its input: a row's stores need values of all the loads of its wave.
+#include <hip/hip_runtime.h>
+
+#include "bsf8_channels.h"
+#include "bsf8_fused.h"
+
+namespace bsf8 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+
+enum Pairs { kNone, kHalf, kHalfOdd, kAdjacent };   // kHalfOdd: R / 2 is no multiple of a lane's channels
+
+// sine and cosine of an angle below 2^31: r = t - n pi / 2 by two FMAs with pi / 2 in two
+// parts (W. J. Cody and W. Waite, "Software Manual for the Elementary Functions", 1980),
+// |r| <= pi / 4, and the Taylor sums of both up to a remainder below 2^-57.
+__device__ __forceinline__ void sine_cosine(double t, double& s, double& c) {
+  const double n = rint(t * 0.63661977236758138);
+  double r = fma(-n, 1.5707963267948966, t);
+  r = fma(-n, 6.123233995736766e-17, r);
+  const double z = r * r;
+  double p = 1.0 / 355687428096000.0;
+  p = fma(p, z, -1.0 / 1307674368000.0);
+  p = fma(p, z, 1.0 / 6227020800.0);
+  p = fma(p, z, -1.0 / 39916800.0);
+  p = fma(p, z, 1.0 / 362880.0);
+  p = fma(p, z, -1.0 / 5040.0);
+  p = fma(p, z, 1.0 / 120.0);
+  p = fma(p, z, -1.0 / 6.0);
+  const double sr = fma(r * z, p, r);
+  double q = 1.0 / 20922789888000.0;
+  q = fma(q, z, -1.0 / 87178291200.0);
+  q = fma(q, z, 1.0 / 479001600.0);
+  q = fma(q, z, -1.0 / 3628800.0);
+  q = fma(q, z, 1.0 / 40320.0);
+  q = fma(q, z, -1.0 / 720.0);
+  q = fma(q, z, 1.0 / 24.0);
+  const double cr = fma(z * z, q, fma(z, -0.5, 1.0));
+  const int k = static_cast<int>(n);
+  s = (k & 1) ? cr : sr;
+  c = (k & 1) ? sr : cr;
+  if (k & 2) s = -s;
+  if ((k + 1) & 2) c = -c;
+}
+
+__device__ __forceinline__ double position(const HeadsJob& a, int axis, int64_t m) {
+  const int64_t at = axis * a.ld_axis + m;
+  return a.pos64 ? double(static_cast<const int64_t*>(a.pos)[at]) : double(static_cast<const int32_t*>(a.pos)[at]);
+}
+
+// the angle of pair i of token m; p0: the token's position on axis 0
+__device__ __forceinline__ double angle(const HeadsJob& a, int i, int64_t m, double p0) {
+  double p = p0;
+  if (a.n_axes > 1) p = position(a, (a.axis[i >> 3] >> (4 * (i & 7))) & 15, m);
+  return p * double(a.inv_freq[i]);
+}
+
+template <int LPR, int PAIRS>
+__global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
+  constexpr int RPP = 64 / LPR;                     // rows of a wave
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t tok = wave / uint32_t(a.parts), part = wave - tok * uint32_t(a.parts);
+  if (tok >= uint32_t(a.M)) return;                 // whole waves; nothing here waits for another
+  const int64_t m = a.m0 + tok;
+  const int D = a.D, R = a.R, half = R >> 1;
+  const int c0 = (lane & (LPR - 1)) * EPL;
+  const int on = c0 < D ? EPL : 0;                  // D is a multiple of a lane's channels
+  const bool turns = PAIRS != kNone && c0 < R;
+
+  // y[e] = cs[e] x[e] + sn[e] partner[e]; the sign of the sine is the channel's
+  double cs[EPL], sn[EPL];
+  if (PAIRS != kNone) {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      cs[e] = 1.0;
+      sn[e] = 0.0;
+    }
+    if (turns) {
+      const double p0 = a.n_axes == 1 ? position(a, 0, m) : 0.0;
+      if (PAIRS == kAdjacent) {
+#pragma unroll
+        for (int e = 0; e < EPL; e += 2) {
+          if (c0 + e >= R) continue;
+          double s, c;
+          sine_cosine(angle(a, (c0 + e) >> 1, m, p0), s, c);
+          cs[e] = cs[e + 1] = c * a.scale;
+          sn[e + 1] = s * a.scale;
+          sn[e] = -sn[e + 1];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+          const int ch = c0 + e;
+          if (PAIRS == kHalfOdd && ch >= R) continue;
+          const bool second = ch >= half;
+          double s, c;
+          sine_cosine(angle(a, second ? ch - half : ch, m, p0), s, c);
+          cs[e] = c * a.scale;
+          sn[e] = (second ? s : -s) * a.scale;
+        }
+      }
+    }
+  }
+
+  int64_t slot = -1;
+  if (a.to_cache) {
+    slot = a.slot64 ? static_cast<const int64_t*>(a.slots)[m] : int64_t(static_cast<const int32_t*>(a.slots)[m]);
+    if (slot >= a.cache.rows) slot = -1;
+  }
+  const uint32_t page = slot >= 0 ? a.cache.page_of(uint32_t(slot)) : 0;
+  const uint32_t row = slot >= 0 ? uint32_t(slot) - page * uint32_t(a.cache.page_size) : 0;
+
+  const int heads = a.q.heads + a.k.heads + a.v.heads;
+  const int first = int(part) * a.per_part, last = min(heads, first + a.per_part);
+  for (int at = first + lane / LPR; at < last; at += RPP) {
+    const bool is_q = at < a.q.heads, is_v = at >= a.q.heads + a.k.heads;
+    const HeadsDev& src = is_q ? a.q : is_v ? a.v : a.k;
+    const int h = at - (is_q ? 0 : is_v ? a.q.heads + a.k.heads : a.q.heads);
+    const bool skip = a.to_cache && !is_q && slot < 0;
+    const int64_t base = m * src.token + int64_t(h) * src.head;
+    float x[EPL];
+    load_vec(src.p, src.bf16, base + c0, skip ? 0 : on, src.vec, x);
+    float f[EPL];
+    if (is_v) {
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) f[e] = x[e];
+    } else {
+      const void* w = is_q ? a.qw : a.kw;
+      float xp[EPL] = {}, wp[EPL] = {};
+      int pc = 0;
+      if (PAIRS == kHalf) {
+        pc = c0 < half ? c0 + half : c0 - half;
+        load_vec(src.p, src.bf16, base + pc, turns && !skip ? EPL : 0, src.vec, xp);
+      } else if (PAIRS == kHalfOdd) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+          const int ch = c0 + e;
+          if (ch < R && !skip) xp[e] = load_real(src.p, src.bf16, base + (ch < half ? ch + half : ch - half));
+        }
+      } else if (PAIRS == kAdjacent) {
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) xp[e] = x[e ^ 1];
+      }
+      double v[EPL], vp[EPL];
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        v[e] = double(x[e]);
+        vp[e] = double(xp[e]);
+      }
+      if (w != nullptr) {
+        float wv[EPL];
+        load_vec(w, a.w_bf16, c0, on, a.w_vec, wv);
+        if (PAIRS == kHalf) {
+          load_vec(w, a.w_bf16, pc, turns ? EPL : 0, a.w_vec, wp);
+        } else if (PAIRS == kHalfOdd) {
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) {
+            const int ch = c0 + e;
+            if (ch < R) wp[e] = load_real(w, a.w_bf16, ch < half ? ch + half : ch - half);
+          }
+        } else if (PAIRS == kAdjacent) {
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) wp[e] = wv[e ^ 1];
+        }
+        double sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) sum = fma(v[e], v[e], sum);   // zeros past D
+#pragma unroll
+        for (int d = LPR / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        const double rstd = 1.0 / sqrt(sum / double(D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+          v[e] = v[e] * rstd * double(wv[e]);
+          vp[e] = vp[e] * rstd * double(wp[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        double y = v[e];
+        // (beside the sum: a channel that does not turn keeps its zero's sign)
+        if (PAIRS != kNone && (PAIRS == kHalf ? turns : c0 + e < R)) y = fma(cs[e], v[e], sn[e] * vp[e]);
+        f[e] = to_f32(y);
+      }
+    }
+    if (is_q || !a.to_cache) {
+      const HeadsDev& dst = is_q ? a.q_out : a.k_out;
+      store_row(const_cast<void*>(dst.p), dst.bf16, m * dst.token + int64_t(h) * dst.head + c0, on, dst.vec, f);
+      continue;
+    }
+    if (skip) continue;
+    const CacheDev& c = a.cache;
+    uint8_t* out = (is_v ? c.v : c.k) + int64_t(page) * c.page + int64_t(row) * c.row + int64_t(h) * c.head;
+    if (!c.e4m3) {
+      store_row(out, true, c0, on, true, f);
+      continue;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+    for (int d = (LPR < LPG ? LPR : LPG) / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+    float s;
+    uint32_t packed[EPL / 4];
+    encode(f, amax, s, packed);
+    if (on) {
+      *reinterpret_cast<uint2*>(out + c0) = make_uint2(packed[0], packed[1]);
+      if (c0 % kBlock == 0)
+        (is_v ? c.v_scale : c.k_scale)[int64_t(page) * c.s_page + int64_t(row) * c.s_row + int64_t(h) * c.s_head +
+                                       int64_t(c0 / kBlock) * c.s_group] = s;
+    }
+  }
+}
+
+// Rows of the cache back: a wave takes per_wave rows that follow each other, 64 / LPR heads
+// at a time, keys and values together.
+struct ReadJob {
+  CacheDev cache;
+  HeadsDev k, v;              // outputs
+  const int32_t* table;
+  const int32_t* starts;
+  const int32_t* offsets;
+  int64_t ld_table, r0;
+  int32_t B, pages, R, per_wave;
+};
+
+__device__ __forceinline__ void read_codes(const CacheDev& c, const uint8_t* p, float scale, bool there, float (&f)[EPL]) {
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) f[e] = 0.f;
+  if (!there) return;
+  if (!c.e4m3) {
+    Raw<true> r;
+    load_raw<true>(p, 0, EPL, true, r);
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) f[e] = value<true>(r, e);
+    return;
+  }
+  typedef float f2 __attribute__((ext_vector_type(2)));
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int w = int(q ? u.y : u.x);
+    const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), hi = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
+    f[4 * q] = lo[0] * scale;
+    f[4 * q + 1] = lo[1] * scale;
+    f[4 * q + 2] = hi[0] * scale;
+    f[4 * q + 3] = hi[1] * scale;
+  }
+}
+
+template <int LPR>
+__global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadJob a) {
+  constexpr int RPP = 64 / LPR;
+  const int lane = threadIdx.x & 63;
+  const int64_t r_begin = a.r0 + (int64_t(blockIdx.x) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * a.per_wave;
+  if (r_begin >= a.R) return;
+  const int r_end = int(min(int64_t(a.R), r_begin + a.per_wave));
+  const CacheDev& c = a.cache;
+  const int c0 = (lane & (LPR - 1)) * EPL;
+  const bool on = c0 < c.head_dim;
+  // the last sequence whose range begins at or before the first row
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.offsets[mid] <= int(r_begin)) lo = mid;
+    else hi = mid;
+  }
+  int b = lo;
+  for (int r = int(r_begin); r < r_end; ++r) {
+    while (b + 1 < a.B && a.offsets[b + 1] <= r) ++b;
+    const int begin = max(a.offsets[b], 0);
+    if (r < begin || r >= min(a.offsets[b + 1], a.R)) continue;   // no sequence's row
+    const int64_t pos = int64_t(a.starts ? a.starts[b] : 0) + (r - begin);
+    bool there = pos >= 0 && pos < int64_t(a.pages) * c.page_size;
+    const uint32_t col = there ? c.page_of(uint32_t(pos)) : 0;
+    const int32_t page = there ? a.table[int64_t(b) * a.ld_table + col] : -1;
+    there = page >= 0 && page < c.n_pages;
+    const int64_t row = there ? pos - int64_t(col) * c.page_size : 0;
+    const int64_t at = there ? int64_t(page) * c.page + row * c.row : 0;
+    const int64_t s_at = there && c.e4m3 ? int64_t(page) * c.s_page + row * c.s_row : 0;
+    for (int h = lane / LPR; h < c.heads; h += RPP) {
+      const int64_t off = at + int64_t(h) * c.head + int64_t(c0) * (c.e4m3 ? 1 : 2);
+      float ks = 1.f, vs = 1.f;
+      if (there && on && c.e4m3) {
+        const int64_t so = s_at + int64_t(h) * c.s_head + int64_t(c0 / kBlock) * c.s_group;
+        if (a.k.p) ks = c.k_scale[so];
+        if (a.v.p) vs = c.v_scale[so];
+      }
+      float kf[EPL], vf[EPL];
+      read_codes(c, c.k + off, ks, there && on && a.k.p, kf);
+      read_codes(c, c.v + off, vs, there && on && a.v.p, vf);
+      if (a.k.p) store_row(const_cast<void*>(a.k.p), a.k.bf16, int64_t(r) * a.k.token + int64_t(h) * a.k.head + c0, on ? EPL : 0, a.k.vec, kf);
+      if (a.v.p) store_row(const_cast<void*>(a.v.p), a.v.bf16, int64_t(r) * a.v.token + int64_t(h) * a.v.head + c0, on ? EPL : 0, a.v.vec, vf);
+    }
+  }
+}
+
+// waves that fill the device a few times over; more rows per wave only behind that
+constexpr int64_t kEnoughWaves = 8192;
+constexpr int64_t kMostWaves = int64_t(1) << 25;    // of one launch (2^31 threads)
+
+template <int LPR>
+void launch_heads_pairs(const HeadsJob& a, int pairs, unsigned blocks, hipStream_t stream) {
+  switch (pairs) {
+    case kNone: hipLaunchKernelGGL((heads_kernel<LPR, kNone>), dim3(blocks), dim3(kThreads), 0, stream, a); break;
+    case kHalf: hipLaunchKernelGGL((heads_kernel<LPR, kHalf>), dim3(blocks), dim3(kThreads), 0, stream, a); break;
+    case kHalfOdd: hipLaunchKernelGGL((heads_kernel<LPR, kHalfOdd>), dim3(blocks), dim3(kThreads), 0, stream, a); break;
+    default: hipLaunchKernelGGL((heads_kernel<LPR, kAdjacent>), dim3(blocks), dim3(kThreads), 0, stream, a); break;
+  }
+}
+
+}  // namespace
+
+bsf8_status launch_heads(HeadsJob a, int64_t M, hipStream_t stream) {
+  const int heads = a.q.heads + a.k.heads + a.v.heads;
+  if (heads == 0) return BSF8_OK;
+  const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, rows = 64 / lpr;
+  const int pairs = a.R == 0 ? kNone : !a.half ? kAdjacent : (a.R / 2) % EPL == 0 ? kHalf : kHalfOdd;
+  const int64_t passes = (heads + rows - 1) / rows;
+  int64_t per = M * passes / kEnoughWaves;
+  per = per < 1 ? 1 : per > passes ? passes : per;
+  a.per_part = int(per) * rows;
+  a.parts = int((passes + per - 1) / per);
+  const int64_t tokens = kMostWaves / a.parts > 0 ? kMostWaves / a.parts : 1;
+  for (int64_t m0 = 0; m0 < M; m0 += tokens) {
+    a.m0 = m0;
+    a.M = int32_t(M - m0 < tokens ? M - m0 : tokens);
+    const unsigned blocks = unsigned((int64_t(a.M) * a.parts + kWaves - 1) / kWaves);
+    if (lpr == 8) launch_heads_pairs<8>(a, pairs, blocks, stream);
+    else if (lpr == 16) launch_heads_pairs<16>(a, pairs, blocks, stream);
+    else launch_heads_pairs<32>(a, pairs, blocks, stream);
+    const bsf8_status st = device_status(hipGetLastError(), "rope / cache_write launch");
+    if (st != BSF8_OK) return st;
+  }
+  return BSF8_OK;
+}
+
+bsf8_status launch_cache_read(const CacheDev& cache, int64_t B, const int32_t* table, int64_t ld_table, int64_t pages,
+                              const int32_t* starts, const int32_t* offsets, int64_t R, const HeadsDev& k,
+                              const HeadsDev& v, hipStream_t stream) {
+  ReadJob a{};
+  a.cache = cache;
+  a.k = k;
+  a.v = v;
+  a.table = table;
+  a.starts = starts;
+  a.offsets = offsets;
+  a.ld_table = ld_table;
+  a.B = int32_t(B);
+  a.pages = int32_t(pages);
+  a.R = int32_t(R);
+  const int64_t per = R / kEnoughWaves;
+  a.per_wave = int32_t(per < 1 ? 1 : per > 16 ? 16 : per);
+  for (int64_t r0 = 0; r0 < R; r0 += kMostWaves * a.per_wave) {
+    a.r0 = r0;
+    const int64_t n = R - r0 < kMostWaves * a.per_wave ? R - r0 : kMostWaves * a.per_wave;
+    const unsigned blocks = unsigned((n + int64_t(kWaves) * a.per_wave - 1) / (int64_t(kWaves) * a.per_wave));
+    if (cache.head_dim <= 64) hipLaunchKernelGGL(cache_read_kernel<8>, dim3(blocks), dim3(kThreads), 0, stream, a);
+    else if (cache.head_dim <= 128) hipLaunchKernelGGL(cache_read_kernel<16>, dim3(blocks), dim3(kThreads), 0, stream, a);
+    else hipLaunchKernelGGL(cache_read_kernel<32>, dim3(blocks), dim3(kThreads), 0, stream, a);
+    const bsf8_status st = device_status(hipGetLastError(), "cache_read launch");
+    if (st != BSF8_OK) return st;
+  }
+  return BSF8_OK;
+}
+
+}  // namespace bsf8

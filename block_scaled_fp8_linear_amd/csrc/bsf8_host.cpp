@@ -401,6 +401,246 @@ bsf8_status bsf8_expert_plan(const void* ids, int32_t ids_bytes, int64_t M, int6
                             static_cast<hipStream_t>(stream));
 }
 
+// ---- heads of tokens and the paged cache
+
+// Whether `n` dimensions of `size` elements at `stride` above `width` adjacent elements keep all elements apart:
+// ordered by stride, each steps over what lies within it.
+static bool strides_apart(int64_t width, const int64_t* size, const int64_t* stride, int n) {
+  bool used[4] = {};
+  int64_t within = width;   // elements from the first to the last address of what is inside, counted with it
+  for (int k = 0; k < n; ++k) {
+    int at = -1;
+    for (int i = 0; i < n; ++i)
+      if (!used[i] && (at < 0 || stride[i] < stride[at] || (stride[i] == stride[at] && size[i] < size[at]))) at = i;
+    used[at] = true;
+    if (size[at] <= 1) continue;
+    if (stride[at] < within) return false;
+    if (stride[at] > (INT64_MAX / 8 - within) / (size[at] - 1)) return false;   // (no memory has as many bytes)
+    within += stride[at] * (size[at] - 1);
+  }
+  return true;
+}
+
+static bsf8_status cache_checks(const bsf8_cache* p, CacheDev* out) {
+  if (p == nullptr) return fail(BSF8_E_INVALID_ARG, "null cache");
+  const bsf8_cache& c = *p;
+  const bool e4m3 = c.dtype == BSF8_DT_F8_E4M3;
+  if (!e4m3 && c.dtype != BSF8_DT_BF16) return fail(BSF8_E_INVALID_ARG, "cache dtype %d (F8_E4M3 or BF16)", c.dtype);
+  if (c.heads < 1 || c.head_dim < 1 || c.page_size < 1 || c.n_pages < 1)
+    return fail(BSF8_E_INVALID_ARG, "cache of %d heads of %d, %lld pages of %d rows", c.heads, c.head_dim,
+                (long long)c.n_pages, c.page_size);
+  if (c.k == nullptr || c.v == nullptr) return fail(BSF8_E_INVALID_ARG, "null cache pointer");
+  if (e4m3 != (c.k_scale != nullptr) || e4m3 != (c.v_scale != nullptr))
+    return fail(BSF8_E_INVALID_ARG, "an E4M3 cache has k_scale and v_scale, a BF16 cache neither");
+  if (c.head_dim % 16 || c.head_dim > BSF8_CACHE_MAX_HEAD_DIM)
+    return fail(BSF8_E_UNSUPPORTED, "head_dim %d (a multiple of 16 up to %d)", c.head_dim, BSF8_CACHE_MAX_HEAD_DIM);
+  if (c.n_pages > INT32_MAX / c.page_size) return fail(BSF8_E_UNSUPPORTED, "n_pages * page_size beyond 2^31 - 1");
+  const int64_t size[4] = {c.n_pages, c.page_size, c.heads, ceil_div(c.head_dim, kBlock)};
+  const int64_t at[3] = {c.page, c.row, c.head}, s_at[4] = {c.s_page, c.s_row, c.s_head, c.s_group};
+  for (int i = 0; i < 3; ++i)
+    if (at[i] < 0 || at[i] > INT64_MAX / 16) return fail(BSF8_E_INVALID_ARG, "cache stride %lld", (long long)at[i]);
+  if (!strides_apart(c.head_dim, size, at, 3)) return fail(BSF8_E_INVALID_ARG, "cache strides let elements share an address");
+  const int64_t esz = e4m3 ? 1 : 2;
+  if (reinterpret_cast<uintptr_t>(c.k) % 16 || reinterpret_cast<uintptr_t>(c.v) % 16 || c.page * esz % 16 ||
+      c.row * esz % 16 || c.head * esz % 16)
+    return fail(BSF8_E_ALIGNMENT, "cache addresses and strides are multiples of 16 bytes");
+  if (c.row > (int64_t(1) << 27) / esz) return fail(BSF8_E_UNSUPPORTED, "cache rows further apart than 2^27 bytes");
+  CacheDev d{};
+  if (e4m3) {
+    for (int i = 0; i < 4; ++i)
+      if (s_at[i] < 0) return fail(BSF8_E_INVALID_ARG, "negative scale stride");
+    if (!strides_apart(1, size, s_at, 4)) return fail(BSF8_E_INVALID_ARG, "scale strides let elements share an address");
+    if (reinterpret_cast<uintptr_t>(c.k_scale) % 4 || reinterpret_cast<uintptr_t>(c.v_scale) % 4)
+      return fail(BSF8_E_ALIGNMENT, "a scale address is not element aligned");
+    if (c.s_row > (int64_t(1) << 25)) return fail(BSF8_E_UNSUPPORTED, "scale rows further apart than 2^25 elements");
+    d.k_scale = c.k_scale;
+    d.v_scale = c.v_scale;
+    d.s_page = c.s_page;
+    d.s_row = c.s_row;
+    d.s_head = c.s_head;
+    d.s_group = c.s_group;
+  }
+  if (out == nullptr) return BSF8_OK;
+  d.k = static_cast<uint8_t*>(c.k);
+  d.v = static_cast<uint8_t*>(c.v);
+  d.page = c.page * esz;
+  d.row = c.row * esz;
+  d.head = c.head * esz;
+  d.heads = c.heads;
+  d.head_dim = c.head_dim;
+  d.page_size = c.page_size;
+  d.n_pages = int32_t(c.n_pages);
+  d.rows = int32_t(c.n_pages * c.page_size);
+  d.e4m3 = e4m3 ? 1 : 0;
+  // T. Granlund and P. Montgomery, "Division by invariant integers using multiplication", 1994
+  int l = 0;
+  while ((int64_t(1) << l) < c.page_size) ++l;
+  d.magic = uint32_t((uint64_t(1) << (31 + l)) / uint64_t(c.page_size) + 1);
+  d.shift = uint32_t(31 + l);
+  *out = d;
+  return BSF8_OK;
+}
+
+bsf8_status bsf8_cache_validate(const bsf8_cache* cache) { return cache_checks(cache, nullptr); }
+
+// Heads of M tokens: M > 0.  heads < 0: any number; out: no two elements at one address.
+static bsf8_status heads_checks(const char* name, const bsf8_heads& h, int64_t M, int32_t D, int32_t heads, bool out,
+                                HeadsDev* dev) {
+  if (!dtype_ok(h.dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "%s dtype %d (F32 or BF16)", name, h.dtype);
+  if (h.heads < 1 || (heads >= 0 && h.heads != heads)) return fail(BSF8_E_INVALID_ARG, "%s has %d heads", name, h.heads);
+  if (h.data == nullptr) return fail(BSF8_E_INVALID_ARG, "%s is null", name);
+  if (h.token < 0 || h.head < 0) return fail(BSF8_E_INVALID_ARG, "%s has a negative stride", name);
+  if (M > INT32_MAX / h.heads) return fail(BSF8_E_UNSUPPORTED, "%s: M * heads beyond 2^31 - 1", name);
+  const int64_t size[2] = {M, h.heads}, stride[2] = {h.token, h.head};
+  if (out && !strides_apart(D, size, stride, 2)) return fail(BSF8_E_INVALID_ARG, "%s: elements share an address", name);
+  if (h.token > INT64_MAX / 8 / M || h.head > INT64_MAX / 8 / h.heads)
+    return fail(BSF8_E_INVALID_ARG, "%s: strides beyond any memory", name);
+  const int64_t esz = h.dtype == BSF8_DT_BF16 ? 2 : 4;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(h.data);
+  if (at % uintptr_t(esz)) return fail(BSF8_E_ALIGNMENT, "%s is not element aligned", name);
+  dev->p = h.data;
+  dev->token = h.token;
+  dev->head = h.head;
+  dev->heads = h.heads;
+  dev->bf16 = esz == 2 ? 1 : 0;
+  dev->vec = at % 16 == 0 && (M == 1 || h.token * esz % 16 == 0) && (h.heads == 1 || h.head * esz % 16 == 0) ? 1 : 0;
+  return BSF8_OK;
+}
+
+// What bsf8_rope and bsf8_cache_write have in common: the rotation and the queries.  keys: the rope has keys of its own.
+static bsf8_status rope_checks(const bsf8_rope_args& r, bool keys, HeadsJob* a) {
+  if (r.M < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (r.head_dim < 1 || r.rotary_dim < 0 || r.rotary_dim > r.head_dim || r.rotary_dim % 2)
+    return fail(BSF8_E_INVALID_ARG, "rotary_dim %d of head_dim %d (even, up to head_dim)", r.rotary_dim, r.head_dim);
+  if (r.head_dim % 16 || r.head_dim > BSF8_CACHE_MAX_HEAD_DIM)
+    return fail(BSF8_E_UNSUPPORTED, "head_dim %d (a multiple of 16 up to %d)", r.head_dim, BSF8_CACHE_MAX_HEAD_DIM);
+  if (r.pairing != BSF8_PAIR_HALF && r.pairing != BSF8_PAIR_ADJACENT) return fail(BSF8_E_INVALID_ARG, "pairing %d", r.pairing);
+  if (r.q.data == nullptr && r.q_out.data != nullptr) return fail(BSF8_E_INVALID_ARG, "q_out without q");
+  if (r.q.data == nullptr && r.q_weight) return fail(BSF8_E_INVALID_ARG, "q_weight without q");
+  if (!keys && (r.k.data || r.k_out.data)) return fail(BSF8_E_INVALID_ARG, "the keys of a cache write are its own");
+  if (keys && r.k.data == nullptr && (r.k_out.data || r.k_weight)) return fail(BSF8_E_INVALID_ARG, "k_out or k_weight without k");
+  if (r.q_weight || r.k_weight) {
+    if (!dtype_ok(r.weight_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "weight dtype %d (F32 or BF16)", r.weight_dtype);
+    if (!(r.eps > 0.0) || !std::isfinite(r.eps)) return fail(BSF8_E_INVALID_ARG, "eps %g (positive)", r.eps);
+  }
+  if (r.rotary_dim) {
+    if (r.n_axes < 1 || r.n_axes > BSF8_ROPE_MAX_AXES) return fail(BSF8_E_INVALID_ARG, "%d axes (1 to %d)", r.n_axes, BSF8_ROPE_MAX_AXES);
+    if (r.position_bytes != 4 && r.position_bytes != 8) return fail(BSF8_E_INVALID_ARG, "positions of %d bytes (4 or 8)", r.position_bytes);
+    if (!std::isfinite(r.scale)) return fail(BSF8_E_INVALID_ARG, "scale %g", r.scale);
+    if (r.axis)
+      for (int i = 0; i < r.rotary_dim / 2; ++i)
+        if (r.axis[i] >= r.n_axes) return fail(BSF8_E_INVALID_ARG, "pair %d is on axis %d of %d", i, r.axis[i], r.n_axes);
+  }
+  a->D = r.head_dim;
+  a->R = r.rotary_dim;
+  a->half = r.pairing == BSF8_PAIR_HALF ? 1 : 0;
+  if (r.M == 0) return BSF8_OK;
+  if (r.M > INT32_MAX) return fail(BSF8_E_UNSUPPORTED, "M too large");
+  if (r.rotary_dim) {
+    if (r.positions == nullptr || r.inv_freq == nullptr) return fail(BSF8_E_INVALID_ARG, "null positions or inv_freq");
+    if (r.ld_axis < 0 || (r.n_axes > 1 && r.ld_axis > INT64_MAX / 32)) return fail(BSF8_E_INVALID_ARG, "ld_axis %lld", (long long)r.ld_axis);
+    if (reinterpret_cast<uintptr_t>(r.positions) % uintptr_t(r.position_bytes) || reinterpret_cast<uintptr_t>(r.inv_freq) % 4)
+      return fail(BSF8_E_ALIGNMENT, "positions or inv_freq not element aligned");
+    a->n_axes = r.axis ? r.n_axes : 1;
+    a->pos64 = r.position_bytes == 8 ? 1 : 0;
+    a->ld_axis = r.ld_axis;
+    a->pos = r.positions;
+    a->inv_freq = r.inv_freq;
+    a->scale = r.scale;
+    if (r.axis)
+      for (int i = 0; i < r.rotary_dim / 2; ++i) a->axis[i / 8] |= uint32_t(r.axis[i]) << (4 * (i % 8));
+  }
+  if (r.q_weight || r.k_weight) {
+    a->w_bf16 = r.weight_dtype == BSF8_DT_BF16 ? 1 : 0;
+    const uintptr_t both = reinterpret_cast<uintptr_t>(r.q_weight) | reinterpret_cast<uintptr_t>(r.k_weight);
+    if (both % (a->w_bf16 ? 2 : 4)) return fail(BSF8_E_ALIGNMENT, "a weight is not element aligned");
+    a->w_vec = both % 16 == 0 ? 1 : 0;
+    a->qw = r.q_weight;
+    a->kw = r.k_weight;
+    a->eps = r.eps;
+  }
+  if (r.q.data) {
+    bsf8_status st = heads_checks("q", r.q, r.M, r.head_dim, -1, false, &a->q);
+    if (st == BSF8_OK) st = heads_checks("q_out", r.q_out, r.M, r.head_dim, r.q.heads, true, &a->q_out);
+    if (st != BSF8_OK) return st;
+  }
+  if (r.k.data) {
+    bsf8_status st = heads_checks("k", r.k, r.M, r.head_dim, -1, false, &a->k);
+    if (st == BSF8_OK) st = heads_checks("k_out", r.k_out, r.M, r.head_dim, r.k.heads, true, &a->k_out);
+    if (st != BSF8_OK) return st;
+  }
+  if (int64_t(a->q.heads) + a->k.heads > INT32_MAX / 4 || r.M > INT32_MAX / (int64_t(a->q.heads) + a->k.heads + 1))
+    return fail(BSF8_E_UNSUPPORTED, "M * heads beyond 2^31 - 1");
+  return BSF8_OK;
+}
+
+bsf8_status bsf8_rope(const bsf8_rope_args* args, void* stream) {
+  if (args == nullptr) return fail(BSF8_E_INVALID_ARG, "null arguments");
+  HeadsJob a{};
+  const bsf8_status st = rope_checks(*args, true, &a);
+  if (st != BSF8_OK || args->M == 0) return st;
+  if (a.q.heads == 0 && a.k.heads == 0) return fail(BSF8_E_INVALID_ARG, "neither q nor k is given");
+  return launch_heads(a, args->M, static_cast<hipStream_t>(stream));
+}
+
+bsf8_status bsf8_cache_write(const bsf8_cache* cache, int64_t M, const bsf8_heads* k, const bsf8_heads* v, const void* slots,
+                             int32_t slot_bytes, const bsf8_rope_args* rope, void* stream) {
+  HeadsJob a{};
+  bsf8_status st = cache_checks(cache, &a.cache);
+  if (st != BSF8_OK) return st;
+  if (M < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (slot_bytes != 4 && slot_bytes != 8) return fail(BSF8_E_INVALID_ARG, "slots of %d bytes (4 or 8)", slot_bytes);
+  if (rope) {
+    if (rope->M != M || rope->head_dim != cache->head_dim)
+      return fail(BSF8_E_INVALID_ARG, "rope of M %lld, head_dim %d", (long long)rope->M, rope->head_dim);
+    st = rope_checks(*rope, false, &a);
+    if (st != BSF8_OK) return st;
+  }
+  if (M == 0) return BSF8_OK;
+  if (k == nullptr || v == nullptr || slots == nullptr) return fail(BSF8_E_INVALID_ARG, "null pointer");
+  if (M > INT32_MAX / (2 * int64_t(cache->heads) + a.q.heads + 1)) return fail(BSF8_E_UNSUPPORTED, "M * heads beyond 2^31 - 1");
+  st = heads_checks("k", *k, M, cache->head_dim, cache->heads, false, &a.k);
+  if (st == BSF8_OK) st = heads_checks("v", *v, M, cache->head_dim, cache->heads, false, &a.v);
+  if (st != BSF8_OK) return st;
+  if (reinterpret_cast<uintptr_t>(slots) % uintptr_t(slot_bytes)) return fail(BSF8_E_ALIGNMENT, "slots not element aligned");
+  a.D = cache->head_dim;
+  a.to_cache = 1;
+  a.slots = slots;
+  a.slot64 = slot_bytes == 8 ? 1 : 0;
+  return launch_heads(a, M, static_cast<hipStream_t>(stream));
+}
+
+static bsf8_status table_checks(const bsf8_cache& c, int64_t B, const int32_t* table, int64_t ld_table, int64_t pages) {
+  if (table == nullptr) return fail(BSF8_E_INVALID_ARG, "null table");
+  if (pages < 1 || (B > 1 && ld_table < pages)) return fail(BSF8_E_INVALID_ARG, "table of %lld pages, pitch %lld", (long long)pages, (long long)ld_table);
+  if (reinterpret_cast<uintptr_t>(table) % 4) return fail(BSF8_E_ALIGNMENT, "table not element aligned");
+  if (B > INT32_MAX || pages > INT32_MAX / c.page_size) return fail(BSF8_E_UNSUPPORTED, "B, or pages * page_size, beyond 2^31 - 1");
+  if (B > 1 && ld_table > INT64_MAX / 8 / B) return fail(BSF8_E_INVALID_ARG, "table pitch beyond any memory");
+  return BSF8_OK;
+}
+
+bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* table, int64_t ld_table, int64_t pages,
+                            const int32_t* starts, const int32_t* offsets, int64_t R, const bsf8_heads* k_out,
+                            const bsf8_heads* v_out, void* stream) {
+  CacheDev c{};
+  bsf8_status st = cache_checks(cache, &c);
+  if (st != BSF8_OK) return st;
+  if (B < 0 || R < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (B == 0 || R == 0) return BSF8_OK;
+  HeadsDev k{}, v{};
+  if ((k_out == nullptr || k_out->data == nullptr) && (v_out == nullptr || v_out->data == nullptr))
+    return fail(BSF8_E_INVALID_ARG, "neither k_out nor v_out is given");
+  if (offsets == nullptr) return fail(BSF8_E_INVALID_ARG, "null offsets");
+  st = table_checks(*cache, B, table, ld_table, pages);
+  if (st == BSF8_OK && k_out && k_out->data) st = heads_checks("k_out", *k_out, R, cache->head_dim, cache->heads, true, &k);
+  if (st == BSF8_OK && v_out && v_out->data) st = heads_checks("v_out", *v_out, R, cache->head_dim, cache->heads, true, &v);
+  if (st != BSF8_OK) return st;
+  if (k.p && v.p && k.bf16 != v.bf16) return fail(BSF8_E_INVALID_ARG, "k_out and v_out of different types");
+  if (reinterpret_cast<uintptr_t>(offsets) % 4 || reinterpret_cast<uintptr_t>(starts) % 4)
+    return fail(BSF8_E_ALIGNMENT, "offsets or starts not element aligned");
+  return launch_cache_read(c, B, table, ld_table, pages, starts, offsets, R, k, v, static_cast<hipStream_t>(stream));
+}
+
 // Workspace of the two-step form of bsf8_linear_w8a8_dynamic: the codes (row
 // pitch K rounded up to 16 bytes), the K-major scales, then the W8A8 call's own
 // workspace, each from a 256-byte boundary.

@@ -78,6 +78,44 @@ bsf8_status launch_quant_norm(const NormDev& a, bool x_bf16, bool h_bf16, hipStr
 bsf8_status launch_expert_plan(const void* ids, bool ids64, int64_t M, int64_t top, int64_t E, int32_t* offsets,
                                int32_t* rows, int32_t* slots, hipStream_t stream);
 
+// Heads of tokens (bsf8_heads) and a paged cache (bsf8_cache) as the kernels take them.
+struct HeadsDev {
+  const void* p;        // null: absent (heads 0)
+  int64_t token, head;  // elements
+  int32_t heads, bf16;
+  int32_t vec;          // every row's 8-channel pieces are 16-byte aligned
+};
+struct CacheDev {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page, row, head;                  // bytes
+  int64_t s_page, s_row, s_head, s_group;   // elements
+  int32_t heads, head_dim, page_size, n_pages;
+  int32_t rows;                             // n_pages * page_size
+  int32_t e4m3;
+  uint32_t magic, shift;                    // i / page_size = i * magic >> shift, i < 2^31
+  __host__ __device__ uint32_t page_of(uint32_t i) const { return uint32_t(uint64_t(i) * magic >> shift); }
+};
+struct HeadsJob {
+  HeadsDev q, q_out, k, k_out, v;
+  int32_t M, D, R;
+  int32_t half;         // pairs (i, i + R / 2), else (2i, 2i + 1)
+  int32_t n_axes, pos64, slot64, to_cache, w_bf16, w_vec;
+  int32_t parts, per_part;   // waves of a token, heads of a wave
+  int64_t m0, ld_axis;
+  const void* pos;
+  const float* inv_freq;
+  double scale, eps;
+  const void *qw, *kw;
+  const void* slots;
+  CacheDev cache;
+  uint32_t axis[BSF8_CACHE_MAX_HEAD_DIM / 2 / 8];   // four bits per pair
+};
+bsf8_status launch_heads(HeadsJob a, int64_t M, hipStream_t stream);
+bsf8_status launch_cache_read(const CacheDev& cache, int64_t B, const int32_t* table, int64_t ld_table, int64_t pages,
+                              const int32_t* starts, const int32_t* offsets, int64_t R, const HeadsDev& k,
+                              const HeadsDev& v, hipStream_t stream);
+
 size_t w8a16_workspace_bytes(const WeightDev& w, int64_t M);
 bsf8_status launch_w8a16(const WeightDev& w, bool aligned, const void* x, bool x_bf16, int64_t M,
                          int64_t ldx, void* y, bool y_bf16, int64_t ldy, void* ws, size_t ws_bytes,

@@ -524,6 +524,144 @@ bsf8_status bsf8_linear_w8a8_experts(const bsf8_experts* w, const uint8_t* xq, i
 const char* bsf8_experts_describe(const bsf8_experts* w, int64_t R);
 
 /*
+ * Between the Q/K/V projection and the output projection: rotary positions, a
+ * paged cache of keys and values, and the attention of one new token over it.
+ * ("Qwen checkpoints with block FP8 weights", operator paragraph: the attention
+ *  projections share the operator; "FP8 Native Serving": an FP8 cache of keys
+ *  and values read by paged decode attention.)
+ *
+ * bsf8_heads -- heads of M tokens: element (token m, head h, channel d) at
+ * data[m * token + h * head + d] (strides in elements), F32 or BF16.  A grouped
+ * projection's output [M, ldy] is three of them: q at column 0, k and v behind it,
+ * token = ldy, head = head_dim.  Element alignment is enough; 16-byte accesses are
+ * taken where address and strides allow them.
+ */
+typedef struct bsf8_heads {
+  void* data;      /* NULL: absent */
+  int32_t dtype;   /* BSF8_DT_F32 or BSF8_DT_BF16 */
+  int32_t heads;
+  int64_t token, head;
+} bsf8_heads;
+
+/*
+ * bsf8_cache -- a paged cache of one layer's keys and values, in caller memory:
+ * n_pages pages of page_size rows (one token each) of `heads` heads.  Channel d of
+ * (page p, row r, head h) at k[p * page + r * row + h * head + d], v alike, so
+ * that token-major and head-major pages, and pages that hold keys and values side
+ * by side, are all descriptions of one struct.  A slot is p * page_size + r.
+ * E4M3: each row of a head is quantized as bsf8_quant_act quantizes a token's
+ * channels, in groups of 128 from the head's channel 0 (the last may be shorter);
+ * the scale of group g at k_scale[p * s_page + r * s_row + h * s_head + g * s_group].
+ * BF16: values as they are, no scales.
+ * head_dim is a multiple of 16 up to BSF8_CACHE_MAX_HEAD_DIM; k and v are 16-byte
+ * aligned with strides of a multiple of 16 bytes (ALIGNMENT otherwise); strides
+ * let no two elements share an address (INVALID_ARG otherwise); n_pages * page_size
+ * and 16 * row (bytes) are below 2^31 (UNSUPPORTED otherwise).  Attention reads
+ * fastest with head-major pages of a multiple of 16 rows (better 32) and s_row == 1.
+ */
+#define BSF8_CACHE_MAX_HEAD_DIM 256
+typedef struct bsf8_cache {
+  int32_t dtype;               /* BSF8_DT_F8_E4M3 or BSF8_DT_BF16 */
+  int32_t heads, head_dim, page_size;
+  int64_t n_pages;
+  void* k;
+  void* v;
+  int64_t page, row, head;     /* of k and of v, in elements */
+  float* k_scale;              /* NULL for BF16 */
+  float* v_scale;
+  int64_t s_page, s_row, s_head, s_group;
+} bsf8_cache;
+
+/* bsf8_cache_validate -- the checks of a descriptor that every call below makes. */
+bsf8_status bsf8_cache_validate(const bsf8_cache* cache);
+
+/*
+ * bsf8_rope -- rotary positions with any number of axes, for queries and keys in
+ * one launch, with the head norm of models that have one.  For token m and head
+ * row x of D = head_dim channels, R = rotary_dim of them rotated:
+ *   x' = x / sqrt(mean(x^2) + eps) * weight        (weight given; else x' = x)
+ *   t_i = positions[axis[i] * ld_axis + m] * inv_freq[i],  i in [0, R / 2)
+ *   (a, b) = channels (i, i + R/2) (BSF8_PAIR_HALF) or (2i, 2i + 1) (BSF8_PAIR_ADJACENT)
+ *   y_a = scale * (x'_a cos t_i - x'_b sin t_i),  y_b = scale * (x'_b cos t_i + x'_a sin t_i)
+ * and channels from R on are x'.  All of it is F64 with one rounding to F32, which
+ * is stored, or rounded to BF16.  Angles: the product in F64 (exact for positions
+ * below 2^29), reduced by two-part pi / 2; positions are taken as F64 numbers, and
+ * |t_i| is below 2^31.
+ * Non-finite inputs are outside the defined domain.
+ *
+ * positions : int32 (position_bytes 4) or int64 (8), n_axes rows (1 to 16) of M.
+ * axis      : HOST bytes [R / 2], the axis of each pair, read during the call;
+ *             NULL means axis 0 throughout.
+ * inv_freq  : device F32 [R / 2].
+ * q, q_out, k, k_out : q or k may be absent; an output has its input's heads and
+ *             any type.  An output may be its input itself (same address, strides
+ *             and type); no other overlap.
+ * q_weight, k_weight : device [D] F32 or BF16 (weight_dtype, of both), or NULL.
+ * R is even, 0 to D (0: positions, axis and inv_freq are not read); D a multiple of
+ * 16 up to BSF8_CACHE_MAX_HEAD_DIM (UNSUPPORTED otherwise).
+ * Errors: INVALID_ARG, ALIGNMENT (an address not element aligned), UNSUPPORTED (D, or
+ * M * heads beyond 2^31 - 1), DEVICE.
+ */
+typedef enum bsf8_pairing { BSF8_PAIR_HALF = 0, BSF8_PAIR_ADJACENT = 1 } bsf8_pairing;
+#define BSF8_ROPE_MAX_AXES 16
+typedef struct bsf8_rope_args {
+  int64_t M;
+  int32_t head_dim, rotary_dim;
+  int32_t pairing;             /* bsf8_pairing */
+  int32_t n_axes;
+  const void* positions;
+  int32_t position_bytes;
+  int64_t ld_axis;
+  const uint8_t* axis;
+  const float* inv_freq;
+  double scale;
+  double eps;                  /* positive where a weight is given */
+  bsf8_heads q, q_out, k, k_out;
+  const void* q_weight;
+  const void* k_weight;
+  int32_t weight_dtype;
+} bsf8_rope_args;
+bsf8_status bsf8_rope(const bsf8_rope_args* args, void* stream);
+
+/*
+ * bsf8_cache_write -- M tokens' keys and values into the cache: token m to slot
+ * slots[m].  With rope (or its k_weight) the keys are normed and rotated on the way
+ * as bsf8_rope does, and rope->q, when given, goes to rope->q_out in the same launch;
+ * rope->k and rope->k_out are absent (the keys are k).  What is stored is made of
+ * the F32 values: E4M3 codes and scales bit for bit as bsf8_quant_act makes them,
+ * or their rounding to BF16.
+ * slots : int32 (slot_bytes 4) or int64 (8).  A token whose slot lies outside
+ *         [0, n_pages * page_size) is not written (its query is rotated all the
+ *         same).  Slots of one call differ; of two tokens with one slot, the row is
+ *         left with parts of either.  Rows without a token keep what they hold.
+ * Errors: as bsf8_rope and bsf8_cache_validate; INVALID_ARG also where k or v has
+ * other heads than the cache, or rope another M or head_dim.
+ */
+bsf8_status bsf8_cache_write(const bsf8_cache* cache, int64_t M, const bsf8_heads* k, const bsf8_heads* v,
+                             const void* slots, int32_t slot_bytes, const bsf8_rope_args* rope, void* stream);
+
+/*
+ * bsf8_cache_read -- ranges of B sequences back as plain rows: row r in
+ * [offsets[b], offsets[b + 1]) of k_out and v_out is position
+ * starts[b] + r - offsets[b] of sequence b (starts NULL: 0), whose page is
+ * table[b * ld_table + position / page_size].  Codes come back as their value times
+ * their scale, one F32 product, rounded once where the output is BF16.
+ * offsets : device int32 [B + 1], ascending; an entry outside [0, R] counts as the
+ *           nearer end.  Where they descend rows are undefined; no access leaves
+ *           the arrays.
+ * table   : device int32 [B, pages], row pitch ld_table >= pages.
+ * A position outside [0, pages * page_size) or on a page outside [0, n_pages) reads
+ * as zeros.  Rows outside every range keep what they hold.  The host learns nothing
+ * of the ranges; R bounds them.
+ * k_out, v_out : heads of R tokens with the cache's head count and one type; either
+ *           may be absent.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED, DEVICE.
+ */
+bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* table, int64_t ld_table, int64_t pages,
+                            const int32_t* starts, const int32_t* offsets, int64_t R, const bsf8_heads* k_out,
+                            const bsf8_heads* v_out, void* stream);
+
+/*
  * bsf8_linear_w8a8_dynamic -- the W8A8 arm on unquantized activations: x is
  * quantized per token in 1x128 groups exactly as bsf8_quant_act does (amax /
  * 448, E4M3 round-to-nearest-even, saturating) and the product is then that

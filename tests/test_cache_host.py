@@ -1,0 +1,144 @@
+"""Refusals of the rotary positions and the paged cache, before any launch (no GPU needed)."""
+import ctypes
+
+import pytest
+
+import block_scaled_fp8_linear_amd as B
+
+FAKE = 1 << 40
+name = B.status_name
+
+
+def make_cache(**kw):
+    """Head-major E4M3 pages of 16 rows, 4 heads of 192 channels; ``kw`` replaces fields."""
+    c = B.Cache(B.DT_F8_E4M3, 4, 192, 16, 10, FAKE, FAKE, 4 * 16 * 192, 192, 16 * 192, FAKE, FAKE, 4 * 2 * 16, 1, 32, 16)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+def _validate(**kw):
+    return name(B.lib().bsf8_cache_validate(ctypes.byref(make_cache(**kw))))
+
+
+def test_cache_descriptor():
+    assert name(B.lib().bsf8_cache_validate(None)) == "INVALID_ARG"
+    assert _validate() == "OK"
+    assert _validate(page=16 * 4 * 192, row=4 * 192, head=192) == "OK"                       # token-major
+    assert _validate(page=2 * 16 * 4 * 192, row=4 * 192, head=192) == "OK"                   # keys and values side by side
+    assert _validate(dtype=B.DT_BF16, k_scale=None, v_scale=None) == "OK"
+    assert _validate(n_pages=1, page=0) == "OK" and _validate(heads=1, head=0, s_head=0) == "OK"
+    for bad in (dict(dtype=B.DT_F32), dict(dtype=B.DT_F8_E5M2), dict(heads=0), dict(head_dim=0), dict(page_size=0),
+                dict(n_pages=0), dict(heads=-1), dict(n_pages=-5), dict(k=None), dict(v=None), dict(k_scale=None),
+                dict(v_scale=None), dict(dtype=B.DT_BF16), dict(dtype=B.DT_BF16, k_scale=None), dict(page=-16), dict(row=-192),
+                dict(row=176), dict(head=192), dict(page=4 * 16 * 192 - 16), dict(page=0), dict(s_row=-1), dict(s_row=0),
+                dict(s_group=15), dict(s_head=16), dict(s_page=127), dict(page=1 << 62), dict(n_pages=1, page=1 << 62)):
+        assert _validate(**bad) == "INVALID_ARG", bad
+    for bad in (dict(k=FAKE + 8), dict(v=FAKE + 1), dict(row=200, head=16 * 200, page=64 * 200), dict(k_scale=FAKE + 2),
+                dict(v_scale=FAKE + 1), dict(dtype=B.DT_BF16, k_scale=None, v_scale=None, head=16 * 192 + 4, page=1 << 14)):
+        assert _validate(**bad) == "ALIGNMENT", bad
+    for bad in (dict(head_dim=72), dict(head_dim=272), dict(head_dim=8), dict(n_pages=1 << 27), dict(n_pages=1 << 40),
+                dict(heads=1, head=0, row=1 << 28, page=1 << 33),
+                dict(s_row=1 << 26, s_head=16, s_group=64, s_page=1 << 30)):
+        assert _validate(**bad) == "UNSUPPORTED", bad
+
+
+def _rope(**kw):
+    a = B.RopeArgs()
+    a.M, a.head_dim, a.rotary_dim, a.n_axes, a.positions, a.position_bytes = 5, 64, 32, 1, FAKE, 4
+    a.inv_freq, a.scale, a.eps, a.weight_dtype = FAKE, 1.0, 1e-6, B.DT_F32
+    a.q = a.q_out = B.Heads(FAKE, B.DT_BF16, 3, 192, 64)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return name(B.lib().bsf8_rope(ctypes.byref(a), None))
+
+
+def H(data=FAKE, dtype=B.DT_BF16, heads=3, token=192, head=64):
+    return B.Heads(data, dtype, heads, token, head)
+
+
+def test_rope_refusals():
+    assert name(B.lib().bsf8_rope(None, None)) == "INVALID_ARG"
+    assert _rope(M=0) == "OK" and _rope(M=0, positions=None) == "OK"
+    for bad in (dict(M=-1), dict(head_dim=0), dict(rotary_dim=66), dict(rotary_dim=-2), dict(rotary_dim=31), dict(pairing=2),
+                dict(n_axes=0), dict(n_axes=17), dict(positions=None), dict(position_bytes=2), dict(inv_freq=None),
+                dict(scale=float("nan")), dict(scale=float("inf")), dict(axis=bytes([0] * 15 + [1])), dict(n_axes=3, axis=bytes([3] * 16)),
+                dict(q=H(None)), dict(q_out=H(None)), dict(q=H(None), q_out=H(None)), dict(q=H(heads=0)),
+                dict(q_out=H(heads=2)), dict(q=H(dtype=B.DT_F16)), dict(q_out=H(dtype=B.DT_U8)), dict(q=H(token=-1)),
+                dict(q=H(head=-64)), dict(q_out=H(token=100)), dict(q_out=H(head=63)), dict(q_out=H(token=0)),
+                dict(k=H()), dict(k_out=H()), dict(k_weight=FAKE), dict(q_weight=FAKE, eps=0.0),
+                dict(q_weight=FAKE, eps=float("nan")), dict(q_weight=FAKE, weight_dtype=B.DT_F16), dict(ld_axis=-1),
+                dict(q=H(token=1 << 61)), dict(q=H(None), q_out=H(None), k=H(), k_out=H(), q_weight=FAKE)):
+        assert _rope(**bad) == "INVALID_ARG", bad
+    for bad in (dict(q=H(FAKE + 1)), dict(q_out=H(FAKE + 1)), dict(q=H(FAKE + 2, B.DT_F32)), dict(positions=FAKE + 2),
+                dict(positions=FAKE + 4, position_bytes=8), dict(inv_freq=FAKE + 2), dict(q_weight=FAKE + 2),
+                dict(k=H(), k_out=H(FAKE + 1))):
+        assert _rope(**bad) == "ALIGNMENT", bad
+    for bad in (dict(head_dim=72), dict(head_dim=272), dict(M=1 << 31), dict(M=1 << 30)):
+        assert _rope(**bad) == "UNSUPPORTED", bad
+
+
+def _write(cache=None, M=5, k=H(token=768, head=192, heads=4), v=H(token=768, head=192, heads=4), slots=FAKE, b=8, rope=None):
+    c = make_cache() if cache is None else cache
+    ref = lambda x: ctypes.byref(x) if x is not None else None
+    return name(B.lib().bsf8_cache_write(ref(c), M, ref(k), ref(v), slots, b, ref(rope), None))
+
+
+def test_cache_write_refusals():
+    def rope(**kw):
+        a = B.RopeArgs()
+        a.M, a.head_dim, a.rotary_dim, a.n_axes, a.positions, a.position_bytes = 5, 192, 64, 1, FAKE, 4
+        a.inv_freq, a.scale, a.eps, a.weight_dtype = FAKE, 1.0, 1e-6, B.DT_F32
+        for key, val in kw.items():
+            setattr(a, key, val)
+        return a
+
+    heads = dict(token=768, head=192, heads=4)
+    assert _write(M=0) == "OK" and _write(M=0, k=None, v=None, slots=None) == "OK"
+    assert name(B.lib().bsf8_cache_write(None, 0, None, None, None, 8, None, None)) == "INVALID_ARG"
+    for bad in (dict(cache=make_cache(heads=0)), dict(M=-1), dict(k=None), dict(v=None), dict(slots=None), dict(b=2),
+                dict(k=H(token=768, head=192, heads=3)), dict(v=H(token=768, head=192, heads=5)), dict(k=H(None, **heads)),
+                dict(k=H(dtype=B.DT_U8, **heads)), dict(rope=rope(M=4)), dict(rope=rope(head_dim=64)),
+                dict(rope=rope(k=H(**heads))), dict(rope=rope(k_out=H(**heads))), dict(rope=rope(q=H(**heads))),
+                dict(rope=rope(q_weight=FAKE)), dict(rope=rope(k_weight=FAKE, eps=-1.0)), dict(rope=rope(rotary_dim=194))):
+        assert _write(**bad) == "INVALID_ARG", bad
+    for bad in (dict(k=H(FAKE + 1, **heads)), dict(v=H(FAKE + 2, B.DT_F32, **heads)), dict(slots=FAKE + 4), dict(slots=FAKE + 2, b=4),
+                dict(rope=rope(k_weight=FAKE + 1))):
+        assert _write(**bad) == "ALIGNMENT", bad
+    assert _write(M=1 << 29) == "UNSUPPORTED" and _write(M=1 << 40) == "UNSUPPORTED"
+    assert _write(cache=make_cache(head_dim=72)) == "UNSUPPORTED"
+
+
+def _read(cache=None, B_=3, table=FAKE, ld=8, pages=8, starts=None, off=FAKE, R=20, k=H(token=768, head=192, heads=4),
+          v=H(token=768, head=192, heads=4)):
+    c = make_cache() if cache is None else cache
+    ref = lambda x: ctypes.byref(x) if x is not None else None
+    return name(B.lib().bsf8_cache_read(ref(c), B_, table, ld, pages, starts, off, R, ref(k), ref(v), None))
+
+
+def test_cache_read_refusals():
+    heads = dict(token=768, head=192, heads=4)
+    assert _read(B_=0) == "OK" and _read(R=0) == "OK"
+    assert name(B.lib().bsf8_cache_read(None, 0, None, 0, 0, None, None, 0, None, None, None)) == "INVALID_ARG"
+    for bad in (dict(B_=-1), dict(R=-1), dict(table=None), dict(ld=7), dict(pages=0), dict(pages=-1), dict(off=None),
+                dict(k=None, v=None), dict(k=H(None, **heads), v=None), dict(k=H(dtype=B.DT_F32, **heads)),
+                dict(v=H(token=768, head=192, heads=3)), dict(k=H(token=700, head=192, heads=4)), dict(k=H(token=0, head=192, heads=4)),
+                dict(ld=1 << 61), dict(k=H(dtype=B.DT_U8, **heads))):
+        assert _read(**bad) == "INVALID_ARG", bad
+    for bad in (dict(table=FAKE + 2), dict(off=FAKE + 1), dict(starts=FAKE + 2), dict(k=H(FAKE + 1, **heads))):
+        assert _read(**bad) == "ALIGNMENT", bad
+    for bad in (dict(B_=1 << 31), dict(pages=1 << 27, ld=1 << 27), dict(R=1 << 30)):
+        assert _read(**bad) == "UNSUPPORTED", bad
+
+
+def test_rope_axes():
+    assert B.rope_axes([2, 3, 1]) == bytes([0, 0, 1, 1, 1, 2])
+    assert B.rope_axes([24, 20, 20], interleaved=True)[:7] == bytes([0, 1, 2, 0, 1, 2, 0])
+    a = B.rope_axes([24, 20, 20], interleaved=True)
+    assert [a.count(i) for i in range(3)] == [24, 20, 20] and a[60:] == bytes(4)
+    assert B.rope_axes([5]) == bytes(5)
+    for bad in ([], [1] * 17, [3, -1]):
+        with pytest.raises(ValueError):
+            B.rope_axes(bad)
+    with pytest.raises(ValueError):
+        B.rope_axes([0, 4], interleaved=True)
