@@ -20,6 +20,7 @@ Entry points mirror ``include/bsf8.h``:
 * ``PagedKVCache(k, v, ...)``           a paged cache of keys and values: E4M3 codes with 1x128 scales, or bfloat16
 * ``cache_write(cache, k, v, slots, ...)``  keys (rotated on the way) and values into the cache
 * ``cache_read(cache, table, offsets, R)``  ranges of cached sequences back as plain rows
+* ``paged_attention(q, cache, table, lens)``  one new token per sequence over its cached keys and values
 """
 from __future__ import annotations
 
@@ -100,6 +101,12 @@ class RopeArgs(ctypes.Structure):
                 ("k_out", Heads), ("q_weight", _ptr), ("k_weight", _ptr), ("weight_dtype", _i32)]
 
 
+class AttentionArgs(ctypes.Structure):
+    """bsf8_attention_args."""
+    _fields_ = [("B", _i64), ("q", Heads), ("out", Heads), ("table", _ptr), ("ld_table", _i64), ("pages", _i64),
+                ("lens", _ptr), ("window", _i64), ("scale", _f64), ("lse", _ptr)]
+
+
 class Unit(ctypes.Structure):
     _fields_ = [("prefix", ctypes.c_char * 256), ("prefix_truncated", ctypes.c_int32), ("status", ctypes.c_int32),
                 ("weight", TensorDesc), ("scale_inv", TensorDesc), ("scale", TensorDesc),
@@ -169,6 +176,10 @@ EXPORTS = [
                                         _i32, ctypes.POINTER(RopeArgs), _ptr]),
     ("bsf8_cache_read", ctypes.c_int, [ctypes.POINTER(Cache), _i64, _ptr, _i64, _i64, _ptr, _ptr, _i64,
                                        ctypes.POINTER(Heads), ctypes.POINTER(Heads), _ptr]),
+    ("bsf8_attention_workspace_size", ctypes.c_int, [ctypes.POINTER(Cache), _i64, _i32, _i64,
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    ("bsf8_paged_attention", ctypes.c_int, [ctypes.POINTER(Cache), ctypes.POINTER(AttentionArgs), _ptr, ctypes.c_size_t,
+                                            _ptr]),
     ("bsf8_upcast", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_dense_workspace_size", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(ctypes.c_size_t)]),
@@ -1201,13 +1212,69 @@ def cache_read(cache: PagedKVCache, table, offsets, R: int, *, starts=None, out_
 
 
 
+def paged_attention(q, cache: PagedKVCache, table, lens, *, scale=None, window=0, lse=False, out=None, out_dtype=None,
+                    workspace=None):
+    """Attention of one new token per sequence: q [B, heads, D] (float32 or bfloat16) over the cached keys and values of
+    sequence b at positions 0 .. lens[b] - 1 (with ``window``, the last ``window`` of them), on the pages that table[b] names
+    (int32 [B, pages]); heads a multiple of the cache's, which neighbouring query heads share.  -> out [B, heads, D] of q's
+    type unless out_dtype or ``out`` says otherwise, or with ``lse`` (out, log-sum-exp float32 [B, heads]).
+
+    scale: D ** -0.5 by default.  A sequence of length 0 gives zeros and -inf; positions on pages outside the cache are left
+    out.  lens (int32 [B]) and table stay on the GPU, so a captured call follows their new values.  workspace: (tensor,
+    bytes) as attention_workspace_size says; without it a call that needs one takes its own from the allocator, so that
+    graphs captured on one stream may be replayed at the same time."""
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    idx = cache._idx
+    _same_device(idx, q=q, table=table, lens=lens, out=out, workspace=workspace[0] if workspace is not None else None)
+    if q.dim() != 3:
+        raise ValueError("q must be [B, heads, head_dim]")
+    B, H, D = q.shape
+    if D != cache.head_dim or H == 0 or H % cache.heads:
+        raise ValueError(f"q must be [B, heads, {cache.head_dim}] with heads a multiple of {cache.heads}")
+    a = AttentionArgs()
+    a.B, a.window, a.scale = B, window, D ** -0.5 if scale is None else scale
+    a.q = _heads("q", q, B, H, D, real)
+    a.lens = _vector("lens", lens, B, (torch.int32,))
+    a.pages, a.ld_table = _table("table", table, B)
+    a.table = table.data_ptr()
+    out, a.out = _turned("out", q, B, H, D, out, out_dtype, real)
+    sums = None
+    if lse:
+        sums = torch.empty((B, H), dtype=torch.float32, device=q.device)
+        a.lse = sums.data_ptr()
+    if workspace is not None:
+        ws, wsb = workspace
+        if wsb > (ws.numel() * ws.element_size() if ws is not None and ws.is_contiguous() else 0):
+            raise ValueError(f"the workspace must be a contiguous tensor of at least the {wsb} bytes given")
+    else:
+        wsb = attention_workspace_size(cache, B, H, a.pages) if B else 0
+        ws = torch.empty(wsb, dtype=torch.uint8, device=q.device) if wsb else None
+    _launch("paged_attention", idx, lib().bsf8_paged_attention, cache._ref, ctypes.byref(a),
+            ws.data_ptr() if ws is not None else None, wsb)
+    return (out, sums) if lse else out
+
+
+def attention_workspace_size(cache: PagedKVCache, B: int, heads: int, pages: int) -> int:
+    """Workspace bytes of paged_attention for B sequences of up to ``pages`` pages (they go by the device's compute units)."""
+    b = ctypes.c_size_t()
+    if _current()[0]() == cache._idx:
+        st = lib().bsf8_attention_workspace_size(cache._ref, B, heads, pages, ctypes.byref(b))
+    else:
+        with _torch().cuda.device(cache._idx):
+            st = lib().bsf8_attention_workspace_size(cache._ref, B, heads, pages, ctypes.byref(b))
+    if st != 0:
+        _check(st, "attention_workspace_size")
+    return b.value
+
+
 __all__ = ["BSF8Error", "BlockFP8Weight", "validate", "quant_act", "quant_glu", "glu_act", "quant_norm", "expert_plan", "linear_w8a16", "linear_w8a8",
            "linear_w8a8_dynamic", "linear_w8a8_noalloc", "linear_w8a8_epilogue", "linear_w8a8_experts",
            "ExpertsFP8Weight", "ARM_W8A8_EPILOGUE", "NOALLOC_SCRATCH_BYTES", "upcast",
            "linear_dense", "dense_workspace_size", "lib", "status_name", "ARM_W8A16", "ARM_W8A8", "ARM_DENSE",
            "ARM_W8A8_DYNAMIC",
            "EXPORTS", "LIB_PATH", "MAX_MEMBERS", "scales_kmajor", "PagedKVCache", "rope", "rope_axes", "cache_write",
-           "cache_read"]
+           "cache_read", "paged_attention", "attention_workspace_size"]
 
 
 READ_STREAM_SINK_WORDS = 2048  # BSF8_READ_STREAM_SINK_WORDS in include/bsf8.h

@@ -641,6 +641,58 @@ bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* t
   return launch_cache_read(c, B, table, ld_table, pages, starts, offsets, R, k, v, static_cast<hipStream_t>(stream));
 }
 
+// Shape checks that the attention and its workspace share; q_heads per key head whole.
+static bsf8_status attention_shape(const bsf8_cache& cache, const CacheDev& c, int64_t B, int32_t q_heads, int64_t pages) {
+  if (B < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (q_heads < 1 || q_heads % cache.heads) return fail(BSF8_E_INVALID_ARG, "%d query heads over %d", q_heads, cache.heads);
+  if (pages < 1) return fail(BSF8_E_INVALID_ARG, "table of %lld pages", (long long)pages);
+  if (B > INT32_MAX / q_heads || B * q_heads > (int64_t(1) << 24) - 1 || pages > (INT32_MAX - 4096) / cache.page_size ||
+      attention_tiles(c, B, q_heads, pages * cache.page_size) > INT32_MAX / 2)
+    return fail(BSF8_E_UNSUPPORTED, "B * heads, pages * page_size, or their product, too large");
+  return BSF8_OK;
+}
+
+bsf8_status bsf8_attention_workspace_size(const bsf8_cache* cache, int64_t B, int32_t q_heads, int64_t pages, size_t* bytes) {
+  if (bytes == nullptr) return fail(BSF8_E_INVALID_ARG, "null pointer");
+  *bytes = 0;
+  CacheDev c{};
+  bsf8_status st = cache_checks(cache, &c);
+  if (st == BSF8_OK) st = attention_shape(*cache, c, B, q_heads, pages);
+  if (st == BSF8_OK) *bytes = attention_workspace_bytes(c, B, q_heads, pages * cache->page_size);
+  return st;
+}
+
+bsf8_status bsf8_paged_attention(const bsf8_cache* cache, const bsf8_attention_args* args, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  CacheDev c{};
+  bsf8_status st = cache_checks(cache, &c);
+  if (st != BSF8_OK) return st;
+  if (args == nullptr) return fail(BSF8_E_INVALID_ARG, "null arguments");
+  const bsf8_attention_args& a = *args;
+  if (a.B < 0) return fail(BSF8_E_INVALID_ARG, "negative size");
+  if (a.window < 0) return fail(BSF8_E_INVALID_ARG, "window %lld (0 or more)", (long long)a.window);
+  if (!std::isfinite(a.scale)) return fail(BSF8_E_INVALID_ARG, "scale %g", a.scale);
+  if (a.B == 0) return BSF8_OK;
+  st = attention_shape(*cache, c, a.B, a.q.heads, a.pages);
+  if (st != BSF8_OK) return st;
+  HeadsDev q{}, out{};
+  st = heads_checks("q", a.q, a.B, cache->head_dim, -1, false, &q);
+  if (st == BSF8_OK) st = heads_checks("out", a.out, a.B, cache->head_dim, a.q.heads, true, &out);
+  if (st == BSF8_OK) st = table_checks(*cache, a.B, a.table, a.ld_table, a.pages);
+  if (st != BSF8_OK) return st;
+  if (a.lens == nullptr) return fail(BSF8_E_INVALID_ARG, "null lens");
+  if (reinterpret_cast<uintptr_t>(a.lens) % 4 || reinterpret_cast<uintptr_t>(a.lse) % 4)
+    return fail(BSF8_E_ALIGNMENT, "lens or lse not element aligned");
+  const size_t need = attention_workspace_bytes(c, a.B, a.q.heads, a.pages * cache->page_size);
+  if (need) {
+    if (workspace == nullptr || workspace_bytes < need)
+      return fail(BSF8_E_WORKSPACE, "%zu bytes of workspace needed, %zu given", need, workspace ? workspace_bytes : size_t(0));
+    if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(BSF8_E_ALIGNMENT, "workspace not 256-byte aligned");
+  }
+  return launch_attention(c, q, out, a.B, a.table, a.ld_table, a.pages, a.lens, a.window, a.scale, a.lse, workspace,
+                          static_cast<hipStream_t>(stream));
+}
+
 // Workspace of the two-step form of bsf8_linear_w8a8_dynamic: the codes (row
 // pitch K rounded up to 16 bytes), the K-major scales, then the W8A8 call's own
 // workspace, each from a 256-byte boundary.

@@ -116,6 +116,12 @@ bsf8_status launch_cache_read(const CacheDev& cache, int64_t B, const int32_t* t
                               const int32_t* starts, const int32_t* offsets, int64_t R, const HeadsDev& k,
                               const HeadsDev& v, hipStream_t stream);
 
+int64_t attention_tiles(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound);   // an upper bound
+size_t attention_workspace_bytes(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound);
+bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDev& out, int64_t B, const int32_t* table,
+                             int64_t ld_table, int64_t pages, const int32_t* lens, int64_t window, double scale, float* lse,
+                             void* ws, hipStream_t stream);
+
 size_t w8a16_workspace_bytes(const WeightDev& w, int64_t M);
 bsf8_status launch_w8a16(const WeightDev& w, bool aligned, const void* x, bool x_bf16, int64_t M,
                          int64_t ldx, void* y, bool y_bf16, int64_t ldy, void* ws, size_t ws_bytes,

@@ -662,6 +662,49 @@ bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* t
                             const bsf8_heads* v_out, void* stream);
 
 /*
+ * bsf8_paged_attention -- one new token per sequence over its cached keys and values
+ * (the token's own among them).  For sequence b with n = lens[b], query head h,
+ * and key head h / (q.heads / cache->heads):
+ *   s_t = scale * sum_d q[b, h, d] * k_t[d],   t in [max(0, n - window), n)  (window 0: all)
+ *   out[b, h] = sum_t exp(s_t) v_t / sum_t exp(s_t),    lse[b, h] = log(sum_t exp(s_t))
+ * in F32 with a running maximum; BF16 and E4M3 values enter the products exactly, an
+ * F32 query as three BF16 terms that hold all of its bits.  The softmax weights enter
+ * their product with the values as two BF16 terms (17 bits or more; three, 24 bits,
+ * where q or out is F32).  The sums' order depends on the batch and on the device's
+ * compute units, never on timing.
+ * lens  : device int32 [B]; clamped to [0, pages * page_size].  A sequence with no
+ *         position (length 0) has out = 0 and lse = -inf.
+ * table : device int32 [B, pages], row pitch ld_table.  A position on a page outside
+ *         [0, n_pages) is left out of the sums.  What rows past the length hold (NaN
+ *         too) does not reach the result.
+ * q, out : [B, heads] F32 or BF16; heads a multiple of the cache's.  out may not
+ *         overlap an input.
+ * lse   : device F32 [B, heads] contiguous, or NULL.
+ * workspace : bsf8_attention_workspace_size bytes (256-byte aligned; may be NULL when
+ *         that is 0); nothing in it needs clearing.  Calls that overlap in time must
+ *         not share one.
+ * Nothing of the lengths is read on the host: a captured call follows new lengths and
+ * tables.
+ * Errors: INVALID_ARG, ALIGNMENT, UNSUPPORTED (pages * page_size beyond 2^31 - 4097, B *
+ * heads beyond 2^24 - 1, or 128-token tiles of all sequences and key heads beyond 2^30),
+ * WORKSPACE, DEVICE.
+ */
+typedef struct bsf8_attention_args {
+  int64_t B;
+  bsf8_heads q, out;
+  const int32_t* table;
+  int64_t ld_table, pages;
+  const int32_t* lens;
+  int64_t window;
+  double scale;
+  float* lse;
+} bsf8_attention_args;
+bsf8_status bsf8_attention_workspace_size(const bsf8_cache* cache, int64_t B, int32_t q_heads, int64_t pages,
+                                          size_t* bytes);
+bsf8_status bsf8_paged_attention(const bsf8_cache* cache, const bsf8_attention_args* args, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
+/*
  * bsf8_linear_w8a8_dynamic -- the W8A8 arm on unquantized activations: x is
  * quantized per token in 1x128 groups exactly as bsf8_quant_act does (amax /
  * 448, E4M3 round-to-nearest-even, saturating) and the product is then that

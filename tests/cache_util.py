@@ -94,3 +94,58 @@ def rope_tolerance(want, x, scale=1.0, weight=None, eps=1e-6, bf16=False):
 
 def to_f64(x):
     return x.float().cpu().numpy().astype(np.float64)
+
+
+def make_table(g, lens, page, pages, columns=None, behind=-1):
+    """Pages of each sequence in random order; entries behind its last page are ``behind``."""
+    need = [-(-n // page) for n in lens]
+    table = np.full((len(lens), columns or max(1, max(need))), behind, np.int32)
+    perm = g.permutation(pages)[:sum(need)]
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = perm[at:at + n]
+        at += n
+    return table
+
+
+def attention64(q, values, table, lens, page, window, scale, n_pages):
+    """(out, lse, tolerance of out without its own rounding, tolerance of lse) in 64 bits.
+
+    What F32 loses, per head row (u = 2^-24; an F32 sum of N terms in any order and rounding direction is off by at most
+    2 N u of the sum of their magnitudes, which also covers what a matrix instruction does inside):
+      a logit: its D products and scales, at most ds = 2 (3 D + 8) u scale sum |q k| (three terms of an F32 query);
+      a weight: exp(2 ds) - 1 against the exact ones' (its own logit's and the maximum's, which cancels in the quotient
+        but for its rounding), the exponent's rounding, 2 u times its size in base 2, and 4 u of the hardware's exp2;
+      its split into two BF16 terms: 2^-16;
+      the sums over n tokens, 2 n u of sum p |v|, once for the numerator and once for the denominator, and some 64
+        roundings of rescaling and joining."""
+    K, V = values
+    B, H, D = q.shape
+    kv = K.shape[2]
+    G = H // kv
+    u = 2.0 ** -24
+    out, lse = np.zeros((B, H, D)), np.full((B, H), -np.inf)
+    tol, tol_lse = np.zeros((B, H, D)), np.zeros((B, H))
+    for b, n in enumerate(lens):
+        n = min(max(int(n), 0), table.shape[1] * page)
+        pos = np.arange(max(0, n - window) if window else 0, n)
+        pg = table[b, pos // page] if n else np.zeros(0, int)
+        ok = (pg >= 0) & (pg < n_pages)
+        pos, pg = pos[ok], pg[ok]
+        if len(pos) == 0:
+            continue
+        for h in range(kv):
+            k, v = K[pg, pos % page, h], V[pg, pos % page, h]
+            rows = slice(h * G, (h + 1) * G)
+            s = scale * (q[b, rows] @ k.T)
+            m = s.max(-1, keepdims=True)
+            p = np.exp(s - m)
+            z = p.sum(-1, keepdims=True)
+            out[b, rows] = p @ v / z
+            lse[b, rows] = (m + np.log(z))[:, 0]
+            ds = 2 * (3 * D + 8) * u * abs(scale) * (np.abs(q[b, rows]) @ np.abs(k).T).max(-1)
+            size = np.abs(s / np.log(2)).max(-1)
+            rel = np.expm1(2 * ds) + (4 * size + 8) * u + 2.0 ** -16 + (4 * len(pos) + 64) * u
+            tol[b, rows] = rel[:, None] * (p @ np.abs(v) / z)
+            tol_lse[b, rows] = ds + (2 * len(pos) + 64 + 4 * size) * u
+    return out, lse, tol, tol_lse
