@@ -27,7 +27,7 @@
 // The blocks find their ranges by a sum over the lengths, so nothing is read on the host.
 #include <hip/hip_runtime.h>
 
-#include <climits>
+#include <type_traits>
 
 #include "bsf8_channels.h"
 #include "bsf8_fused.h"
@@ -60,10 +60,10 @@ struct AttentionDev {
   int32_t items;        // of a sequence: key heads x row tiles
   int32_t window;       // 0: none
   int32_t bound;        // pages * page_size
-  int32_t uniform;      // 16 tokens that start at a multiple of 16 are on one page
-  int32_t scale_vec;    // four of a page's scales that follow each other are one aligned load
   int32_t blocks;       // grid of the first kernel
-  float scale;          // log2(e) included
+  int32_t negative;     // the scale is: queries change their sign, and `scale` is its size
+  float scale;          // log2(e) included; not zero
+  double natural;       // the size of the scale
 };
 
 __device__ __forceinline__ int first_token(const AttentionDev& a, int n) { return a.window ? max(0, n - a.window) : 0; }
@@ -137,8 +137,8 @@ __device__ __forceinline__ float sum_of_groups(float x) {
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Four channels of a head's result: o / l, and with channel 0 the log of the sum (natural, from
-// base 2); zeros and -inf where there was no token.
+// Four channels of a head's result: o / l, and with channel 0 the log of the sum, the maximum's
+// part of it in F64 (it can be large); zeros and -inf where there was no token.
 __device__ __forceinline__ void store_result(const AttentionDev& a, int b, int head, int ch, f4 o, float m, float l) {
   const bool none = m == -INFINITY;
   float v[4];
@@ -167,7 +167,7 @@ __device__ __forceinline__ void store_result(const AttentionDev& a, int b, int h
     }
   }
   if (a.lse && ch == 0)
-    a.lse[int64_t(b) * a.q.heads + head] = none ? -INFINITY : 0.69314718055994531f * m + logf(l);
+    a.lse[int64_t(b) * a.q.heads + head] = none ? -INFINITY : static_cast<float>(a.natural * double(m) + double(logf(l)));
 }
 
 __device__ __forceinline__ v8bf as_bf16(u4 v) { return __builtin_bit_cast(v8bf, v); }
@@ -187,10 +187,55 @@ __device__ __forceinline__ void split(const float (&x)[8], v8bf (&t)[N]) {
   }
 }
 
+// Queries of 16 heads: the B operand, in the channel order of the keys' pieces; zeros for heads
+// past `rows` and channels past head_dim.  All loads go out before any is used.
+template <bool E4M3, int QS, int QT>
+__device__ __forceinline__ void load_queries(const AttentionDev& a, int b, int head0, int rows, v8bf (&qf)[QS][QT]) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15, D = a.c.head_dim;
+  const int64_t base = int64_t(b) * a.q.token + int64_t(head0 + min(i16, rows - 1)) * a.q.head;
+  const auto channel = [&](int s) { return E4M3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8; };
+  float x[QS][8];
+  if (a.q.vec) {
+    if (QT == 1 || a.q.bf16) {
+      u4 v[QS];
+#pragma unroll
+      for (int s = 0; s < QS; ++s)
+        v[s] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(a.q.p) + base + min(channel(s), D - 8));
+#pragma unroll
+      for (int s = 0; s < QS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = __uint_as_float((e & 1) ? v[s][e >> 1] & 0xFFFF0000u : v[s][e >> 1] << 16);
+    } else {
+      f4 v[QS][2];
+#pragma unroll
+      for (int s = 0; s < QS; ++s)
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          v[s][y] = reinterpret_cast<const f4*>(static_cast<const float*>(a.q.p) + base + min(channel(s), D - 8))[y];
+#pragma unroll
+      for (int s = 0; s < QS; ++s)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[s][e] = v[s][e >> 2][e & 3];
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < QS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[s][e] = load_real(a.q.p, a.q.bf16, base + min(channel(s), D - 8) + e);
+  }
+#pragma unroll
+  for (int s = 0; s < QS; ++s) {
+    const bool there = i16 < rows && channel(s) < D;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[s][e] = !there ? 0.f : a.negative ? -x[s][e] : x[s][e];
+    split<QT>(x[s], qf[s]);
+  }
+}
+
 // Blocks per compute unit (waves per SIMD) that the registers allow.
 template <bool E4M3, int NG>
 struct Shape {
-  static constexpr int kBlocksPerCu = NG == 2 ? 1 : 2;
+  static constexpr int kBlocksPerCu = NG == 2 ? 2 : 3;
   static constexpr int kChannels = NG * 128;
   static constexpr int kSlot = kRows * kChannels + 2 * kRows;   // floats of a partial result
 };
@@ -198,11 +243,19 @@ struct Shape {
 // NG: 128-channel groups of a head.  QT: BF16 terms of a query (1: BF16 queries, 3: F32);
 // PT: of a softmax weight.  A weight in one term would be off by 2^-9 of itself, as much as
 // the rounding of a BF16 output; two leave 2^-17, three 2^-25.
-template <bool E4M3, int NG, int QT, int PT>
+// PAGES: kAny, each lane looks up a token's page; kHalves, pages are a multiple of 16 rows, so
+// that each half of a wave's 32 tokens is on one page, whose rows all exist: addresses are
+// scalar, and rows past the length are read and left out; kHalvesWide, also four scales are
+// one load.  (A choice inside the kernel would be a branch around loads, and where its sides
+// meet the compiler waits for all of them.)
+enum Pages { kAny, kHalves, kHalvesWide };
+template <bool E4M3, int NG, int QT, int PT, int PAGES>
 __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPerCu)) void attention_kernel(AttentionDev a) {
   using S = Shape<E4M3, NG>;
   constexpr int KV = E4M3 ? 2 * NG : 4 * NG;   // 16-byte key loads per token and lane
+  constexpr int QS = 4 * NG;                   // query pieces: 32 channels each
   constexpr int PITCH = S::kChannels + 4;
+  constexpr bool PAGES16 = PAGES != kAny;
   __shared__ float lds_o[kWaves][kRows][PITCH];
   __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
 
@@ -220,17 +273,18 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
   int n_tiles = tiles_of(a, n, first);
   int item = (t_begin - before * a.items) / n_tiles, j = (t_begin - before * a.items) - item * n_tiles;
 
-  // byte offsets of a lane's pieces within a row; channels past head_dim are read as others
-  // that exist (queries are zero there, and outputs are not stored)
+  // byte offsets of a lane's pieces within a row, with its token's (the key's i16, the first
+  // value's 4 g); channels past head_dim are read as others that exist (queries are zero there,
+  // and outputs are not stored)
   uint32_t k_off[KV], v_off[NG];
 #pragma unroll
   for (int s = 0; s < KV; ++s) {
     const int ch = E4M3 ? min(s * 64 + g * 16, D - 16) : min(s * 32 + g * 8, D - 8);
-    k_off[s] = uint32_t(i16) * uint32_t(a.c.row) + uint32_t(ch) * (E4M3 ? 1 : 2);
+    k_off[s] = (PAGES16 ? uint32_t(i16) * uint32_t(a.c.row) : 0) + uint32_t(ch) * (E4M3 ? 1 : 2);
   }
 #pragma unroll
   for (int c = 0; c < NG; ++c)
-    v_off[c] = uint32_t(4 * g) * uint32_t(a.c.row) + uint32_t(min(c * 128 + i16 * 8, D - 8)) * (E4M3 ? 1 : 2);
+    v_off[c] = (PAGES16 ? uint32_t(4 * g) * uint32_t(a.c.row) : 0) + uint32_t(min(c * 128 + i16 * 8, D - 8)) * (E4M3 ? 1 : 2);
 
   for (int t = t_begin; t < t_end;) {
     const int j_end = min(n_tiles, j + (t_end - t));
@@ -238,22 +292,14 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     const int rows = min(kRows, a.G - row0), head0 = h * a.G + row0;
     const int start = first_token(a, n), stop = min(n, (first + j_end) * kTile);
 
-    // queries: the B operand, in the channel order of the keys' pieces
-    v8bf qf[E4M3 ? 2 * KV : KV][QT];
-#pragma unroll
-    for (int s = 0; s < (E4M3 ? 2 * KV : KV); ++s) {
-      const int ch = E4M3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
-      float x[8];
-      load_vec(a.q.p, a.q.bf16, int64_t(b) * a.q.token + int64_t(head0 + i16) * a.q.head + ch, i16 < rows && ch < D ? 8 : 0,
-               a.q.vec, x);
-      split<QT>(x, qf[s]);
-    }
+    v8bf qf[QS][QT];
+    load_queries<E4M3, QS, QT>(a, b, head0, rows, qf);
 
     const uint8_t* k_base = a.c.k + int64_t(h) * a.c.head;
     const uint8_t* v_base = a.c.v + int64_t(h) * a.c.head;
     const float* ks_base = E4M3 ? a.c.k_scale + int64_t(h) * a.c.s_head : nullptr;
     const float* vs_base = E4M3 ? a.c.v_scale + int64_t(h) * a.c.s_head : nullptr;
-    ConstInts table = (ConstInts)(a.table + int64_t(b) * a.ld_table);
+    const int32_t* table = a.table + int64_t(b) * a.ld_table;
 
     f4 o[NG][8];
 #pragma unroll
@@ -262,82 +308,88 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       for (int x = 0; x < 8; ++x) o[c][x] = f4{0.f, 0.f, 0.f, 0.f};
     float m = -INFINITY, l = 0.f;
 
-    // ---- the pages of a wave's 32 tokens: two halves on a page each, or a token per lane
-    struct Where {
-      uint32_t mask;        // bit x: token x of the 32 exists
-      int fast;             // both halves' pages are named by e0 / e1, r0 / r1 (page and row of their first token)
-      int e0, e1, r0, r1;
-      int le, lr;           // page and row of token lane & 31
+    // ---- where a wave's 32 tokens lie.  Entries of the table are asked for two tiles ahead
+    struct Entries {
+      int e0, e1;           // pages of the halves; or e0: page of token lane & 31
     };
-    const auto locate = [&](int pos, Where& w) {
+    const auto entries = [&](int pos) {
       // (columns past the table's end are not read: tokens there do not exist)
-      if (a.uniform) {
-        const uint32_t p0 = a.c.page_of(uint32_t(pos)), p1 = a.c.page_of(uint32_t(pos + 16));
-        w.r0 = pos - int(p0) * a.c.page_size;
-        w.r1 = pos + 16 - int(p1) * a.c.page_size;
-        w.e0 = table[min(int(p0), a.pages - 1)];
-        w.e1 = table[min(int(p1), a.pages - 1)];
-        w.fast = pos >= start && pos + kWaveTokens <= stop && uint32_t(w.e0) < uint32_t(a.c.n_pages) &&
-                 uint32_t(w.e1) < uint32_t(a.c.n_pages);
-        w.le = (lane & 16) ? w.e1 : w.e0;
-        w.lr = ((lane & 16) ? w.r1 : w.r0) + i16;
+      Entries e;
+      if (PAGES16) {
+        ConstInts at = (ConstInts)table;
+        e.e0 = at[min(int(a.c.page_of(uint32_t(pos))), a.pages - 1)];
+        e.e1 = at[min(int(a.c.page_of(uint32_t(pos + 16))), a.pages - 1)];
       } else {
-        const uint32_t p = a.c.page_of(uint32_t(pos + (lane & 31)));
-        w.fast = 0;
-        w.e0 = w.e1 = w.r0 = w.r1 = 0;
-        w.le = a.table[int64_t(b) * a.ld_table + min(int(p), a.pages - 1)];
-        w.lr = pos + (lane & 31) - int(p) * a.c.page_size;
+        e.e0 = table[min(int(a.c.page_of(uint32_t(pos + (lane & 31)))), a.pages - 1)];
+        e.e1 = 0;
       }
-      w.mask = ~0u;
-      if (!w.fast) {
+      return e;
+    };
+    struct Where {
+      uint32_t mask;              // bit x: token x of the 32 exists
+      int64_t at[2], s_at[2];     // of the halves: bytes, elements of scales
+      int le, lr;                 // or page and row of token lane & 31
+    };
+    const auto locate = [&](int pos, Entries e, Where& w) {
+      if (PAGES16) {
+        const auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
+        w.mask = below(stop - pos) & ~below(start - pos);
+        // a page outside the cache: page 0 is read in its place and left out
+        if (uint32_t(e.e0) >= uint32_t(a.c.n_pages)) {
+          e.e0 = 0;
+          w.mask &= 0xFFFF0000u;
+        }
+        if (uint32_t(e.e1) >= uint32_t(a.c.n_pages)) {
+          e.e1 = 0;
+          w.mask &= 0xFFFFu;
+        }
+        const int r0 = pos - int(a.c.page_of(uint32_t(pos))) * a.c.page_size;
+        const int r1 = pos + 16 - int(a.c.page_of(uint32_t(pos + 16))) * a.c.page_size;
+        w.at[0] = int64_t(e.e0) * a.c.page + int64_t(r0) * a.c.row;
+        w.at[1] = int64_t(e.e1) * a.c.page + int64_t(r1) * a.c.row;
+        if (E4M3) {
+          w.s_at[0] = int64_t(e.e0) * a.c.s_page + int64_t(r0) * a.c.s_row;
+          w.s_at[1] = int64_t(e.e1) * a.c.s_page + int64_t(r1) * a.c.s_row;
+        }
+      } else {
         const int tok = pos + (lane & 31);
+        w.le = e.e0;
+        w.lr = tok - int(a.c.page_of(uint32_t(tok))) * a.c.page_size;
         const bool there = tok >= start && tok < stop && uint32_t(w.le) < uint32_t(a.c.n_pages);
         w.mask = uint32_t(__ballot(there));
-        if (!there) w.le = w.lr = 0;   // row 0 of page 0 is read in its place and left out
+        if (!there) w.le = w.lr = 0;
       }
     };
 
     u4 kr[2][KV];
     float ksc[NG][2][4], vsc[NG][2][4];
     const auto load_keys = [&](const Where& w) {
-      if (w.fast) {
-        const uint8_t* p0 = k_base + int64_t(w.e0) * a.c.page + int64_t(w.r0) * a.c.row;
-        const uint8_t* p1 = k_base + int64_t(w.e1) * a.c.page + int64_t(w.r1) * a.c.row;
 #pragma unroll
-        for (int s = 0; s < KV; ++s) {
-          if (s * (E4M3 ? 64 : 32) >= D) continue;
-          kr[0][s] = *reinterpret_cast<const u4*>(p0 + k_off[s]);
-          kr[1][s] = *reinterpret_cast<const u4*>(p1 + k_off[s]);
-        }
-      } else {
+      for (int x = 0; x < 2; ++x) {
+        const uint8_t* p = k_base;
+        if (PAGES16) p += w.at[x];
+        else p += int64_t(__shfl(w.le, 16 * x + i16, 64)) * a.c.page + int64_t(__shfl(w.lr, 16 * x + i16, 64)) * a.c.row;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int e = __shfl(w.le, 16 * x + i16, 64), r = __shfl(w.lr, 16 * x + i16, 64);
-          const uint8_t* p = k_base + int64_t(e) * a.c.page + int64_t(r - i16) * a.c.row;
-#pragma unroll
-          for (int s = 0; s < KV; ++s) {
-            if (s * (E4M3 ? 64 : 32) >= D) continue;
-            kr[x][s] = *reinterpret_cast<const u4*>(p + int64_t(k_off[s]));
-          }
-        }
+        for (int s = 0; s < KV; ++s)
+          kr[x][s] = *reinterpret_cast<const u4*>(p + k_off[s]);
       }
     };
     // scales of a lane's eight tokens
     const auto load_scales = [&](const Where& w, const float* base, float (&sc)[NG][2][4]) {
 #pragma unroll
-      for (int c = 0; c < NG; ++c) {
+      for (int c = 0; c < NG; ++c)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float* p = base + int64_t(c) * a.c.s_group;
-          if (w.fast) {
-            p += int64_t(x ? w.e1 : w.e0) * a.c.s_page + int64_t(x ? w.r1 : w.r0) * a.c.s_row;
-            if (a.scale_vec) {
+          if (PAGES16) {
+            p += w.s_at[x];
+            if (PAGES == kHalvesWide) {
               const f4 v = *reinterpret_cast<const f4*>(p + 4 * g);
 #pragma unroll
               for (int r = 0; r < 4; ++r) sc[c][x][r] = v[r];
             } else {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) sc[c][x][r] = p[int64_t(4 * g + r) * a.c.s_row];
+              for (int r = 0; r < 4; ++r) sc[c][x][r] = p[uint32_t(4 * g + r) * uint32_t(a.c.s_row)];
             }
           } else {
 #pragma unroll
@@ -347,52 +399,53 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
             }
           }
         }
-      }
     };
-    u4 vr[NG][8];   // (E4M3: the first two words)
+    constexpr int VW = E4M3 ? 2 : 4;
+    uint32_t vr[NG][8][VW];
     const auto load_values = [&](const Where& w) {
-      const auto piece = [&](const uint8_t* p, u4& v) {
-        if (E4M3) {
-          const u2 x = *reinterpret_cast<const u2*>(p);
-          v[0] = x[0];
-          v[1] = x[1];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint8_t* p = v_base;
+        if (PAGES16) {
+          p += w.at[e >> 2] + int64_t(e & 3) * a.c.row;
         } else {
-          v = *reinterpret_cast<const u4*>(p);
-        }
-      };
-      if (w.fast) {
-        const uint8_t* p0 = v_base + int64_t(w.e0) * a.c.page + int64_t(w.r0) * a.c.row;
-        const uint8_t* p1 = v_base + int64_t(w.e1) * a.c.page + int64_t(w.r1) * a.c.row;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-#pragma unroll
-          for (int c = 0; c < NG; ++c)
-            piece((e < 4 ? p0 : p1) + int64_t(e & 3) * a.c.row + v_off[c], vr[c][e]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
           const int tok = (e >> 2) * 16 + 4 * g + (e & 3);
-          const int pe = __shfl(w.le, tok, 64), r = __shfl(w.lr, tok, 64);
-          const uint8_t* p = v_base + int64_t(pe) * a.c.page + int64_t(r - 4 * g) * a.c.row;
+          p += int64_t(__shfl(w.le, tok, 64)) * a.c.page + int64_t(__shfl(w.lr, tok, 64)) * a.c.row;
+        }
 #pragma unroll
-          for (int c = 0; c < NG; ++c)
-            piece(p + int64_t(v_off[c]), vr[c][e]);
+        for (int c = 0; c < NG; ++c) {
+          if (E4M3) {
+            const u2 v = *reinterpret_cast<const u2*>(p + v_off[c]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) vr[c][e][x] = v[x];
+          } else {
+            const u4 v = *reinterpret_cast<const u4*>(p + v_off[c]);
+#pragma unroll
+            for (int x = 0; x < VW; ++x) vr[c][e][x] = v[x];
+          }
         }
       }
     };
 
     int pos = (first + j) * kTile + wave * kWaveTokens;
-    Where w, next;
+    Where w;
+    Entries ahead;
     if (pos < stop) {
-      locate(pos, w);
-      load_keys(w);
+      locate(pos, entries(pos), w);
       if (E4M3) load_scales(w, ks_base, ksc);
-      load_values(w);
+      load_keys(w);
       if (E4M3) load_scales(w, vs_base, vsc);
+      load_values(w);
+      ahead = entries(pos + kTile);
     }
-    for (; pos < stop; pos += kTile) {
-      const bool more = pos + kTile < stop;
-      if (more) locate(pos + kTile, next);
+    // one tile's products, the next one's loads (not for the last: apart, for the same reason)
+    const auto tile = [&](auto last) {
+      constexpr bool LAST = decltype(last)::value;
+      const uint32_t mask = w.mask;
+      if (!LAST) {
+        locate(pos + kTile, ahead, w);
+        ahead = entries(pos + 2 * kTile);
+      }
 
       // ---- logits of 8 tokens and one head per lane
       float s[8];
@@ -403,7 +456,6 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
         for (int c = 0; c < NG; ++c) acc[c] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < KV; ++p) {
-          if (p * (E4M3 ? 64 : 32) >= D) continue;
           constexpr int PARTS = E4M3 ? 2 : 1;
 #pragma unroll
           for (int y = 0; y < PARTS; ++y) {
@@ -420,27 +472,28 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
             v *= ksc[0][x][r];
             if (NG == 2) v = fmaf(acc[NG - 1][r], ksc[NG - 1][x][r], v);
           }
-          s[4 * x + r] = v * a.scale;
+          s[4 * x + r] = v;
         }
       }
-      if (more) {
-        load_keys(next);
-        if (E4M3) load_scales(next, ks_base, ksc);
+      if (!LAST) {
+        if (E4M3) load_scales(w, ks_base, ksc);
+        load_keys(w);
       }
-      if (w.mask != ~0u) {
-        const uint32_t mine = w.mask >> (4 * g);
+      if (mask != ~0u) {
+        const uint32_t mine = mask >> (4 * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (!((mine >> ((e >> 2) * 16 + (e & 3))) & 1)) s[e] = -INFINITY;
       }
 
-      // ---- running maximum and sum
+      // ---- running maximum and sum, of logits that are not scaled yet: a difference of two
+      // that matter is exact, and its scaling rounds it relative to the difference
       float top = s[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
       top = fmaxf(m, max_of_groups(top));
       if (__ballot(top > m)) {
-        const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m - top);
+        const float f = top == -INFINITY ? 1.f : __builtin_amdgcn_exp2f((m - top) * a.scale);
         l *= f;
 #pragma unroll
         for (int c = 0; c < NG; ++c)
@@ -452,13 +505,13 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       float p[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        p[e] = __builtin_amdgcn_exp2f(s[e] - ref);
+        p[e] = __builtin_amdgcn_exp2f((s[e] - ref) * a.scale);
         l += p[e];
       }
 
       // ---- values: rows of tokens that do not exist may hold anything
-      if (w.mask != ~0u) {
-        const uint32_t mine = w.mask >> (4 * g);
+      if (mask != ~0u) {
+        const uint32_t mine = mask >> (4 * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const bool there = (mine >> ((e >> 2) * 16 + (e & 3))) & 1;
@@ -466,7 +519,7 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
           for (int c = 0; c < NG; ++c) {
             if (E4M3 && !there) vsc[c][e >> 2][e & 3] = 0.f;
 #pragma unroll
-            for (int x = 0; x < (E4M3 ? 2 : 4); ++x) vr[c][e][x] = there ? vr[c][e][x] : 0u;
+            for (int x = 0; x < VW; ++x) vr[c][e][x] = there ? vr[c][e][x] : 0u;
           }
         }
       }
@@ -474,7 +527,7 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       if (E4M3) {
 #pragma unroll
         for (int c = 0; c < NG; ++c) {
-            float ps[8];
+          float ps[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) ps[e] = p[e] * vsc[c][e >> 2][e & 3];
           split<PT>(ps, pt[c]);
@@ -488,10 +541,11 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
         for (int x = 0; x < 4; ++x) {   // channels 2 x and 2 x + 1 of each lane's eight
           uint32_t pair[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            pair[e] = E4M3 ? __builtin_bit_cast(uint32_t, (x & 1) ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, true)
-                                                                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, false))
-                           : vr[c][e][x];
+          for (int e = 0; e < 8; ++e) {
+            if constexpr (!E4M3) pair[e] = vr[c][e][x];
+            else if (x & 1) pair[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, true));
+            else pair[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, false));
+          }
           u4 lo, hi;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -505,12 +559,13 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
           }
         }
       }
-      if (more) {
-        load_values(next);
-        if (E4M3) load_scales(next, vs_base, vsc);
-        w = next;
+      if (!LAST) {
+        if (E4M3) load_scales(w, vs_base, vsc);
+        load_values(w);
       }
-    }
+    };
+    for (; pos + kTile < stop; pos += kTile) tile(std::false_type{});
+    if (pos < stop) tile(std::true_type{});
 
     // ---- the waves' parts of the segment
     l = sum_of_groups(l);
@@ -522,7 +577,7 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     float top = lds_m[0][i16];
 #pragma unroll
     for (int x = 1; x < kWaves; ++x) top = fmaxf(top, lds_m[x][i16]);
-    const float mine = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    const float mine = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale);
 #pragma unroll
     for (int c = 0; c < NG; ++c)
 #pragma unroll
@@ -548,7 +603,7 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       for (int y = 1; y < kWaves; ++y) all_m = fmaxf(all_m, lds_m[y][row]);
 #pragma unroll
       for (int y = 0; y < kWaves; ++y)
-        all_l += all_m == -INFINITY ? 0.f : lds_l[y][row] * __builtin_amdgcn_exp2f(lds_m[y][row] - all_m);
+        all_l += all_m == -INFINITY ? 0.f : lds_l[y][row] * __builtin_amdgcn_exp2f((lds_m[y][row] - all_m) * a.scale);
       if (whole) {
         store_result(a, b, head0 + row, ch, v, all_m, all_l);
       } else {
@@ -607,12 +662,12 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) top = fmaxf(top, pm[y]);
     if (top == -INFINITY) continue;
-    float f = __builtin_amdgcn_exp2f(m - top);
+    float f = __builtin_amdgcn_exp2f((m - top) * a.scale);
     l *= f;
     o *= f;
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) {
-      f = __builtin_amdgcn_exp2f(pm[y] - top);
+      f = __builtin_amdgcn_exp2f((pm[y] - top) * a.scale);
       if (f == 0.f) continue;   // (a part without a token)
       l = fmaf(pl[y], f, l);
       o += v[y] * f;
@@ -633,7 +688,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a
   if (top != -INFINITY) {
 #pragma unroll
     for (int y = 0; y < GROUPS; ++y) {
-      const float f = __builtin_amdgcn_exp2f(lds_m[y] - top);
+      const float f = __builtin_amdgcn_exp2f((lds_m[y] - top) * a.scale);
       sum = fmaf(lds_l[y], f, sum);
       v += *reinterpret_cast<const f4*>(&lds_o[y][ch]) * f;
     }
@@ -664,11 +719,18 @@ int64_t grid_blocks(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound
 }
 
 template <bool E4M3, int NG>
-void launch_attention_kernel(const AttentionDev& a, bool f32, hipStream_t stream) {
-  if (f32)
-    hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3>), dim3(unsigned(a.blocks)), dim3(kThreads), 0, stream, a);
-  else
-    hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2>), dim3(unsigned(a.blocks)), dim3(kThreads), 0, stream, a);
+void launch_attention_kernel(const AttentionDev& a, bool f32, bool scale_vec, hipStream_t stream) {
+  const dim3 grid{unsigned(a.blocks)}, block{kThreads};
+  if (a.c.page_size % 16) {
+    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kAny>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kAny>), grid, block, 0, stream, a);
+  } else if (!E4M3 || scale_vec) {   // (BF16: no scales)
+    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kHalvesWide>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kHalvesWide>), grid, block, 0, stream, a);
+  } else if constexpr (E4M3) {
+    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kHalves>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kHalves>), grid, block, 0, stream, a);
+  }
 }
 
 }  // namespace
@@ -702,17 +764,18 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   a.items = c.heads * a.row_tiles;
   a.bound = int32_t(pages * c.page_size);
   a.window = window >= a.bound ? 0 : int32_t(window);
-  a.uniform = c.page_size % 16 == 0 ? 1 : 0;
-  a.scale_vec = c.e4m3 && c.s_row == 1 && ((c.s_page | c.s_head | c.s_group) & 3) == 0 &&
-                        ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15) == 0
-                    ? 1 : 0;
+  const bool scale_vec = c.s_row == 1 && ((c.s_page | c.s_head | c.s_group) & 3) == 0 &&
+                         ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15) == 0;
   a.blocks = int32_t(grid_blocks(c, B, q.heads, a.bound));
-  a.scale = float(scale * 1.4426950408889634);
+  a.negative = scale < 0.0 ? 1 : 0;
+  a.natural = scale < 0.0 ? -scale : scale;
+  a.scale = float(a.natural * 1.4426950408889634);
+  if (!(a.scale > 1e-30f)) a.scale = 1e-30f;   // (the weights are 1 there, and -inf times it stays -inf)
   const bool f32 = !q.bf16 || !out.bf16, wide = c.head_dim > 128;
-  if (c.e4m3 && wide) launch_attention_kernel<true, 2>(a, f32, stream);
-  else if (c.e4m3) launch_attention_kernel<true, 1>(a, f32, stream);
-  else if (wide) launch_attention_kernel<false, 2>(a, f32, stream);
-  else launch_attention_kernel<false, 1>(a, f32, stream);
+  if (c.e4m3 && wide) launch_attention_kernel<true, 2>(a, f32, scale_vec, stream);
+  else if (c.e4m3) launch_attention_kernel<true, 1>(a, f32, scale_vec, stream);
+  else if (wide) launch_attention_kernel<false, 2>(a, f32, scale_vec, stream);
+  else launch_attention_kernel<false, 1>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");
   if (st != BSF8_OK || a.bound <= kTile) return st;
   const unsigned rows = unsigned(B * q.heads);
