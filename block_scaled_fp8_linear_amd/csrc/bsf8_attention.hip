@@ -22,9 +22,10 @@
 // (32 per wave), numbered through, and every block of a fixed grid takes an equal range of
 // tiles, whatever the lengths are: long sequences spread over many blocks, short ones share
 // one.  A block that holds an item whole stores its result; parts go to the workspace (at most
-// two per block: its first and its last item) and the second kernel adds them, in an order that
-// the lengths alone decide.
-// The blocks find their ranges by a sum over the lengths, so nothing is read on the host.
+// two per block: its first and its last item) and a second kernel adds them, in an order that
+// the lengths alone decide.  The blocks find their ranges by a sum over the lengths, so nothing
+// is read on the host; the block that holds an item's beginning leaves a note of where its
+// parts are, so that the second kernel need not find them again.
 #include <hip/hip_runtime.h>
 
 #include <type_traits>
@@ -46,6 +47,8 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef const __attribute__((address_space(4))) int32_t* ConstInts;   // read by the scalar unit
 
+struct Task;
+
 struct AttentionDev {
   CacheDev c;
   HeadsDev q, out;
@@ -53,6 +56,8 @@ struct AttentionDev {
   const int32_t* lens;
   float* lse;
   float* part;          // partial results: slots of kRows x chunks x 128 floats, then kRows maxima and kRows sums
+  Task* tasks;   // what is to be joined: by item if there are no more items than blocks, else by block
+  int32_t by_item;
   int64_t ld_table;
   int32_t B, pages;
   int32_t G;            // query heads per key head
@@ -66,62 +71,65 @@ struct AttentionDev {
   double natural;       // the size of the scale
 };
 
+// An item whose parts lie in blocks `slot / 2` .. `to`: the first in `slot`, the others in the
+// first slot of their blocks.
+struct Task {
+  int32_t b, head0, rows, slot, to;   // rows 0: nothing to join
+  int32_t unused[3];
+};
+
 __device__ __forceinline__ int first_token(const AttentionDev& a, int n) { return a.window ? max(0, n - a.window) : 0; }
-__device__ __forceinline__ int length(const AttentionDev& a, int b) {
-  return min(max(((ConstInts)(a.lens))[b], 0), a.bound);
-}
 // tiles of a sequence of n tokens (one, all of it masked, where there is none), and the first one's number
 __device__ __forceinline__ int tiles_of(const AttentionDev& a, int n, int& first) {
   first = first_token(a, n) / kTile;
   return n > 0 ? (n - 1) / kTile - first + 1 : 1;
 }
 
-// sums of a lane's value over the lanes up to it
-__device__ __forceinline__ int running_sum(int v) {
-  const int lane = threadIdx.x & 63;
+// 64 sequences, one per lane: their lengths, tiles, and the tiles up to and with them.
+struct Lengths {
+  int n, tiles, sum;
+};
+__device__ __forceinline__ Lengths lengths_of(const AttentionDev& a, int base) {
+  const int lane = threadIdx.x & 63, b = base + lane;
+  Lengths x;
+  x.n = min(max(a.lens[min(b, a.B - 1)], 0), a.bound);
+  int first;
+  x.tiles = b < a.B ? tiles_of(a, x.n, first) : 0;
+  x.sum = x.tiles;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
-    const int up = __shfl_up(v, d, 64);
-    if (lane >= d) v += up;
+    const int up = __shfl_up(x.sum, d, 64);
+    if (lane >= d) x.sum += up;
   }
-  return v;
+  return x;
 }
-__device__ __forceinline__ int lane_tiles(const AttentionDev& a, int b) {
-  int first;
-  const int n = b < a.B ? min(max(a.lens[b], 0), a.bound) : 0;
-  return b < a.B ? tiles_of(a, n, first) : 0;
-}
-// tiles of the whole batch for one item per sequence
-__device__ __forceinline__ int all_tiles(const AttentionDev& a) {
-  int sum = 0;
-  for (int base = 0; base < a.B; base += 64)
-    sum += __builtin_amdgcn_readlane(running_sum(lane_tiles(a, base + int(threadIdx.x & 63))), 63);
-  return sum;
-}
-// the sequence that holds tile `u` of that numbering, and the tiles before it
-__device__ __forceinline__ int find_sequence(const AttentionDev& a, int u, int& before) {
+// the sequence that holds tile `u` (of one item per sequence), and the tiles before it; x: those of the first 64 at first
+__device__ __forceinline__ int find_sequence(const AttentionDev& a, Lengths& x, int& base, int u, int& before) {
   before = 0;
-  for (int base = 0; base < a.B; base += 64) {
-    const int n = lane_tiles(a, base + int(threadIdx.x & 63)), sum = running_sum(n);
-    const uint64_t past = __ballot(before + sum > u);
+  for (base = 0;; base += 64) {
+    if (base) x = lengths_of(a, base);
+    const uint64_t past = __ballot(before + x.sum > u);
     if (past) {
       const int at = __builtin_ctzll(past);
-      before += __builtin_amdgcn_readlane(sum - n, at);
+      before += __builtin_amdgcn_readlane(x.sum - x.tiles, at);
       return base + at;
     }
-    before += __builtin_amdgcn_readlane(sum, 63);
+    if (base + 64 >= a.B) return a.B - 1;   // (u is a tile of the batch: not reached)
+    before += __builtin_amdgcn_readlane(x.sum, 63);
   }
-  return a.B - 1;
 }
-// the tiles before sequence b
-__device__ __forceinline__ int tiles_before(const AttentionDev& a, int b) {
-  int sum = 0;
-  for (int base = 0; base < b; base += 64) {
-    const int i = base + int(threadIdx.x & 63);
-    sum += __builtin_amdgcn_readlane(running_sum(i < b ? lane_tiles(a, i) : 0), 63);
+
+// Block w's tiles begin at begin_of(w): `few` or, the first `more` blocks, few + 1 tiles each.
+// (Ranges of one size would leave blocks without work: 4096 tiles over 768 blocks in sixes.)
+struct Ranges {
+  int few, more;
+  __device__ __forceinline__ Ranges(int total, int blocks) : few(total / blocks), more(total - few * blocks) {}
+  __device__ __forceinline__ int begin_of(int w) const { return w * few + min(w, more); }
+  __device__ __forceinline__ int block_of(int t) const {
+    const int big = more * (few + 1);
+    return t < big ? t / (few + 1) : more + (t - big) / few;
   }
-  return sum;
-}
+};
 
 // the largest of the four lanes that hold a head (lanes 16 and 32 apart)
 __device__ __forceinline__ float max_of_groups(float x) {
@@ -263,13 +271,19 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
   const int g = lane >> 4, i16 = lane & 15;
   const int D = a.c.head_dim;
 
-  const int total = all_tiles(a) * a.items;
-  const int per = (total + a.blocks - 1) / a.blocks;
-  const int t_begin = int(blockIdx.x) * per, t_end = min(total, t_begin + per);
-  if (t_begin >= t_end) return;
-  int before;
-  int b = find_sequence(a, t_begin / a.items, before);
-  int n = length(a, b), first;
+  Lengths seq = lengths_of(a, 0);
+  int total = __builtin_amdgcn_readlane(seq.sum, 63);
+  for (int base = 64; base < a.B; base += 64) total += __builtin_amdgcn_readlane(lengths_of(a, base).sum, 63);
+  total *= a.items;
+  const Ranges ranges(total, a.blocks);
+  const int t_begin = ranges.begin_of(int(blockIdx.x)), t_end = ranges.begin_of(int(blockIdx.x) + 1);
+  if (t_begin >= t_end) {
+    if (!a.by_item && a.tasks && threadIdx.x == 0) a.tasks[blockIdx.x].rows = 0;
+    return;
+  }
+  int before, base;
+  int b = find_sequence(a, seq, base, t_begin / a.items, before);
+  int n = __builtin_amdgcn_readlane(seq.n, b - base), first;
   int n_tiles = tiles_of(a, n, first);
   int item = (t_begin - before * a.items) / n_tiles, j = (t_begin - before * a.items) - item * n_tiles;
 
@@ -591,7 +605,17 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
         }
     __syncthreads();
     const bool whole = j == 0 && j_end == n_tiles;
-    float* part = a.part + (int64_t(blockIdx.x) * 2 + (t == t_begin ? 0 : 1)) * S::kSlot;
+    const int slot = int(blockIdx.x) * 2 + (t == t_begin ? 0 : 1);
+    if (a.tasks && threadIdx.x == 0 && (a.by_item ? j == 0 : t + j_end - j == t_end)) {
+      Task* task = a.tasks + (a.by_item ? b * a.items + item : int(blockIdx.x));
+      const bool begins = j == 0 && !whole;
+      task->b = b;
+      task->head0 = head0;
+      task->rows = begins ? rows : 0;
+      task->slot = slot;
+      task->to = begins ? ranges.block_of(t + n_tiles - 1) : 0;
+    }
+    float* part = a.part + int64_t(slot) * S::kSlot;
     for (int x = threadIdx.x; x < kRows * (S::kChannels / 4); x += kThreads) {
       const int row = x / (S::kChannels / 4), ch = 4 * (x % (S::kChannels / 4));
       if (row >= rows || ch >= D) continue;
@@ -620,28 +644,27 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     j = 0;
     if (++item == a.items && t < t_end) {
       item = 0;
-      n = length(a, ++b);
+      if (++b == base + 64) {
+        base = b;
+        seq = lengths_of(a, base);
+      }
+      n = __builtin_amdgcn_readlane(seq.n, b - base);
       n_tiles = tiles_of(a, n, first);
     }
   }
 }
 
 // Adds the parts of the items that lie in more than one block, a query head per block of this
-// grid: groups of lanes take every so many parts, with a maximum of their own.
+// kernel: groups of lanes take every so many parts, with a maximum of their own.
 template <int NG>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a) {
   using S = Shape<false, NG>;   // (a slot has one size for both types of cache)
-  constexpr int LANES = S::kChannels / 4, GROUPS = kThreads / LANES, FLIGHT = 4;
+  constexpr int LANES = S::kChannels / 4, GROUPS = kThreads / LANES, FLIGHT = 8;
   __shared__ float lds_o[GROUPS][S::kChannels], lds_m[GROUPS], lds_l[GROUPS];
-  const int heads = a.G * a.c.heads;
-  const int b = int(blockIdx.x / unsigned(heads)), head = int(blockIdx.x) - b * heads;
-  const int h = head / a.G, in_group = head - h * a.G, item = h * a.row_tiles + in_group / kRows, row = in_group % kRows;
-  int first;
-  const int n_tiles = tiles_of(a, length(a, b), first);
-  const int total = all_tiles(a) * a.items, per = (total + a.blocks - 1) / a.blocks;
-  const int begin = tiles_before(a, b) * a.items + item * n_tiles;
-  const int from = begin / per, to = (begin + n_tiles - 1) / per;
-  if (from == to) return;   // one block had all of it
+  const Task task = a.tasks[blockIdx.x];
+  const int row = int(blockIdx.y);
+  if (row >= task.rows) return;
+  const int from = task.slot >> 1, to = task.to;
   const int group = threadIdx.x / LANES, ch = 4 * (threadIdx.x % LANES);
   const bool on = ch < a.c.head_dim;
   float m = -INFINITY, l = 0.f;
@@ -652,8 +675,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) {
       const int blk = min(x + y * GROUPS, to);
-      // its block's first item, unless the block begins before it
-      const float* p = a.part + (int64_t(blk) * 2 + (blk == from && begin > from * per ? 1 : 0)) * S::kSlot;
+      const float* p = a.part + int64_t(blk == from ? task.slot : 2 * blk) * S::kSlot;
       v[y] = on ? *reinterpret_cast<const f4*>(p + row * S::kChannels + ch) : f4{0.f, 0.f, 0.f, 0.f};
       pm[y] = x + y * GROUPS <= to ? p[kRows * S::kChannels + row] : -INFINITY;
       pl[y] = p[kRows * S::kChannels + kRows + row];
@@ -693,7 +715,7 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a
       v += *reinterpret_cast<const f4*>(&lds_o[y][ch]) * f;
     }
   }
-  store_result(a, b, head, ch, v, top, sum);
+  store_result(a, task.b, task.head0 + row, ch, v, top, sum);
 }
 
 int compute_units() {
@@ -742,7 +764,7 @@ int64_t attention_tiles(const CacheDev& c, int64_t B, int32_t q_heads, int64_t b
 size_t attention_workspace_bytes(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
   if (bound <= kTile || B == 0) return 0;   // no item is ever split
   const size_t slot = c.head_dim > 128 ? Shape<false, 2>::kSlot : Shape<false, 1>::kSlot;
-  return size_t(grid_blocks(c, B, q_heads, bound)) * 2 * slot * sizeof(float);
+  return size_t(grid_blocks(c, B, q_heads, bound)) * (2 * slot * sizeof(float) + sizeof(Task));
 }
 
 bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDev& out, int64_t B, const int32_t* table,
@@ -767,6 +789,11 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   const bool scale_vec = c.s_row == 1 && ((c.s_page | c.s_head | c.s_group) & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15) == 0;
   a.blocks = int32_t(grid_blocks(c, B, q.heads, a.bound));
+  if (a.bound > kTile) {
+    const size_t slot = c.head_dim > 128 ? Shape<false, 2>::kSlot : Shape<false, 1>::kSlot;
+    a.tasks = reinterpret_cast<Task*>(a.part + size_t(a.blocks) * 2 * slot);
+    a.by_item = B * a.items <= a.blocks ? 1 : 0;
+  }
   a.negative = scale < 0.0 ? 1 : 0;
   a.natural = scale < 0.0 ? -scale : scale;
   a.scale = float(a.natural * 1.4426950408889634);
@@ -778,9 +805,10 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   else launch_attention_kernel<false, 1>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");
   if (st != BSF8_OK || a.bound <= kTile) return st;
-  const unsigned rows = unsigned(B * q.heads);
-  if (wide) hipLaunchKernelGGL(attention_join_kernel<2>, dim3(rows), dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL(attention_join_kernel<1>, dim3(rows), dim3(kThreads), 0, stream, a);
+  const unsigned rows = unsigned(a.G < kRows ? a.G : kRows);
+  const dim3 grid(a.by_item ? unsigned(B * a.items) : unsigned(a.blocks), rows);
+  if (wide) hipLaunchKernelGGL(attention_join_kernel<2>, grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL(attention_join_kernel<1>, grid, dim3(kThreads), 0, stream, a);
   return device_status(hipGetLastError(), "paged_attention join launch");
 }
 
