@@ -195,81 +195,103 @@ __device__ __forceinline__ void split(const float (&x)[8], v8bf (&t)[N]) {
   }
 }
 
-// Queries of 16 heads: the B operand, in the channel order of the keys' pieces; zeros for heads
-// past `rows` and channels past head_dim.  All loads go out before any is used.
-template <bool E4M3, int QS, int QT>
-__device__ __forceinline__ void load_queries(const AttentionDev& a, int b, int head0, int rows, v8bf (&qf)[QS][QT]) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, i16 = lane & 15, D = a.c.head_dim;
-  const int64_t base = int64_t(b) * a.q.token + int64_t(head0 + min(i16, rows - 1)) * a.q.head;
-  const auto channel = [&](int s) { return E4M3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8; };
-  float x[QS][8];
-  if (a.q.vec) {
-    if (QT == 1 || a.q.bf16) {
-      u4 v[QS];
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-        v[s] = *reinterpret_cast<const u4*>(static_cast<const uint16_t*>(a.q.p) + base + min(channel(s), D - 8));
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[s][e] = __uint_as_float((e & 1) ? v[s][e >> 1] & 0xFFFF0000u : v[s][e >> 1] << 16);
-    } else {
-      f4 v[QS][2];
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-          v[s][y] = reinterpret_cast<const f4*>(static_cast<const float*>(a.q.p) + base + min(channel(s), D - 8))[y];
-#pragma unroll
-      for (int s = 0; s < QS; ++s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[s][e] = v[s][e >> 2][e & 3];
-    }
-  } else {
-#pragma unroll
-    for (int s = 0; s < QS; ++s)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[s][e] = load_real(a.q.p, a.q.bf16, base + min(channel(s), D - 8) + e);
-  }
-#pragma unroll
-  for (int s = 0; s < QS; ++s) {
-    const bool there = i16 < rows && channel(s) < D;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[s][e] = !there ? 0.f : a.negative ? -x[s][e] : x[s][e];
-    split<QT>(x[s], qf[s]);
-  }
-}
-
-// Blocks per compute unit (waves per SIMD) that the registers allow.
-template <bool E4M3, int NG>
-struct Shape {
-  static constexpr int kBlocksPerCu = NG == 2 ? 2 : 3;
-  static constexpr int kChannels = NG * 128;
-  static constexpr int kSlot = kRows * kChannels + 2 * kRows;   // floats of a partial result
-};
-
-// NG: 128-channel groups of a head.  QT: BF16 terms of a query (1: BF16 queries, 3: F32);
-// PT: of a softmax weight.  A weight in one term would be off by 2^-9 of itself, as much as
-// the rounding of a BF16 output; two leave 2^-17, three 2^-25.
+// What an instance is made for.
+// DIM: channels that its pieces cover (64, 128, 256).  FULL: a head has exactly DIM of them, so
+// that offsets are constants and rows are whole cache lines, which are read non-temporally (each
+// is read once: 64 sequences to 8192 of 128 BF16 channels 156 -> 144 us, of E4M3 99 -> 93; rows
+// that share lines lose by it, 80 channels 185 -> 218).
+// QT: BF16 terms of a query (1: BF16 queries, 3: F32).  PT: of a softmax weight.  A weight in one
+// term would be off by 2^-9 of itself, as much as the rounding of a BF16 output; two leave 2^-17,
+// three 2^-25.
 // PAGES: kAny, each lane looks up a token's page; kHalves, pages are a multiple of 16 rows, so
 // that each half of a wave's 32 tokens is on one page, whose rows all exist: addresses are
 // scalar, and rows past the length are read and left out; kHalvesWide, also four scales are
 // one load.  (A choice inside the kernel would be a branch around loads, and where its sides
 // meet the compiler waits for all of them.)
 enum Pages { kAny, kHalves, kHalvesWide };
-template <bool E4M3, int NG, int QT, int PT, int PAGES>
-__global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPerCu)) void attention_kernel(AttentionDev a) {
-  using S = Shape<E4M3, NG>;
-  constexpr int KV = E4M3 ? 2 * NG : 4 * NG;   // 16-byte key loads per token and lane
-  constexpr int QS = 4 * NG;                   // query pieces: 32 channels each
-  constexpr int PITCH = S::kChannels + 4;
-  constexpr bool PAGES16 = PAGES != kAny;
+template <bool E4M3_, int DIM_, bool FULL_, int QT_, int PT_, int PAGES_>
+struct Config {
+  static constexpr bool E4M3 = E4M3_, FULL = FULL_, PAGES16 = PAGES_ != kAny;
+  static constexpr int DIM = DIM_, QT = QT_, PT = PT_, PAGES = PAGES_;
+  static constexpr int NG = DIM > 128 ? 2 : 1;         // 128-channel groups
+  static constexpr int KV = E4M3 ? DIM / 64 : DIM / 32;   // 16-byte key loads per token and lane
+  static constexpr int QS = DIM / 32;                  // query pieces: 32 channels each
+  static constexpr int CHANNELS = NG * 128;
+  static constexpr int SLOT = kRows * CHANNELS + 2 * kRows;   // floats of a partial result
+};
+// Blocks per compute unit (waves per SIMD) that the registers allow.
+constexpr int blocks_per_cu(bool e4m3, int dim) { return dim > 128 ? 2 : 3; }
+constexpr int slot_floats(int dim) { return Config<false, 128, false, 1, 2, kAny>::SLOT + (dim > 128 ? kRows * 128 : 0); }
+
+template <bool NT, typename T>
+__device__ __forceinline__ T fetch(const uint8_t* p) {
+  if (NT) return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+  return *reinterpret_cast<const T*>(p);
+}
+
+// Queries of 16 heads: the B operand, in the channel order of the keys' pieces; zeros for heads
+// past `rows` and channels past head_dim.  begin() asks for them, end() makes the operand.
+template <class C>
+struct Queries {
+  static constexpr int W = C::QT == 1 ? 1 : 2;
+  u4 raw[C::QS][W];       // BF16 values, or F32 ones
+  __device__ __forceinline__ static int channel(int s) {
+    const int g = (threadIdx.x & 63) >> 4;
+    return C::E4M3 ? (s >> 1) * 64 + g * 16 + (s & 1) * 8 : s * 32 + g * 8;
+  }
+  __device__ __forceinline__ void begin(const AttentionDev& a, int b, int head0, int rows) {
+    const int D = C::FULL ? C::DIM : a.c.head_dim;
+    const int64_t base = int64_t(b) * a.q.token + int64_t(head0 + min(int(threadIdx.x & 15), rows - 1)) * a.q.head;
+    if (a.q.vec && (C::QT == 1 || !a.q.bf16)) {
+#pragma unroll
+      for (int s = 0; s < C::QS; ++s)
+#pragma unroll
+        for (int y = 0; y < W; ++y)
+          raw[s][y] = reinterpret_cast<const u4*>(static_cast<const uint8_t*>(a.q.p) +
+                                                  (base + min(channel(s), D - 8)) * (C::QT == 1 ? 2 : 4))[y];
+      return;
+    }
+#pragma unroll
+    for (int s = 0; s < C::QS; ++s)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float x = load_real(a.q.p, a.q.bf16, base + min(channel(s), D - 8) + e);
+        if (C::QT == 1) raw[s][0][e >> 1] = (e & 1) ? raw[s][0][e >> 1] | __float_as_uint(x) : __float_as_uint(x) >> 16;
+        else raw[s][e >> 2][e & 3] = __float_as_uint(x);
+      }
+  }
+  __device__ __forceinline__ void end(const AttentionDev& a, int rows, v8bf (&qf)[C::QS][C::QT]) const {
+    const int D = C::FULL ? C::DIM : a.c.head_dim;
+#pragma unroll
+    for (int s = 0; s < C::QS; ++s) {
+      const bool there = int(threadIdx.x & 15) < rows && channel(s) < D;
+      const uint32_t sign = a.negative ? (C::QT == 1 ? 0x80008000u : 0x80000000u) : 0u;
+      if (C::QT == 1) {
+        u4 v;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = there ? raw[s][0][x] ^ sign : 0u;
+        qf[s][0] = as_bf16(v);
+      } else {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = there ? __uint_as_float(raw[s][(e >> 2) % W][e & 3] ^ sign) : 0.f;
+        split<C::QT>(x, qf[s]);
+      }
+    }
+  }
+};
+
+template <class C>
+__global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C::DIM)) void attention_kernel(AttentionDev a) {
+  constexpr bool E4M3 = C::E4M3, PAGES16 = C::PAGES16;
+  constexpr int NG = C::NG, KV = C::KV, QT = C::QT, PT = C::PT, QS = C::QS;
+  constexpr int PITCH = C::CHANNELS + 4;
   __shared__ float lds_o[kWaves][kRows][PITCH];
   __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
-  const int D = a.c.head_dim;
+  const int D = C::FULL ? C::DIM : a.c.head_dim;
 
   Lengths seq = lengths_of(a, 0);
   int total = __builtin_amdgcn_readlane(seq.sum, 63);
@@ -281,70 +303,63 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     if (!a.by_item && a.tasks && threadIdx.x == 0) a.tasks[blockIdx.x].rows = 0;
     return;
   }
+  // the item at t_begin: sequence, key head, first query head of the key head's, tile
   int before, base;
   int b = find_sequence(a, seq, base, t_begin / a.items, before);
   int n = __builtin_amdgcn_readlane(seq.n, b - base), first;
   int n_tiles = tiles_of(a, n, first);
-  int item = (t_begin - before * a.items) / n_tiles, j = (t_begin - before * a.items) - item * n_tiles;
+  const int item = (t_begin - before * a.items) / n_tiles;
+  int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * kRows;
+  int j = (t_begin - before * a.items) - item * n_tiles;
 
   // byte offsets of a lane's pieces within a row, with its token's (the key's i16, the first
   // value's 4 g); channels past head_dim are read as others that exist (queries are zero there,
   // and outputs are not stored)
-  uint32_t k_off[KV], v_off[NG];
-#pragma unroll
-  for (int s = 0; s < KV; ++s) {
-    const int ch = E4M3 ? min(s * 64 + g * 16, D - 16) : min(s * 32 + g * 8, D - 8);
-    k_off[s] = (PAGES16 ? uint32_t(i16) * uint32_t(a.c.row) : 0) + uint32_t(ch) * (E4M3 ? 1 : 2);
-  }
-#pragma unroll
-  for (int c = 0; c < NG; ++c)
-    v_off[c] = (PAGES16 ? uint32_t(4 * g) * uint32_t(a.c.row) : 0) + uint32_t(min(c * 128 + i16 * 8, D - 8)) * (E4M3 ? 1 : 2);
+  const auto key_channel = [&](int s) {
+    return C::FULL ? (E4M3 ? s * 64 + g * 16 : s * 32 + g * 8) : E4M3 ? min(s * 64 + g * 16, D - 16) : min(s * 32 + g * 8, D - 8);
+  };
+  const uint32_t k_row = PAGES16 ? uint32_t(i16) * uint32_t(a.c.row) : 0, v_row = PAGES16 ? uint32_t(4 * g) * uint32_t(a.c.row) : 0;
+  const auto key_offset = [&](int s) { return k_row + uint32_t(key_channel(s)) * (E4M3 ? 1 : 2); };
+  const auto value_offset = [&](int c) { return v_row + uint32_t(min(c * 128 + i16 * 8, D - 8)) * (E4M3 ? 1 : 2); };
 
   for (int t = t_begin; t < t_end;) {
+    // the item's tiles j .. j_end - 1 are this block's
     const int j_end = min(n_tiles, j + (t_end - t));
-    const int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * kRows;
     const int rows = min(kRows, a.G - row0), head0 = h * a.G + row0;
     const int start = first_token(a, n), stop = min(n, (first + j_end) * kTile);
 
-    v8bf qf[QS][QT];
-    load_queries<E4M3, QS, QT>(a, b, head0, rows, qf);
-
-    const uint8_t* k_base = a.c.k + int64_t(h) * a.c.head;
-    const uint8_t* v_base = a.c.v + int64_t(h) * a.c.head;
-    const float* ks_base = E4M3 ? a.c.k_scale + int64_t(h) * a.c.s_head : nullptr;
-    const float* vs_base = E4M3 ? a.c.v_scale + int64_t(h) * a.c.s_head : nullptr;
-    const int32_t* table = a.table + int64_t(b) * a.ld_table;
-
-    f4 o[NG][8];
-#pragma unroll
-    for (int c = 0; c < NG; ++c)
-#pragma unroll
-      for (int x = 0; x < 8; ++x) o[c][x] = f4{0.f, 0.f, 0.f, 0.f};
-    float m = -INFINITY, l = 0.f;
-
-    // ---- where a wave's 32 tokens lie.  Entries of the table are asked for two tiles ahead
+    // ---- where a wave's 32 tokens lie.  Entries of the table are asked for a tile before they are needed
     struct Entries {
       int e0, e1;           // pages of the halves; or e0: page of token lane & 31
+      int r0, r1;           // their rows
     };
     const auto entries = [&](int pos) {
       // (columns past the table's end are not read: tokens there do not exist)
       Entries e;
       if (PAGES16) {
-        ConstInts at = (ConstInts)table;
-        e.e0 = at[min(int(a.c.page_of(uint32_t(pos))), a.pages - 1)];
-        e.e1 = at[min(int(a.c.page_of(uint32_t(pos + 16))), a.pages - 1)];
+        const int p0 = int(__umulhi(uint32_t(pos), a.c.magic) >> (a.c.shift - 32));   // (shift is 35 or more)
+        e.r0 = pos - p0 * a.c.page_size;
+        const bool same = e.r0 + 16 < a.c.page_size;
+        e.r1 = same ? e.r0 + 16 : 0;
+        ConstInts table = (ConstInts)(a.table + int64_t(b) * a.ld_table);
+        e.e0 = table[min(p0, a.pages - 1)];
+        e.e1 = table[min(same ? p0 : p0 + 1, a.pages - 1)];
       } else {
-        e.e0 = table[min(int(a.c.page_of(uint32_t(pos + (lane & 31)))), a.pages - 1)];
-        e.e1 = 0;
+        const int tok = pos + (lane & 31), p = int(a.c.page_of(uint32_t(tok)));
+        e.r0 = tok - p * a.c.page_size;
+        e.e0 = a.table[int64_t(b) * a.ld_table + min(p, a.pages - 1)];
+        e.e1 = e.r1 = 0;
       }
       return e;
     };
     struct Where {
       uint32_t mask;              // bit x: token x of the 32 exists
-      int64_t at[2], s_at[2];     // of the halves: bytes, elements of scales
-      int le, lr;                 // or page and row of token lane & 31
+      int64_t at[2], s_at[2];     // of the halves: bytes, elements of scales; at[0] and s_at[0] of the head alone where
+      int le, lr;                 // each lane has a page and row of token lane & 31
     };
     const auto locate = [&](int pos, Entries e, Where& w) {
+      w.at[0] = int64_t(h) * a.c.head;
+      if (E4M3) w.s_at[0] = int64_t(h) * a.c.s_head;
       if (PAGES16) {
         const auto below = [](int x) { return x >= 32 ? ~0u : x <= 0 ? 0u : (1u << x) - 1u; };
         w.mask = below(stop - pos) & ~below(start - pos);
@@ -357,22 +372,24 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
           e.e1 = 0;
           w.mask &= 0xFFFFu;
         }
-        const int r0 = pos - int(a.c.page_of(uint32_t(pos))) * a.c.page_size;
-        const int r1 = pos + 16 - int(a.c.page_of(uint32_t(pos + 16))) * a.c.page_size;
-        w.at[0] = int64_t(e.e0) * a.c.page + int64_t(r0) * a.c.row;
-        w.at[1] = int64_t(e.e1) * a.c.page + int64_t(r1) * a.c.row;
+        w.at[1] = w.at[0] + uint64_t(uint32_t(e.e1)) * uint32_t(a.c.page) + uint64_t(uint32_t(e.r1)) * uint32_t(a.c.row);
+        w.at[0] += uint64_t(uint32_t(e.e0)) * uint32_t(a.c.page) + uint64_t(uint32_t(e.r0)) * uint32_t(a.c.row);
         if (E4M3) {
-          w.s_at[0] = int64_t(e.e0) * a.c.s_page + int64_t(r0) * a.c.s_row;
-          w.s_at[1] = int64_t(e.e1) * a.c.s_page + int64_t(r1) * a.c.s_row;
+          w.s_at[1] = w.s_at[0] + uint64_t(uint32_t(e.e1)) * uint32_t(a.c.s_page) + uint64_t(uint32_t(e.r1)) * uint32_t(a.c.s_row);
+          w.s_at[0] += uint64_t(uint32_t(e.e0)) * uint32_t(a.c.s_page) + uint64_t(uint32_t(e.r0)) * uint32_t(a.c.s_row);
         }
       } else {
         const int tok = pos + (lane & 31);
         w.le = e.e0;
-        w.lr = tok - int(a.c.page_of(uint32_t(tok))) * a.c.page_size;
+        w.lr = e.r0;
         const bool there = tok >= start && tok < stop && uint32_t(w.le) < uint32_t(a.c.n_pages);
         w.mask = uint32_t(__ballot(there));
         if (!there) w.le = w.lr = 0;
       }
+    };
+    // the place of token `tok` where each lane looks up one
+    const auto lane_at = [&](const Where& w, int tok) {
+      return w.at[0] + int64_t(__shfl(w.le, tok, 64)) * a.c.page + int64_t(__shfl(w.lr, tok, 64)) * a.c.row;
     };
 
     u4 kr[2][KV];
@@ -380,83 +397,76 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     const auto load_keys = [&](const Where& w) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint8_t* p = k_base;
-        if (PAGES16) p += w.at[x];
-        else p += int64_t(__shfl(w.le, 16 * x + i16, 64)) * a.c.page + int64_t(__shfl(w.lr, 16 * x + i16, 64)) * a.c.row;
+        const uint8_t* p = a.c.k + (PAGES16 ? w.at[x] : lane_at(w, 16 * x + i16));
 #pragma unroll
-        for (int s = 0; s < KV; ++s)
-          kr[x][s] = *reinterpret_cast<const u4*>(p + k_off[s]);
+        for (int s = 0; s < KV; ++s) kr[x][s] = fetch<C::FULL, u4>(p + key_offset(s));
       }
     };
     // scales of a lane's eight tokens
-    const auto load_scales = [&](const Where& w, const float* base, float (&sc)[NG][2][4]) {
+    const auto load_scales = [&](const Where& w, const float* of, float (&sc)[NG][2][4]) {
 #pragma unroll
       for (int c = 0; c < NG; ++c)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float* p = base + int64_t(c) * a.c.s_group;
-          if (PAGES16) {
-            p += w.s_at[x];
-            if (PAGES == kHalvesWide) {
-              const f4 v = *reinterpret_cast<const f4*>(p + 4 * g);
+          const float* p = of + int64_t(c) * a.c.s_group;
+          if (C::PAGES == kHalvesWide) {
+            const f4 v = *reinterpret_cast<const f4*>(p + w.s_at[x] + 4 * g);
 #pragma unroll
-              for (int r = 0; r < 4; ++r) sc[c][x][r] = v[r];
-            } else {
+            for (int r = 0; r < 4; ++r) sc[c][x][r] = v[r];
+          } else if (PAGES16) {
 #pragma unroll
-              for (int r = 0; r < 4; ++r) sc[c][x][r] = p[uint32_t(4 * g + r) * uint32_t(a.c.s_row)];
-            }
+            for (int r = 0; r < 4; ++r) sc[c][x][r] = (p + w.s_at[x])[uint32_t(4 * g + r) * uint32_t(a.c.s_row)];
           } else {
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
               const int tok = 16 * x + 4 * g + r;
-              sc[c][x][r] = p[int64_t(__shfl(w.le, tok, 64)) * a.c.s_page + int64_t(__shfl(w.lr, tok, 64)) * a.c.s_row];
+              sc[c][x][r] = p[w.s_at[0] + int64_t(__shfl(w.le, tok, 64)) * a.c.s_page + int64_t(__shfl(w.lr, tok, 64)) * a.c.s_row];
             }
           }
         }
     };
     constexpr int VW = E4M3 ? 2 : 4;
-    uint32_t vr[NG][8][VW];
+    typedef uint32_t vw __attribute__((ext_vector_type(VW)));
+    vw vr[NG][8];
     const auto load_values = [&](const Where& w) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint8_t* p = v_base;
-        if (PAGES16) {
-          p += w.at[e >> 2] + int64_t(e & 3) * a.c.row;
-        } else {
-          const int tok = (e >> 2) * 16 + 4 * g + (e & 3);
-          p += int64_t(__shfl(w.le, tok, 64)) * a.c.page + int64_t(__shfl(w.lr, tok, 64)) * a.c.row;
-        }
+        const uint8_t* p = a.c.v + (PAGES16 ? w.at[e >> 2] + uint64_t(uint32_t(e & 3)) * uint32_t(a.c.row)
+                                            : lane_at(w, (e >> 2) * 16 + 4 * g + (e & 3)));
 #pragma unroll
-        for (int c = 0; c < NG; ++c) {
-          if (E4M3) {
-            const u2 v = *reinterpret_cast<const u2*>(p + v_off[c]);
-#pragma unroll
-            for (int x = 0; x < 2; ++x) vr[c][e][x] = v[x];
-          } else {
-            const u4 v = *reinterpret_cast<const u4*>(p + v_off[c]);
-#pragma unroll
-            for (int x = 0; x < VW; ++x) vr[c][e][x] = v[x];
-          }
-        }
+        for (int c = 0; c < NG; ++c) vr[c][e] = fetch<C::FULL, vw>(p + value_offset(c));
       }
     };
+
 
     int pos = (first + j) * kTile + wave * kWaveTokens;
     Where w;
     Entries ahead;
+    Queries<C> queries;
+    if (pos < stop) ahead = entries(pos);
+    queries.begin(a, b, head0, rows);
     if (pos < stop) {
-      locate(pos, entries(pos), w);
-      if (E4M3) load_scales(w, ks_base, ksc);
+      locate(pos, ahead, w);
+      if (E4M3) load_scales(w, a.c.k_scale, ksc);
       load_keys(w);
-      if (E4M3) load_scales(w, vs_base, vsc);
+      if (E4M3) load_scales(w, a.c.v_scale, vsc);
       load_values(w);
       ahead = entries(pos + kTile);
     }
-    // one tile's products, the next one's loads (not for the last: apart, for the same reason)
-    const auto tile = [&](auto last) {
-      constexpr bool LAST = decltype(last)::value;
+    v8bf qf[QS][QT];
+    queries.end(a, rows, qf);
+    f4 o[NG][8];
+#pragma unroll
+    for (int c = 0; c < NG; ++c)
+#pragma unroll
+      for (int x = 0; x < 8; ++x) o[c][x] = f4{0.f, 0.f, 0.f, 0.f};
+    float m = -INFINITY, l = 0.f;
+
+    // one tile's products and, behind the registers' last use, the next one's loads
+    const auto tile = [&](auto loads) {
+      constexpr bool LOADS = decltype(loads)::value;
       const uint32_t mask = w.mask;
-      if (!LAST) {
+      if (LOADS) {
         locate(pos + kTile, ahead, w);
         ahead = entries(pos + 2 * kTile);
       }
@@ -489,8 +499,8 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
           s[4 * x + r] = v;
         }
       }
-      if (!LAST) {
-        if (E4M3) load_scales(w, ks_base, ksc);
+      if (LOADS) {
+        if (E4M3) load_scales(w, a.c.k_scale, ksc);
         load_keys(w);
       }
       if (mask != ~0u) {
@@ -553,18 +563,19 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       for (int c = 0; c < NG; ++c) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {   // channels 2 x and 2 x + 1 of each lane's eight
-          uint32_t pair[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (!E4M3) pair[e] = vr[c][e][x];
-            else if (x & 1) pair[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, true));
-            else pair[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(vr[c][e][x >> 1], 1.0f, false));
-          }
           u4 lo, hi;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            lo[e] = __builtin_amdgcn_perm(pair[2 * e + 1], pair[2 * e], 0x05040100u);
-            hi[e] = __builtin_amdgcn_perm(pair[2 * e + 1], pair[2 * e], 0x07060302u);
+            if constexpr (E4M3) {
+              // both tokens' bytes of the two channels side by side, then two conversions
+              const uint32_t both = __builtin_amdgcn_perm(vr[c][2 * e + 1][x >> 1], vr[c][2 * e][x >> 1],
+                                                          (x & 1) ? 0x07030602u : 0x05010400u);
+              lo[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(both, 1.0f, false));
+              hi[e] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(both, 1.0f, true));
+            } else {
+              lo[e] = __builtin_amdgcn_perm(vr[c][2 * e + 1][x % VW], vr[c][2 * e][x % VW], 0x05040100u);
+              hi[e] = __builtin_amdgcn_perm(vr[c][2 * e + 1][x % VW], vr[c][2 * e][x % VW], 0x07060302u);
+            }
           }
 #pragma unroll
           for (int q = 0; q < PT; ++q) {
@@ -573,13 +584,13 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
           }
         }
       }
-      if (!LAST) {
-        if (E4M3) load_scales(w, vs_base, vsc);
+      if (LOADS) {
+        if (E4M3) load_scales(w, a.c.v_scale, vsc);
         load_values(w);
       }
     };
-    for (; pos + kTile < stop; pos += kTile) tile(std::false_type{});
-    if (pos < stop) tile(std::true_type{});
+    for (; pos + kTile < stop; pos += kTile) tile(std::true_type{});
+    if (pos < stop) tile(std::false_type{});
 
     // ---- the waves' parts of the segment
     l = sum_of_groups(l);
@@ -607,7 +618,7 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
     const bool whole = j == 0 && j_end == n_tiles;
     const int slot = int(blockIdx.x) * 2 + (t == t_begin ? 0 : 1);
     if (a.tasks && threadIdx.x == 0 && (a.by_item ? j == 0 : t + j_end - j == t_end)) {
-      Task* task = a.tasks + (a.by_item ? b * a.items + item : int(blockIdx.x));
+      Task* task = a.tasks + (a.by_item ? b * a.items + h * a.row_tiles + row0 / kRows : int(blockIdx.x));
       const bool begins = j == 0 && !whole;
       task->b = b;
       task->head0 = head0;
@@ -615,9 +626,9 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       task->slot = slot;
       task->to = begins ? ranges.block_of(t + n_tiles - 1) : 0;
     }
-    float* part = a.part + int64_t(slot) * S::kSlot;
-    for (int x = threadIdx.x; x < kRows * (S::kChannels / 4); x += kThreads) {
-      const int row = x / (S::kChannels / 4), ch = 4 * (x % (S::kChannels / 4));
+    float* part = a.part + int64_t(slot) * C::SLOT;
+    for (int x = threadIdx.x; x < kRows * (C::CHANNELS / 4); x += kThreads) {
+      const int row = x / (C::CHANNELS / 4), ch = 4 * (x % (C::CHANNELS / 4));
       if (row >= rows || ch >= D) continue;
       f4 v = *reinterpret_cast<const f4*>(&lds_o[0][row][ch]);
 #pragma unroll
@@ -631,10 +642,10 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
       if (whole) {
         store_result(a, b, head0 + row, ch, v, all_m, all_l);
       } else {
-        *reinterpret_cast<f4*>(part + row * S::kChannels + ch) = v;
+        *reinterpret_cast<f4*>(part + row * C::CHANNELS + ch) = v;
         if (ch == 0) {
-          part[kRows * S::kChannels + row] = all_m;
-          part[kRows * S::kChannels + kRows + row] = all_l;
+          part[kRows * C::CHANNELS + row] = all_m;
+          part[kRows * C::CHANNELS + kRows + row] = all_l;
         }
       }
     }
@@ -642,8 +653,12 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
 
     t += j_end - j;
     j = 0;
-    if (++item == a.items && t < t_end) {
-      item = 0;
+    if ((row0 += kRows) >= a.G) {
+      row0 = 0;
+      ++h;
+    }
+    if (h == a.c.heads && t < t_end) {
+      h = 0;
       if (++b == base + 64) {
         base = b;
         seq = lengths_of(a, base);
@@ -656,11 +671,11 @@ __global__ __launch_bounds__(kThreads, QT > 1 ? 1 : (Shape<E4M3, NG>::kBlocksPer
 
 // Adds the parts of the items that lie in more than one block, a query head per block of this
 // kernel: groups of lanes take every so many parts, with a maximum of their own.
-template <int NG>
+template <int DIM>
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a) {
-  using S = Shape<false, NG>;   // (a slot has one size for both types of cache)
-  constexpr int LANES = S::kChannels / 4, GROUPS = kThreads / LANES, FLIGHT = 8;
-  __shared__ float lds_o[GROUPS][S::kChannels], lds_m[GROUPS], lds_l[GROUPS];
+  using C = Config<false, DIM, false, 1, 2, kAny>;   // (a slot has one size for both types of cache)
+  constexpr int LANES = C::CHANNELS / 4, GROUPS = kThreads / LANES, FLIGHT = 8;
+  __shared__ float lds_o[GROUPS][C::CHANNELS], lds_m[GROUPS], lds_l[GROUPS];
   const Task task = a.tasks[blockIdx.x];
   const int row = int(blockIdx.y);
   if (row >= task.rows) return;
@@ -675,10 +690,10 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) {
       const int blk = min(x + y * GROUPS, to);
-      const float* p = a.part + int64_t(blk == from ? task.slot : 2 * blk) * S::kSlot;
-      v[y] = on ? *reinterpret_cast<const f4*>(p + row * S::kChannels + ch) : f4{0.f, 0.f, 0.f, 0.f};
-      pm[y] = x + y * GROUPS <= to ? p[kRows * S::kChannels + row] : -INFINITY;
-      pl[y] = p[kRows * S::kChannels + kRows + row];
+      const float* p = a.part + int64_t(blk == from ? task.slot : 2 * blk) * C::SLOT;
+      v[y] = on ? *reinterpret_cast<const f4*>(p + row * C::CHANNELS + ch) : f4{0.f, 0.f, 0.f, 0.f};
+      pm[y] = x + y * GROUPS <= to ? p[kRows * C::CHANNELS + row] : -INFINITY;
+      pl[y] = p[kRows * C::CHANNELS + kRows + row];
     }
     float top = m;
 #pragma unroll
@@ -734,25 +749,30 @@ int compute_units() {
 int64_t grid_blocks(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
   const int64_t row_tiles = (q_heads / c.heads + kRows - 1) / kRows;
   const int64_t most = B * c.heads * row_tiles * (bound / kTile + 2);
-  const int64_t held = int64_t(compute_units()) * (c.head_dim > 128 ? Shape<false, 2>::kBlocksPerCu
-                                                   : c.e4m3         ? Shape<true, 1>::kBlocksPerCu
-                                                                    : Shape<false, 1>::kBlocksPerCu);
+  const int64_t held = int64_t(compute_units()) * blocks_per_cu(c.e4m3 != 0, c.head_dim);
   return most < held ? most : held;
 }
 
-template <bool E4M3, int NG>
-void launch_attention_kernel(const AttentionDev& a, bool f32, bool scale_vec, hipStream_t stream) {
+template <bool E4M3, int DIM, bool FULL, int QT, int PT>
+void launch_pages(const AttentionDev& a, bool scale_vec, hipStream_t stream) {
   const dim3 grid{unsigned(a.blocks)}, block{kThreads};
-  if (a.c.page_size % 16) {
-    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kAny>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kAny>), grid, block, 0, stream, a);
-  } else if (!E4M3 || scale_vec) {   // (BF16: no scales)
-    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kHalvesWide>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kHalvesWide>), grid, block, 0, stream, a);
-  } else if constexpr (E4M3) {
-    if (f32) hipLaunchKernelGGL((attention_kernel<E4M3, NG, 3, 3, kHalves>), grid, block, 0, stream, a);
-    else hipLaunchKernelGGL((attention_kernel<E4M3, NG, 1, 2, kHalves>), grid, block, 0, stream, a);
-  }
+  if (a.c.page_size % 16)
+    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kAny>>), grid, block, 0, stream, a);
+  else if (!E4M3 || scale_vec)   // (BF16: no scales)
+    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalvesWide>>), grid, block, 0, stream, a);
+  else if constexpr (E4M3)
+    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalves>>), grid, block, 0, stream, a);
+}
+template <bool E4M3>
+void launch_dims(const AttentionDev& a, bool f32, bool scale_vec, hipStream_t stream) {
+  const int D = a.c.head_dim;
+  if (f32 && D > 128) launch_pages<E4M3, 256, false, 3, 3>(a, scale_vec, stream);
+  else if (f32) launch_pages<E4M3, 128, false, 3, 3>(a, scale_vec, stream);
+  else if (D == 64) launch_pages<E4M3, 64, true, 1, 2>(a, scale_vec, stream);
+  else if (D == 128) launch_pages<E4M3, 128, true, 1, 2>(a, scale_vec, stream);
+  else if (D == 256) launch_pages<E4M3, 256, true, 1, 2>(a, scale_vec, stream);
+  else if (D > 128) launch_pages<E4M3, 256, false, 1, 2>(a, scale_vec, stream);
+  else launch_pages<E4M3, 128, false, 1, 2>(a, scale_vec, stream);
 }
 
 }  // namespace
@@ -763,7 +783,7 @@ int64_t attention_tiles(const CacheDev& c, int64_t B, int32_t q_heads, int64_t b
 
 size_t attention_workspace_bytes(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
   if (bound <= kTile || B == 0) return 0;   // no item is ever split
-  const size_t slot = c.head_dim > 128 ? Shape<false, 2>::kSlot : Shape<false, 1>::kSlot;
+  const size_t slot = slot_floats(c.head_dim);
   return size_t(grid_blocks(c, B, q_heads, bound)) * (2 * slot * sizeof(float) + sizeof(Task));
 }
 
@@ -790,7 +810,7 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
                          ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15) == 0;
   a.blocks = int32_t(grid_blocks(c, B, q.heads, a.bound));
   if (a.bound > kTile) {
-    const size_t slot = c.head_dim > 128 ? Shape<false, 2>::kSlot : Shape<false, 1>::kSlot;
+    const size_t slot = slot_floats(c.head_dim);
     a.tasks = reinterpret_cast<Task*>(a.part + size_t(a.blocks) * 2 * slot);
     a.by_item = B * a.items <= a.blocks ? 1 : 0;
   }
@@ -798,17 +818,15 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   a.natural = scale < 0.0 ? -scale : scale;
   a.scale = float(a.natural * 1.4426950408889634);
   if (!(a.scale > 1e-30f)) a.scale = 1e-30f;   // (the weights are 1 there, and -inf times it stays -inf)
-  const bool f32 = !q.bf16 || !out.bf16, wide = c.head_dim > 128;
-  if (c.e4m3 && wide) launch_attention_kernel<true, 2>(a, f32, scale_vec, stream);
-  else if (c.e4m3) launch_attention_kernel<true, 1>(a, f32, scale_vec, stream);
-  else if (wide) launch_attention_kernel<false, 2>(a, f32, scale_vec, stream);
-  else launch_attention_kernel<false, 1>(a, f32, scale_vec, stream);
+  const bool f32 = !q.bf16 || !out.bf16;
+  if (c.e4m3) launch_dims<true>(a, f32, scale_vec, stream);
+  else launch_dims<false>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");
   if (st != BSF8_OK || a.bound <= kTile) return st;
   const unsigned rows = unsigned(a.G < kRows ? a.G : kRows);
   const dim3 grid(a.by_item ? unsigned(B * a.items) : unsigned(a.blocks), rows);
-  if (wide) hipLaunchKernelGGL(attention_join_kernel<2>, grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL(attention_join_kernel<1>, grid, dim3(kThreads), 0, stream, a);
+  if (c.head_dim > 128) hipLaunchKernelGGL(attention_join_kernel<256>, grid, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL(attention_join_kernel<128>, grid, dim3(kThreads), 0, stream, a);
   return device_status(hipGetLastError(), "paged_attention join launch");
 }
 

@@ -444,7 +444,8 @@ static bsf8_status cache_checks(const bsf8_cache* p, CacheDev* out) {
   if (reinterpret_cast<uintptr_t>(c.k) % 16 || reinterpret_cast<uintptr_t>(c.v) % 16 || c.page * esz % 16 ||
       c.row * esz % 16 || c.head * esz % 16)
     return fail(BSF8_E_ALIGNMENT, "cache addresses and strides are multiples of 16 bytes");
-  if (c.row > (int64_t(1) << 27) / esz) return fail(BSF8_E_UNSUPPORTED, "cache rows further apart than 2^27 bytes");
+  if (c.row > (int64_t(1) << 27) / esz || c.page > UINT32_MAX / esz)
+    return fail(BSF8_E_UNSUPPORTED, "cache rows further apart than 2^27 bytes, or pages than 2^32 - 1");
   CacheDev d{};
   if (e4m3) {
     for (int i = 0; i < 4; ++i)
@@ -452,7 +453,8 @@ static bsf8_status cache_checks(const bsf8_cache* p, CacheDev* out) {
     if (!strides_apart(1, size, s_at, 4)) return fail(BSF8_E_INVALID_ARG, "scale strides let elements share an address");
     if (reinterpret_cast<uintptr_t>(c.k_scale) % 4 || reinterpret_cast<uintptr_t>(c.v_scale) % 4)
       return fail(BSF8_E_ALIGNMENT, "a scale address is not element aligned");
-    if (c.s_row > (int64_t(1) << 25)) return fail(BSF8_E_UNSUPPORTED, "scale rows further apart than 2^25 elements");
+    if (c.s_row > (int64_t(1) << 25) || c.s_page > UINT32_MAX)
+      return fail(BSF8_E_UNSUPPORTED, "scale rows further apart than 2^25 elements, or pages than 2^32 - 1");
     d.k_scale = c.k_scale;
     d.v_scale = c.v_scale;
     d.s_page = c.s_page;

@@ -556,7 +556,8 @@ typedef struct bsf8_heads {
  * head_dim is a multiple of 16 up to BSF8_CACHE_MAX_HEAD_DIM; k and v are 16-byte
  * aligned with strides of a multiple of 16 bytes (ALIGNMENT otherwise); strides
  * let no two elements share an address (INVALID_ARG otherwise); n_pages * page_size
- * and 16 * row (bytes) are below 2^31 (UNSUPPORTED otherwise).  Attention reads
+ * is below 2^31, rows lie at most 2^27 bytes (scales 2^25 elements) apart and pages less
+ * than 2^32 (UNSUPPORTED otherwise).  Attention reads
  * fastest with head-major pages of a multiple of 16 rows (better 32) and s_row == 1.
  */
 #define BSF8_CACHE_MAX_HEAD_DIM 256

@@ -38,7 +38,7 @@ def test_cache_descriptor():
                 dict(v_scale=FAKE + 1), dict(dtype=B.DT_BF16, k_scale=None, v_scale=None, head=16 * 192 + 4, page=1 << 14)):
         assert _validate(**bad) == "ALIGNMENT", bad
     for bad in (dict(head_dim=72), dict(head_dim=272), dict(head_dim=8), dict(n_pages=1 << 27), dict(n_pages=1 << 40),
-                dict(heads=1, head=0, row=1 << 28, page=1 << 33),
+                dict(heads=1, head=0, row=1 << 28, page=1 << 33), dict(page=1 << 32), dict(s_page=1 << 32),
                 dict(s_row=1 << 26, s_head=16, s_group=64, s_page=1 << 30)):
         assert _validate(**bad) == "UNSUPPORTED", bad
 
