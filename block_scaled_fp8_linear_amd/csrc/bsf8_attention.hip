@@ -36,11 +36,10 @@
 namespace bsf8 {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
+constexpr int kMostWaves = 8;                 // of a block; four or eight
 constexpr int kWaveTokens = 32;
-constexpr int kTile = kWaves * kWaveTokens;   // tokens
 constexpr int kRows = 16;                     // query heads of an item
+constexpr int kWholeTokens = 512;             // up to here an item is a block's
 
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
@@ -66,6 +65,8 @@ struct AttentionDev {
   int32_t window;       // 0: none
   int32_t bound;        // pages * page_size
   int32_t blocks;       // grid of the first kernel
+  int32_t whole;        // a block per item, nothing to join
+  int32_t tile_shift;   // a tile is 1 << tile_shift tokens: 32 for each wave of a block
   int32_t negative;     // the scale is: queries change their sign, and `scale` is its size
   float scale;          // log2(e) included; not zero
   double natural;       // the size of the scale
@@ -81,8 +82,8 @@ struct Task {
 __device__ __forceinline__ int first_token(const AttentionDev& a, int n) { return a.window ? max(0, n - a.window) : 0; }
 // tiles of a sequence of n tokens (one, all of it masked, where there is none), and the first one's number
 __device__ __forceinline__ int tiles_of(const AttentionDev& a, int n, int& first) {
-  first = first_token(a, n) / kTile;
-  return n > 0 ? (n - 1) / kTile - first + 1 : 1;
+  first = first_token(a, n) >> a.tile_shift;
+  return n > 0 ? ((n - 1) >> a.tile_shift) - first + 1 : 1;
 }
 
 // 64 sequences, one per lane: their lengths, tiles, and the tiles up to and with them.
@@ -217,10 +218,13 @@ struct Config {
   static constexpr int KV = E4M3 ? DIM / 64 : DIM / 32;   // 16-byte key loads per token and lane
   static constexpr int QS = DIM / 32;                  // query pieces: 32 channels each
   static constexpr int CHANNELS = NG * 128;
+  static constexpr int PITCH = CHANNELS + 4;           // floats of a row in LDS
   static constexpr int SLOT = kRows * CHANNELS + 2 * kRows;   // floats of a partial result
 };
-// Blocks per compute unit (waves per SIMD) that the registers allow.
-constexpr int blocks_per_cu(bool e4m3, int dim) { return dim > 128 ? 2 : 3; }
+// Waves per SIMD that the registers allow.
+constexpr int waves_per_simd(bool e4m3, int dim) { return dim > 128 ? 2 : 3; }
+// Waves of a block: wide heads with F32 queries take half of a SIMD's registers and more.
+constexpr int most_waves(int dim, bool f32) { return dim > 128 && f32 ? 4 : kMostWaves; }
 constexpr int slot_floats(int dim) { return Config<false, 128, false, 1, 2, kAny>::SLOT + (dim > 128 ? kRows * 128 : 0); }
 
 template <bool NT, typename T>
@@ -282,35 +286,50 @@ struct Queries {
 };
 
 template <class C>
-__global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C::DIM)) void attention_kernel(AttentionDev a) {
+__global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), C::QT > 1 ? 1 : waves_per_simd(C::E4M3, C::DIM)) void attention_kernel(AttentionDev a) {
   constexpr bool E4M3 = C::E4M3, PAGES16 = C::PAGES16;
   constexpr int NG = C::NG, KV = C::KV, QT = C::QT, PT = C::PT, QS = C::QS;
-  constexpr int PITCH = C::CHANNELS + 4;
-  __shared__ float lds_o[kWaves][kRows][PITCH];
-  __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
+  constexpr int PITCH = C::PITCH;
+  // a wave's part of a result: its sums (kRows x PITCH), and for all waves maxima and sums of weights
+  extern __shared__ __attribute__((aligned(16))) float lds_o[];
+  __shared__ float lds_m[kMostWaves][kRows], lds_l[kMostWaves][kRows];
+  const int waves = int(blockDim.x >> 6), tile_tokens = 1 << a.tile_shift;
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i16 = lane & 15;
   const int D = C::FULL ? C::DIM : a.c.head_dim;
 
-  Lengths seq = lengths_of(a, 0);
-  int total = __builtin_amdgcn_readlane(seq.sum, 63);
-  for (int base = 64; base < a.B; base += 64) total += __builtin_amdgcn_readlane(lengths_of(a, base).sum, 63);
-  total *= a.items;
-  const Ranges ranges(total, a.blocks);
-  const int t_begin = ranges.begin_of(int(blockIdx.x)), t_end = ranges.begin_of(int(blockIdx.x) + 1);
-  if (t_begin >= t_end) {
-    if (!a.by_item && a.tasks && threadIdx.x == 0) a.tasks[blockIdx.x].rows = 0;
-    return;
+  // the block's tiles, and the item of the first: sequence, key head, first query head of the key head's, tile
+  int t_begin, t_end, b, n, first, n_tiles, item, j, base = 0;
+  Lengths seq;
+  Ranges ranges(0, 1);
+  if (a.whole) {
+    b = int(blockIdx.x / unsigned(a.items));
+    item = int(blockIdx.x) - b * a.items;
+    n = min(max(((ConstInts)a.lens)[b], 0), a.bound);
+    n_tiles = tiles_of(a, n, first);
+    t_begin = j = 0;
+    t_end = n_tiles;
+  } else {
+    seq = lengths_of(a, 0);
+    int total = __builtin_amdgcn_readlane(seq.sum, 63);
+    for (int at = 64; at < a.B; at += 64) total += __builtin_amdgcn_readlane(lengths_of(a, at).sum, 63);
+    total *= a.items;
+    ranges = Ranges(total, a.blocks);
+    t_begin = ranges.begin_of(int(blockIdx.x));
+    t_end = ranges.begin_of(int(blockIdx.x) + 1);
+    if (t_begin >= t_end) {
+      if (!a.by_item && threadIdx.x == 0) a.tasks[blockIdx.x].rows = 0;
+      return;
+    }
+    int before;
+    b = find_sequence(a, seq, base, t_begin / a.items, before);
+    n = __builtin_amdgcn_readlane(seq.n, b - base);
+    n_tiles = tiles_of(a, n, first);
+    item = (t_begin - before * a.items) / n_tiles;
+    j = (t_begin - before * a.items) - item * n_tiles;
   }
-  // the item at t_begin: sequence, key head, first query head of the key head's, tile
-  int before, base;
-  int b = find_sequence(a, seq, base, t_begin / a.items, before);
-  int n = __builtin_amdgcn_readlane(seq.n, b - base), first;
-  int n_tiles = tiles_of(a, n, first);
-  const int item = (t_begin - before * a.items) / n_tiles;
   int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * kRows;
-  int j = (t_begin - before * a.items) - item * n_tiles;
 
   // byte offsets of a lane's pieces within a row, with its token's (the key's i16, the first
   // value's 4 g); channels past head_dim are read as others that exist (queries are zero there,
@@ -326,7 +345,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
     // the item's tiles j .. j_end - 1 are this block's
     const int j_end = min(n_tiles, j + (t_end - t));
     const int rows = min(kRows, a.G - row0), head0 = h * a.G + row0;
-    const int start = first_token(a, n), stop = min(n, (first + j_end) * kTile);
+    const int start = first_token(a, n), stop = min(n, (first + j_end) << a.tile_shift);
 
     // ---- where a wave's 32 tokens lie.  Entries of the table are asked for a tile before they are needed
     struct Entries {
@@ -439,7 +458,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
     };
 
 
-    int pos = (first + j) * kTile + wave * kWaveTokens;
+    int pos = ((first + j) << a.tile_shift) + wave * kWaveTokens;
     Where w;
     Entries ahead;
     Queries<C> queries;
@@ -451,7 +470,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
       load_keys(w);
       if (E4M3) load_scales(w, a.c.v_scale, vsc);
       load_values(w);
-      ahead = entries(pos + kTile);
+      ahead = entries(pos + tile_tokens);
     }
     v8bf qf[QS][QT];
     queries.end(a, rows, qf);
@@ -467,8 +486,8 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
       constexpr bool LOADS = decltype(loads)::value;
       const uint32_t mask = w.mask;
       if (LOADS) {
-        locate(pos + kTile, ahead, w);
-        ahead = entries(pos + 2 * kTile);
+        locate(pos + tile_tokens, ahead, w);
+        ahead = entries(pos + 2 * tile_tokens);
       }
 
       // ---- logits of 8 tokens and one head per lane
@@ -589,7 +608,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
         load_values(w);
       }
     };
-    for (; pos + kTile < stop; pos += kTile) tile(std::true_type{});
+    for (; pos + tile_tokens < stop; pos += tile_tokens) tile(std::true_type{});
     if (pos < stop) tile(std::false_type{});
 
     // ---- the waves' parts of the segment
@@ -600,8 +619,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
     }
     __syncthreads();
     float top = lds_m[0][i16];
-#pragma unroll
-    for (int x = 1; x < kWaves; ++x) top = fmaxf(top, lds_m[x][i16]);
+    for (int x = 1; x < waves; ++x) top = fmaxf(top, lds_m[x][i16]);
     const float mine = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale);
 #pragma unroll
     for (int c = 0; c < NG; ++c)
@@ -612,7 +630,7 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
           f4 v;
 #pragma unroll
           for (int x = 0; x < 4; ++x) v[x] = o[c][4 * y + x][r] * mine;
-          *reinterpret_cast<f4*>(&lds_o[wave][i16][c * 128 + (4 * g + r) * 8 + 4 * y]) = v;
+          *reinterpret_cast<f4*>(&lds_o[(wave * kRows + i16) * PITCH + c * 128 + (4 * g + r) * 8 + 4 * y]) = v;
         }
     __syncthreads();
     const bool whole = j == 0 && j_end == n_tiles;
@@ -627,17 +645,16 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
       task->to = begins ? ranges.block_of(t + n_tiles - 1) : 0;
     }
     float* part = a.part + int64_t(slot) * C::SLOT;
-    for (int x = threadIdx.x; x < kRows * (C::CHANNELS / 4); x += kThreads) {
+    for (int x = threadIdx.x; x < kRows * (C::CHANNELS / 4); x += int(blockDim.x)) {
       const int row = x / (C::CHANNELS / 4), ch = 4 * (x % (C::CHANNELS / 4));
       if (row >= rows || ch >= D) continue;
-      f4 v = *reinterpret_cast<const f4*>(&lds_o[0][row][ch]);
-#pragma unroll
-      for (int y = 1; y < kWaves; ++y) v += *reinterpret_cast<const f4*>(&lds_o[y][row][ch]);
-      float all_m = lds_m[0][row], all_l = 0.f;
-#pragma unroll
-      for (int y = 1; y < kWaves; ++y) all_m = fmaxf(all_m, lds_m[y][row]);
-#pragma unroll
-      for (int y = 0; y < kWaves; ++y)
+      f4 v = f4{0.f, 0.f, 0.f, 0.f};
+      float all_m = -INFINITY, all_l = 0.f;
+      for (int y = 0; y < waves; ++y) {
+        v += *reinterpret_cast<const f4*>(&lds_o[(y * kRows + row) * PITCH + ch]);
+        all_m = fmaxf(all_m, lds_m[y][row]);
+      }
+      for (int y = 0; y < waves; ++y)
         all_l += all_m == -INFINITY ? 0.f : lds_l[y][row] * __builtin_amdgcn_exp2f((lds_m[y][row] - all_m) * a.scale);
       if (whole) {
         store_result(a, b, head0 + row, ch, v, all_m, all_l);
@@ -671,10 +688,10 @@ __global__ __launch_bounds__(kThreads, C::QT > 1 ? 1 : blocks_per_cu(C::E4M3, C:
 
 // Adds the parts of the items that lie in more than one block, a query head per block of this
 // kernel: groups of lanes take every so many parts, with a maximum of their own.
-template <int DIM>
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttentionDev a) {
+template <int DIM, int THREADS>
+__global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionDev a) {
   using C = Config<false, DIM, false, 1, 2, kAny>;   // (a slot has one size for both types of cache)
-  constexpr int LANES = C::CHANNELS / 4, GROUPS = kThreads / LANES, FLIGHT = 8;
+  constexpr int LANES = C::CHANNELS / 4, GROUPS = THREADS / LANES, FLIGHT = 8;
   __shared__ float lds_o[GROUPS][C::CHANNELS], lds_m[GROUPS], lds_l[GROUPS];
   const Task task = a.tasks[blockIdx.x];
   const int row = int(blockIdx.y);
@@ -745,23 +762,45 @@ int compute_units() {
   return known;
 }
 
-// Blocks of the first kernel: as many as the device holds at once, or a block per tile.
-int64_t grid_blocks(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
-  const int64_t row_tiles = (q_heads / c.heads + kRows - 1) / kRows;
-  const int64_t most = B * c.heads * row_tiles * (bound / kTile + 2);
-  const int64_t held = int64_t(compute_units()) * blocks_per_cu(c.e4m3 != 0, c.head_dim);
-  return most < held ? most : held;
+// How a call is cut up, from what the host knows.
+struct Plan {
+  int64_t items;     // of the batch
+  int64_t blocks;
+  int32_t whole, waves;
+};
+Plan plan_of(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound, bool f32) {
+  Plan p{};
+  p.items = B * c.heads * ((q_heads / c.heads + kRows - 1) / kRows);
+  const int64_t held = compute_units() * waves_per_simd(c.e4m3 != 0, c.head_dim);   // blocks of four waves that run at once
+  p.waves = 4;
+  const int64_t tiles = bound / (p.waves * kWaveTokens) + 1;
+  // A block per item where the longest is short (one sequence of 200 tokens 13.4 -> 10.0 us, with
+  // eight waves) or where so many items follow each other on a compute unit that they even out (8
+  // key heads: 256 sequences to 1000 88 -> 77 us, to 2000 149 -> 146, but to 4000 260 -> 282; 64 to
+  // 1000 29.0 -> 29.7, to 2000 44 -> 54; 24 key heads, 256 to 1000 174 -> 127).
+  p.whole = bound <= kWholeTokens || tiles * held <= 8 * p.items ? 1 : 0;
+  if (p.whole) {
+    p.blocks = p.items;
+    if (2 * p.items < held && tiles > 1) p.waves = most_waves(c.head_dim, f32);
+    return p;
+  }
+  const int64_t most = p.items * (tiles + 1);
+  p.blocks = most < held ? most : held;
+  return p;
 }
 
 template <bool E4M3, int DIM, bool FULL, int QT, int PT>
 void launch_pages(const AttentionDev& a, bool scale_vec, hipStream_t stream) {
-  const dim3 grid{unsigned(a.blocks)}, block{kThreads};
+  using Any = Config<E4M3, DIM, FULL, QT, PT, kAny>;
+  const int waves = 1 << (a.tile_shift - 5);
+  const dim3 grid{unsigned(a.blocks)}, block{unsigned(64 * waves)};
+  const unsigned lds = unsigned(waves * kRows * Any::PITCH * sizeof(float));
   if (a.c.page_size % 16)
-    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kAny>>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((attention_kernel<Any>), grid, block, lds, stream, a);
   else if (!E4M3 || scale_vec)   // (BF16: no scales)
-    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalvesWide>>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalvesWide>>), grid, block, lds, stream, a);
   else if constexpr (E4M3)
-    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalves>>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((attention_kernel<Config<E4M3, DIM, FULL, QT, PT, kHalves>>), grid, block, lds, stream, a);
 }
 template <bool E4M3>
 void launch_dims(const AttentionDev& a, bool f32, bool scale_vec, hipStream_t stream) {
@@ -778,13 +817,12 @@ void launch_dims(const AttentionDev& a, bool f32, bool scale_vec, hipStream_t st
 }  // namespace
 
 int64_t attention_tiles(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
-  return B * c.heads * ((q_heads / c.heads + kRows - 1) / kRows) * (bound / kTile + 2);
+  return B * c.heads * ((q_heads / c.heads + kRows - 1) / kRows) * (bound / (4 * kWaveTokens) + 2);
 }
 
 size_t attention_workspace_bytes(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
-  if (bound <= kTile || B == 0) return 0;   // no item is ever split
-  const size_t slot = slot_floats(c.head_dim);
-  return size_t(grid_blocks(c, B, q_heads, bound)) * (2 * slot * sizeof(float) + sizeof(Task));
+  const Plan p = plan_of(c, B, q_heads, bound, false);   // (the type changes the waves of a block, not the blocks)
+  return p.whole ? 0 : size_t(p.blocks) * (2 * slot_floats(c.head_dim) * sizeof(float) + sizeof(Task));
 }
 
 bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDev& out, int64_t B, const int32_t* table,
@@ -808,25 +846,34 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   a.window = window >= a.bound ? 0 : int32_t(window);
   const bool scale_vec = c.s_row == 1 && ((c.s_page | c.s_head | c.s_group) & 3) == 0 &&
                          ((reinterpret_cast<uintptr_t>(c.k_scale) | reinterpret_cast<uintptr_t>(c.v_scale)) & 15) == 0;
-  a.blocks = int32_t(grid_blocks(c, B, q.heads, a.bound));
-  if (a.bound > kTile) {
-    const size_t slot = slot_floats(c.head_dim);
-    a.tasks = reinterpret_cast<Task*>(a.part + size_t(a.blocks) * 2 * slot);
-    a.by_item = B * a.items <= a.blocks ? 1 : 0;
+  const bool f32 = !q.bf16 || !out.bf16;
+  const Plan plan = plan_of(c, B, q.heads, a.bound, f32);
+  a.blocks = int32_t(plan.blocks);
+  a.whole = plan.whole;
+  a.tile_shift = plan.waves == 8 ? 8 : 7;
+  if (!plan.whole) {
+    a.tasks = reinterpret_cast<Task*>(a.part + size_t(a.blocks) * 2 * slot_floats(c.head_dim));
+    a.by_item = plan.items <= a.blocks ? 1 : 0;
   }
   a.negative = scale < 0.0 ? 1 : 0;
   a.natural = scale < 0.0 ? -scale : scale;
   a.scale = float(a.natural * 1.4426950408889634);
   if (!(a.scale > 1e-30f)) a.scale = 1e-30f;   // (the weights are 1 there, and -inf times it stays -inf)
-  const bool f32 = !q.bf16 || !out.bf16;
   if (c.e4m3) launch_dims<true>(a, f32, scale_vec, stream);
   else launch_dims<false>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");
-  if (st != BSF8_OK || a.bound <= kTile) return st;
+  if (st != BSF8_OK || plan.whole) return st;
   const unsigned rows = unsigned(a.G < kRows ? a.G : kRows);
-  const dim3 grid(a.by_item ? unsigned(B * a.items) : unsigned(a.blocks), rows);
-  if (c.head_dim > 128) hipLaunchKernelGGL(attention_join_kernel<256>, grid, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL(attention_join_kernel<128>, grid, dim3(kThreads), 0, stream, a);
+  const dim3 grid(unsigned(a.by_item ? plan.items : plan.blocks), rows);
+  // hundreds of parts to an item: all of them in flight at once
+  const bool many = plan.blocks > 32 * plan.items;
+  if (c.head_dim > 128) {
+    if (many) hipLaunchKernelGGL((attention_join_kernel<256, 1024>), grid, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((attention_join_kernel<256, 256>), grid, dim3(256), 0, stream, a);
+  } else {
+    if (many) hipLaunchKernelGGL((attention_join_kernel<128, 1024>), grid, dim3(1024), 0, stream, a);
+    else hipLaunchKernelGGL((attention_join_kernel<128, 256>), grid, dim3(256), 0, stream, a);
+  }
   return device_status(hipGetLastError(), "paged_attention join launch");
 }
 
