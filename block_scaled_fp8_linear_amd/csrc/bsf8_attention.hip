@@ -222,7 +222,7 @@ struct Config {
   static constexpr int SLOT = kRows * CHANNELS + 2 * kRows;   // floats of a partial result
 };
 // Waves per SIMD that the registers allow.
-constexpr int waves_per_simd(bool e4m3, int dim) { return dim > 128 ? 2 : 3; }
+constexpr int waves_per_simd(int dim, bool f32) { return dim > 128 ? (f32 ? 1 : 2) : f32 ? 2 : 3; }
 // Waves of a block: wide heads with F32 queries take half of a SIMD's registers and more.
 constexpr int most_waves(int dim, bool f32) { return dim > 128 && f32 ? 4 : kMostWaves; }
 constexpr int slot_floats(int dim) { return Config<false, 128, false, 1, 2, kAny>::SLOT + (dim > 128 ? kRows * 128 : 0); }
@@ -286,7 +286,7 @@ struct Queries {
 };
 
 template <class C>
-__global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), C::QT > 1 ? 1 : waves_per_simd(C::E4M3, C::DIM)) void attention_kernel(AttentionDev a) {
+__global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(C::DIM, C::QT > 1)) void attention_kernel(AttentionDev a) {
   constexpr bool E4M3 = C::E4M3, PAGES16 = C::PAGES16;
   constexpr int NG = C::NG, KV = C::KV, QT = C::QT, PT = C::PT, QS = C::QS;
   constexpr int PITCH = C::PITCH;
@@ -611,27 +611,29 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), C::QT > 1 ? 1 :
     for (; pos + tile_tokens < stop; pos += tile_tokens) tile(std::true_type{});
     if (pos < stop) tile(std::false_type{});
 
-    // ---- the waves' parts of the segment
+    // ---- the waves' parts of the segment: maxima, then sums brought to the common one
     l = sum_of_groups(l);
-    if (g == 0) {
-      lds_m[wave][i16] = m;
-      lds_l[wave][i16] = l;
-    }
+    if (g == 0) lds_m[wave][i16] = m;
     __syncthreads();
     float top = lds_m[0][i16];
-    for (int x = 1; x < waves; ++x) top = fmaxf(top, lds_m[x][i16]);
+    for (int y = 0; y < waves; y += 4)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) top = fmaxf(top, lds_m[y + x][i16]);
     const float mine = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((m - top) * a.scale);
+    if (g == 0) lds_l[wave][i16] = l * mine;
+    if (i16 < rows) {
 #pragma unroll
-    for (int c = 0; c < NG; ++c)
+      for (int c = 0; c < NG; ++c)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          f4 v;
+          for (int y = 0; y < 2; ++y) {
+            f4 v;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = o[c][4 * y + x][r] * mine;
-          *reinterpret_cast<f4*>(&lds_o[(wave * kRows + i16) * PITCH + c * 128 + (4 * g + r) * 8 + 4 * y]) = v;
-        }
+            for (int x = 0; x < 4; ++x) v[x] = o[c][4 * y + x][r] * mine;
+            *reinterpret_cast<f4*>(&lds_o[(wave * kRows + i16) * PITCH + c * 128 + (4 * g + r) * 8 + 4 * y]) = v;
+          }
+    }
     __syncthreads();
     const bool whole = j == 0 && j_end == n_tiles;
     const int slot = int(blockIdx.x) * 2 + (t == t_begin ? 0 : 1);
@@ -650,12 +652,13 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), C::QT > 1 ? 1 :
       if (row >= rows || ch >= D) continue;
       f4 v = f4{0.f, 0.f, 0.f, 0.f};
       float all_m = -INFINITY, all_l = 0.f;
-      for (int y = 0; y < waves; ++y) {
-        v += *reinterpret_cast<const f4*>(&lds_o[(y * kRows + row) * PITCH + ch]);
-        all_m = fmaxf(all_m, lds_m[y][row]);
-      }
-      for (int y = 0; y < waves; ++y)
-        all_l += all_m == -INFINITY ? 0.f : lds_l[y][row] * __builtin_amdgcn_exp2f((lds_m[y][row] - all_m) * a.scale);
+      for (int y = 0; y < waves; y += 4)
+#pragma unroll
+        for (int z = y; z < y + 4; ++z) {
+          v += *reinterpret_cast<const f4*>(&lds_o[(z * kRows + row) * PITCH + ch]);
+          all_m = fmaxf(all_m, lds_m[z][row]);
+          all_l += lds_l[z][row];
+        }
       if (whole) {
         store_result(a, b, head0 + row, ch, v, all_m, all_l);
       } else {
@@ -771,7 +774,7 @@ struct Plan {
 Plan plan_of(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound, bool f32) {
   Plan p{};
   p.items = B * c.heads * ((q_heads / c.heads + kRows - 1) / kRows);
-  const int64_t held = compute_units() * waves_per_simd(c.e4m3 != 0, c.head_dim);   // blocks of four waves that run at once
+  const int64_t held = compute_units() * waves_per_simd(c.head_dim, f32);   // blocks of four waves that run at once
   p.waves = 4;
   const int64_t tiles = bound / (p.waves * kWaveTokens) + 1;
   // A block per item where the longest is short (one sequence of 200 tokens 13.4 -> 10.0 us, with
@@ -821,7 +824,7 @@ int64_t attention_tiles(const CacheDev& c, int64_t B, int32_t q_heads, int64_t b
 }
 
 size_t attention_workspace_bytes(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound) {
-  const Plan p = plan_of(c, B, q_heads, bound, false);   // (the type changes the waves of a block, not the blocks)
+  const Plan p = plan_of(c, B, q_heads, bound, false);   // (F32 calls have fewer blocks, or none to join, not more)
   return p.whole ? 0 : size_t(p.blocks) * (2 * slot_floats(c.head_dim) * sizeof(float) + sizeof(Task));
 }
 
