@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, List, Optional, Sequence, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -171,15 +172,12 @@ EXPORTS = [
                                         ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_void_p]),
     ("bsf8_cache_validate", ctypes.c_int, [ctypes.POINTER(Cache)]),
-    ("bsf8_rope", ctypes.c_int, [ctypes.POINTER(RopeArgs), _ptr]),
-    ("bsf8_cache_write", ctypes.c_int, [ctypes.POINTER(Cache), _i64, ctypes.POINTER(Heads), ctypes.POINTER(Heads), _ptr,
-                                        _i32, ctypes.POINTER(RopeArgs), _ptr]),
-    ("bsf8_cache_read", ctypes.c_int, [ctypes.POINTER(Cache), _i64, _ptr, _i64, _i64, _ptr, _ptr, _i64,
-                                       ctypes.POINTER(Heads), ctypes.POINTER(Heads), _ptr]),
-    ("bsf8_attention_workspace_size", ctypes.c_int, [ctypes.POINTER(Cache), _i64, _i32, _i64,
-                                                     ctypes.POINTER(ctypes.c_size_t)]),
-    ("bsf8_paged_attention", ctypes.c_int, [ctypes.POINTER(Cache), ctypes.POINTER(AttentionArgs), _ptr, ctypes.c_size_t,
-                                            _ptr]),
+    # (their structures may come as packed bytes)
+    ("bsf8_rope", ctypes.c_int, [_ptr, _ptr]),
+    ("bsf8_cache_write", ctypes.c_int, [_ptr, _i64, _ptr, _ptr, _ptr, _i32, _ptr, _ptr]),
+    ("bsf8_cache_read", ctypes.c_int, [_ptr, _i64, _ptr, _i64, _i64, _ptr, _ptr, _i64, _ptr, _ptr, _ptr]),
+    ("bsf8_attention_workspace_size", ctypes.c_int, [_ptr, _i64, _i32, _i64, ctypes.POINTER(ctypes.c_size_t)]),
+    ("bsf8_paged_attention", ctypes.c_int, [_ptr, _ptr, _ptr, ctypes.c_size_t, _ptr]),
     ("bsf8_upcast", ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p]),
     ("bsf8_dense_workspace_size", ctypes.c_int, [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                  ctypes.POINTER(ctypes.c_size_t)]),
@@ -975,14 +973,40 @@ def linear_dense(wd, x, out_dtype=None, out=None, workspace=None):
 
 # ---------------------------------------------------- rotary positions and the paged cache
 
-def _heads(name, t, M, heads, D, dtypes, out=None) -> Heads:
-    """bsf8_heads of ``t``, which must be [M, heads, D] of one of ``dtypes`` with unit channel stride."""
-    dt = t.dtype
-    if t.shape == (M, heads, D) and dt in dtypes:
+# The structures below go to the library as packed bytes: one call in place of a ctypes object and an assignment per
+# field (2 to 3 us of a call's host time).
+_HEADS = struct.Struct("Piiqq")                                             # bsf8_heads
+_ROPE = struct.Struct("qiiiiPixxxxqPPdd" + "Piiqq" * 4 + "PPixxxx")         # bsf8_rope_args
+_ATTENTION = struct.Struct("q" + "Piiqq" * 2 + "PqqPqdP")                   # bsf8_attention_args
+_ABSENT = (0, 0, 0, 0, 0)
+_REAL: Dict[object, int] = {}
+
+
+def _real(t) -> int:
+    """The type code of a float32 or bfloat16 tensor, 0 for any other."""
+    if not _REAL:
+        torch = _torch()
+        _REAL.update({torch.float32: DT_F32, torch.bfloat16: DT_BF16})
+    return _REAL.get(t.dtype, 0)
+
+
+def _all_on(idx, names, *tensors):
+    """_on_device against the device number ``idx``; ``names``: the tensors' names, for the refusal."""
+    for t in tensors:
+        if t is not None and t.get_device() != idx:
+            _on_device(_torch().device("cuda", idx), **dict(zip(names.split(), tensors)))
+
+
+def _heads(name, t, M, heads, D, dtype=0):
+    """The fields of bsf8_heads for ``t``, which must be [M, heads, D] with unit channel stride, float32 or bfloat16
+    (``dtype``: that type code)."""
+    code = _real(t)
+    if code and (dtype == 0 or code == dtype) and t.shape == (M, heads, D):
         s0, s1, s2 = t.stride()
         if s2 == 1:
-            return Heads(t.data_ptr(), DT_BF16 if dt is _T.bfloat16 else DT_F32, heads, s0, s1)
-    raise ValueError(f"{name} must be [{M}, {heads}, {D}] with unit channel stride, of one of {dtypes}")
+            return t.data_ptr(), code, heads, s0, s1
+    raise ValueError(f"{name} must be [{M}, {heads}, {D}] with unit channel stride, "
+                     f"{ {0: 'float32 or bfloat16', DT_F32: 'float32', DT_BF16: 'bfloat16'}[dtype]}")
 
 
 class PagedKVCache:
@@ -1041,7 +1065,17 @@ class PagedKVCache:
 PAIRINGS = {"half": 0, "adjacent": 1}
 
 
-def rope_axes(sections: Sequence[int], interleaved: bool = False) -> bytes:
+class RopeAxes(bytes):
+    """Axis numbers of the rotated pairs, kept where the library can read them."""
+
+    def __new__(cls, numbers):
+        self = bytes.__new__(cls, numbers)
+        self._held = ctypes.create_string_buffer(bytes(self), max(1, len(self)))
+        self.address = ctypes.addressof(self._held)
+        return self
+
+
+def rope_axes(sections: Sequence[int], interleaved: bool = False) -> RopeAxes:
     """The axis of each rotated pair, for ``axes`` of rope and cache_write: ``sections`` pairs of each axis one after the
     other, or, interleaved, pair i on axis i % A while i < A * sections[i % A] and on axis 0 otherwise (axis 0 takes what
     the others leave)."""
@@ -1049,63 +1083,75 @@ def rope_axes(sections: Sequence[int], interleaved: bool = False) -> bytes:
     if not 1 <= len(sections) <= 16 or min(sections) < 0:
         raise ValueError("1 to 16 sections of 0 or more pairs")
     if not interleaved:
-        return bytes(a for a, n in enumerate(sections) for _ in range(n))
+        return RopeAxes(a for a, n in enumerate(sections) for _ in range(n))
     A = len(sections)
-    axes = bytes(i % A if i < A * sections[i % A] else 0 for i in range(sum(sections)))
+    axes = RopeAxes(i % A if i < A * sections[i % A] else 0 for i in range(sum(sections)))
     if [axes.count(a) for a in range(A)] != sections:
         raise ValueError(f"sections {sections} cannot be taken in turns")
     return axes
 
 
-def _rotation(a: RopeArgs, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight):
-    """Fill the rotation and the head norms of ``a``."""
-    torch = _torch()
+def _rotation(M, D, positions, inv_freq, axes, pairing, scale, eps):
+    """The fields of bsf8_rope_args up to eps, and what has to live until the call."""
     if pairing not in PAIRINGS:
         raise ValueError(f"pairing must be one of {sorted(PAIRINGS)}")
-    a.M, a.head_dim, a.pairing, a.scale, a.eps = M, D, PAIRINGS[pairing], scale, eps
-    if (positions is None) != (inv_freq is None):
-        raise ValueError("positions and inv_freq: both or neither")
-    if inv_freq is not None:
-        if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
-            raise ValueError("inv_freq must be a contiguous float32 [rotary_dim / 2] tensor")
-        half = inv_freq.shape[0]
-        a.rotary_dim, a.inv_freq = 2 * half, inv_freq.data_ptr()
-        dt = positions.dtype
-        if dt is torch.int32:
-            a.position_bytes = 4
-        elif dt is torch.int64:
-            a.position_bytes = 8
-        else:
-            raise ValueError("positions must be int32 or int64")
-        dims = positions.dim()
-        if dims not in (1, 2) or positions.shape[-1] != M or (M > 1 and positions.stride(-1) != 1):
-            raise ValueError(f"positions must be [M] or [axes, M] with M = {M} and unit token stride")
-        a.positions = positions.data_ptr()
-        a.n_axes, a.ld_axis = (1, 0) if dims == 1 else (positions.shape[0], positions.stride(0))
+    if inv_freq is None or positions is None:
+        if inv_freq is not None or positions is not None:
+            raise ValueError("positions and inv_freq: both or neither")
         if axes is not None:
-            if len(axes) != half:
-                raise ValueError(f"axes must name one axis for each of the {half} pairs")
-            a.axis = axes if type(axes) is bytes else bytes(axes)
-        elif a.n_axes != 1:
-            raise ValueError("positions of several axes need axes (see rope_axes)")
-    elif axes is not None:
-        raise ValueError("axes without positions")
-    if q_weight is not None:
-        a.q_weight, a.weight_dtype = _vector("q_weight", q_weight, D, (torch.float32, torch.bfloat16)), _dt_of(q_weight)
-    if k_weight is not None:
-        a.k_weight, a.weight_dtype = _vector("k_weight", k_weight, D, (torch.float32, torch.bfloat16)), _dt_of(k_weight)
-        if q_weight is not None and q_weight.dtype != k_weight.dtype:
-            raise ValueError("q_weight and k_weight must have one type")
+            raise ValueError("axes without positions")
+        return (M, D, 0, PAIRINGS[pairing], 0, 0, 0, 0, 0, 0, scale, eps), None
+    torch = _torch()
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float32 [rotary_dim / 2] tensor")
+    dt = positions.dtype
+    size = 4 if dt is torch.int32 else 8 if dt is torch.int64 else 0
+    if not size:
+        raise ValueError("positions must be int32 or int64")
+    shape, strides, half = positions.shape, positions.stride(), inv_freq.shape[0]
+    if len(shape) not in (1, 2) or shape[-1] != M or (M > 1 and strides[-1] != 1):
+        raise ValueError(f"positions must be [M] or [axes, M] with M = {M} and unit token stride")
+    n_axes, ld = (1, 0) if len(shape) == 1 else (shape[0], strides[0])
+    at = 0
+    if axes is not None:
+        if len(axes) != half:
+            raise ValueError(f"axes must name one axis for each of the {half} pairs")
+        if type(axes) is not RopeAxes:
+            axes = RopeAxes(axes)
+        at = axes.address
+    elif n_axes != 1:
+        raise ValueError("positions of several axes need axes (see rope_axes)")
+    return (M, D, 2 * half, PAIRINGS[pairing], n_axes, positions.data_ptr(), size, ld, at, inv_freq.data_ptr(), scale, eps), axes
 
 
-def _turned(name, t, M, heads, D, out, out_dtype, real):
-    """(output, its bsf8_heads) of rotated heads ``t``."""
+def _head_weights(D, q_weight, k_weight):
+    """The last fields of bsf8_rope_args."""
+    if q_weight is None and k_weight is None:
+        return 0, 0, 0
+    torch = _torch()
+    real = (torch.float32, torch.bfloat16)
+    if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
+        raise ValueError("q_weight and k_weight must have one type")
+    return (_vector("q_weight", q_weight, D, real) if q_weight is not None else 0,
+            _vector("k_weight", k_weight, D, real) if k_weight is not None else 0,
+            _real(q_weight if q_weight is not None else k_weight))
+
+
+def _turned(name, t, M, heads, D, out, out_dtype):
+    """(output, the fields of its bsf8_heads) of heads ``t``."""
     if out is None:
-        out = _T.empty((M, heads, D), dtype=out_dtype or t.dtype, device=t.device)
-        if out.dtype not in real:
+        if out_dtype is None or out_dtype is t.dtype:
+            out = _T.empty_like(t)
+        else:
+            out = _T.empty((M, heads, D), dtype=out_dtype, device=t.device)
+        if not _real(out):
             raise ValueError("out_dtype must be float32 or bfloat16")
-        return out, Heads(out.data_ptr(), DT_BF16 if out.dtype is _T.bfloat16 else DT_F32, heads, heads * D, D)
-    return out, _heads(name, out, M, heads, D, real if out_dtype is None else (out_dtype,))
+        s0, s1, s2 = out.stride()
+        if s2 == 1:
+            return out, (out.data_ptr(), _real(out), heads, s0, s1)
+        out = _T.empty((M, heads, D), dtype=out.dtype, device=t.device)
+        return out, (out.data_ptr(), _real(out), heads, heads * D, D)
+    return out, _heads(name, out, M, heads, D, 0 if out_dtype is None else _REAL.get(out_dtype, -1))
 
 
 def rope(q, positions, inv_freq, *, k=None, axes=None, pairing="half", scale=1.0, q_weight=None, k_weight=None, eps=1e-6,
@@ -1118,24 +1164,23 @@ def rope(q, positions, inv_freq, *, k=None, axes=None, pairing="half", scale=1.0
     ``pairing`` "half", (2i, 2i + 1) with "adjacent"; ``scale`` multiplies the turned channels.  q_weight, k_weight [D]:
     the RMS norm of each head before it turns.  Computed in 64 bits, rounded to float32 and to the output's type (the
     input's unless out_dtype or the outputs say otherwise); an output may be its input."""
-    torch = _torch()
-    real = (torch.float32, torch.bfloat16)
     idx = _gpu_index("q", q)
-    _same_device(idx, positions=positions, inv_freq=inv_freq, k=k, q_weight=q_weight, k_weight=k_weight, out=out, k_out=k_out)
+    _all_on(idx, "positions inv_freq k q_weight k_weight out k_out", positions, inv_freq, k, q_weight, k_weight, out, k_out)
     if q.dim() != 3 or (k is not None and k.dim() != 3):
         raise ValueError("q and k must be [M, heads, head_dim]")
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight or k_out without k")
     M, H, D = q.shape
-    a = RopeArgs()
-    _rotation(a, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight)
-    a.q = _heads("q", q, M, H, D, real)
-    out, a.q_out = _turned("out", q, M, H, D, out, out_dtype, real)
+    turn, _held = _rotation(M, D, positions, inv_freq, axes, pairing, scale, eps)
+    q_in = _heads("q", q, M, H, D)
+    out, q_out = _turned("out", q, M, H, D, out, out_dtype)
+    k_in = k_to = _ABSENT
     if k is not None:
         kv = k.shape[1]
-        a.k = _heads("k", k, M, kv, D, real)
-        k_out, a.k_out = _turned("k_out", k, M, kv, D, k_out, out_dtype, real)
-    _launch("rope", idx, lib().bsf8_rope, ctypes.byref(a))
+        k_in = _heads("k", k, M, kv, D)
+        k_out, k_to = _turned("k_out", k, M, kv, D, k_out, out_dtype)
+    _launch("rope", idx, lib().bsf8_rope,
+            _ROPE.pack(*turn, *q_in, *q_out, *k_in, *k_to, *_head_weights(D, q_weight, k_weight)))
     return out, k_out
 
 
@@ -1146,31 +1191,29 @@ def cache_write(cache: PagedKVCache, k, v, slots, *, positions=None, inv_freq=No
     rotated (and normed) on the way as rope does, and queries ``q`` in the same launch; returns rope's q', None without q.
     Slots of one call must differ."""
     torch = _torch()
-    real = (torch.float32, torch.bfloat16)
     idx = cache._idx
-    _same_device(idx, k=k, v=v, slots=slots, positions=positions, inv_freq=inv_freq, k_weight=k_weight, q=q,
-                 q_weight=q_weight, out=out)
-    D = cache.head_dim
-    if slots.dim() != 1 or slots.dtype not in (torch.int32, torch.int64) or not slots.is_contiguous():
+    _all_on(idx, "k v slots positions inv_freq k_weight q q_weight out", k, v, slots, positions, inv_freq, k_weight, q, q_weight, out)
+    H, D = cache.heads, cache.head_dim
+    dt = slots.dtype
+    size = 4 if dt is torch.int32 else 8 if dt is torch.int64 else 0
+    if slots.dim() != 1 or not size or not slots.is_contiguous():
         raise ValueError("slots must be a contiguous int32 or int64 [M] tensor")
     M = slots.shape[0]
-    kh = _heads("k", k, M, cache.heads, D, real)
-    vh = _heads("v", v, M, cache.heads, D, real)
+    k_in, v_in = _heads("k", k, M, H, D), _heads("v", v, M, H, D)
     if q is None and (out is not None or out_dtype is not None or q_weight is not None):
         raise ValueError("out, out_dtype or q_weight without q")
-    a = None
+    turns = None
     if inv_freq is not None or positions is not None or axes is not None or k_weight is not None or q is not None:
-        r = RopeArgs()
-        _rotation(r, idx, M, D, positions, inv_freq, axes, pairing, scale, eps, q_weight, k_weight)
+        turn, _held = _rotation(M, D, positions, inv_freq, axes, pairing, scale, eps)
+        q_in = q_out = _ABSENT
         if q is not None:
             if q.dim() != 3:
                 raise ValueError("q must be [M, heads, head_dim]")
-            H = q.shape[1]
-            r.q = _heads("q", q, M, H, D, real)
-            out, r.q_out = _turned("out", q, M, H, D, out, out_dtype, real)
-        a = ctypes.byref(r)
-    _launch("cache_write", idx, lib().bsf8_cache_write, cache._ref, M, ctypes.byref(kh), ctypes.byref(vh), slots.data_ptr(),
-            slots.element_size(), a)
+            q_in = _heads("q", q, M, q.shape[1], D)
+            out, q_out = _turned("out", q, M, q.shape[1], D, out, out_dtype)
+        turns = _ROPE.pack(*turn, *q_in, *q_out, *_ABSENT, *_ABSENT, *_head_weights(D, q_weight, k_weight))
+    _launch("cache_write", idx, lib().bsf8_cache_write, cache._ref, M, _HEADS.pack(*k_in), _HEADS.pack(*v_in),
+            slots.data_ptr(), size, turns)
     return out
 
 
@@ -1187,9 +1230,8 @@ def cache_read(cache: PagedKVCache, table, offsets, R: int, *, starts=None, out_
     them.  bfloat16 unless out_dtype or the outputs say float32; a position without a page reads as zeros, rows outside
     every range keep what the outputs hold (new outputs: undefined)."""
     torch = _torch()
-    real = (torch.float32, torch.bfloat16)
     idx = cache._idx
-    _same_device(idx, table=table, offsets=offsets, starts=starts, k_out=k_out, v_out=v_out)
+    _all_on(idx, "table offsets starts k_out v_out", table, offsets, starts, k_out, v_out)
     B = offsets.shape[0] - 1 if offsets.dim() == 1 else -1
     if B < 0 or R < 0:
         raise ValueError("offsets must be int32 [B + 1] and R at least 0")
@@ -1197,19 +1239,18 @@ def cache_read(cache: PagedKVCache, table, offsets, R: int, *, starts=None, out_
     at = _vector("starts", starts, B, (torch.int32,)) if starts is not None else None
     pages, ld = _table("table", table, B)
     H, D = cache.heads, cache.head_dim
-    new = out_dtype or (k_out if k_out is not None else v_out).dtype if k_out is not None or v_out is not None else \
-        out_dtype or torch.bfloat16
-    if new not in real:
+    if out_dtype is None:
+        out_dtype = k_out.dtype if k_out is not None else v_out.dtype if v_out is not None else torch.bfloat16
+    if out_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("out_dtype must be float32 or bfloat16")
     if k_out is None:
-        k_out = torch.empty((R, H, D), dtype=new, device=cache.device)
+        k_out = torch.empty((R, H, D), dtype=out_dtype, device=cache.device)
     if v_out is None:
-        v_out = torch.empty((R, H, D), dtype=new, device=cache.device)
-    kh, vh = _heads("k_out", k_out, R, H, D, (new,)), _heads("v_out", v_out, R, H, D, (new,))
+        v_out = torch.empty_like(k_out)
+    code = _real(k_out) if k_out.dtype is out_dtype else -1
     _launch("cache_read", idx, lib().bsf8_cache_read, cache._ref, B, table.data_ptr(), ld, pages, at, off, R,
-            ctypes.byref(kh), ctypes.byref(vh))
+            _HEADS.pack(*_heads("k_out", k_out, R, H, D, code)), _HEADS.pack(*_heads("v_out", v_out, R, H, D, code)))
     return k_out, v_out
-
 
 
 def paged_attention(q, cache: PagedKVCache, table, lens, *, scale=None, window=0, lse=False, out=None, out_dtype=None,
@@ -1224,33 +1265,28 @@ def paged_attention(q, cache: PagedKVCache, table, lens, *, scale=None, window=0
     bytes) as attention_workspace_size says; without it a call that needs one takes its own from the allocator, so that
     graphs captured on one stream may be replayed at the same time."""
     torch = _torch()
-    real = (torch.float32, torch.bfloat16)
     idx = cache._idx
-    _same_device(idx, q=q, table=table, lens=lens, out=out, workspace=workspace[0] if workspace is not None else None)
+    _all_on(idx, "q table lens out workspace", q, table, lens, out, workspace[0] if workspace is not None else None)
     if q.dim() != 3:
         raise ValueError("q must be [B, heads, head_dim]")
     B, H, D = q.shape
     if D != cache.head_dim or H == 0 or H % cache.heads:
         raise ValueError(f"q must be [B, heads, {cache.head_dim}] with heads a multiple of {cache.heads}")
-    a = AttentionArgs()
-    a.B, a.window, a.scale = B, window, D ** -0.5 if scale is None else scale
-    a.q = _heads("q", q, B, H, D, real)
-    a.lens = _vector("lens", lens, B, (torch.int32,))
-    a.pages, a.ld_table = _table("table", table, B)
-    a.table = table.data_ptr()
-    out, a.out = _turned("out", q, B, H, D, out, out_dtype, real)
-    sums = None
-    if lse:
-        sums = torch.empty((B, H), dtype=torch.float32, device=q.device)
-        a.lse = sums.data_ptr()
+    q_in = _heads("q", q, B, H, D)
+    at = _vector("lens", lens, B, (torch.int32,))
+    pages, ld = _table("table", table, B)
+    out, to = _turned("out", q, B, H, D, out, out_dtype)
+    sums = torch.empty((B, H), dtype=torch.float32, device=q.device) if lse else None
     if workspace is not None:
         ws, wsb = workspace
         if wsb > (ws.numel() * ws.element_size() if ws is not None and ws.is_contiguous() else 0):
             raise ValueError(f"the workspace must be a contiguous tensor of at least the {wsb} bytes given")
     else:
-        wsb = attention_workspace_size(cache, B, H, a.pages) if B else 0
+        wsb = attention_workspace_size(cache, B, H, pages) if B else 0
         ws = torch.empty(wsb, dtype=torch.uint8, device=q.device) if wsb else None
-    _launch("paged_attention", idx, lib().bsf8_paged_attention, cache._ref, ctypes.byref(a),
+    _launch("paged_attention", idx, lib().bsf8_paged_attention, cache._ref,
+            _ATTENTION.pack(B, *q_in, *to, table.data_ptr(), ld, pages, at, window, D ** -0.5 if scale is None else scale,
+                            sums.data_ptr() if lse else 0),
             ws.data_ptr() if ws is not None else None, wsb)
     return (out, sums) if lse else out
 

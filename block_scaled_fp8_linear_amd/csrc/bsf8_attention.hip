@@ -198,9 +198,10 @@ __device__ __forceinline__ void split(const float (&x)[8], v8bf (&t)[N]) {
 
 // What an instance is made for.
 // DIM: channels that its pieces cover (64, 128, 256).  FULL: a head has exactly DIM of them, so
-// that offsets are constants and rows are whole cache lines, which are read non-temporally (each
-// is read once: 64 sequences to 8192 of 128 BF16 channels 156 -> 144 us, of E4M3 99 -> 93; rows
-// that share lines lose by it, 80 channels 185 -> 218).
+// that offsets are constants and rows are whole cache lines.  Values are then read
+// non-temporally, a line by one instruction and once (64 sequences to 8192 of 128 BF16 channels
+// 147 -> 135 us, of E4M3 91 -> 86); a key's line is asked for by two instructions, half each, and
+// is left to the cache (with non-temporal keys one sequence of 131072 takes 33 us, without 31).
 // QT: BF16 terms of a query (1: BF16 queries, 3: F32).  PT: of a softmax weight.  A weight in one
 // term would be off by 2^-9 of itself, as much as the rounding of a BF16 output; two leave 2^-17,
 // three 2^-25.
