@@ -10,7 +10,7 @@
 // A row is LPR = 8, 16 or 32 lanes of 8 channels (head_dim up to 64, 128, 256), so that a
 // 128-channel scale group is 16 lanes, and a wave holds 64 / LPR rows, all of one token:
 // a lane has the same channels in every row it takes, so its angles' sines and cosines are
-// made once for all the heads of the wave.  The pair's other channel is loaded a second time
+// there once for all the heads of the wave.  The pair's other channel is loaded a second time
 // rather than exchanged between lanes: it is in the cache line that the row's own lanes ask
 // for.  An output may be its input: a row's stores need values of all the loads of its wave.
 #include <hip/hip_runtime.h>
@@ -70,8 +70,93 @@ __device__ __forceinline__ double angle(const HeadsJob& a, int i, int64_t m, dou
   return p * double(a.inv_freq[i]);
 }
 
+// The turn of a lane's channels c0 .. c0 + 7 for token m: y[e] = cs[e] x[e] + sn[e] partner[e];
+// the sign of the sine is the channel's.  A wave's lanes make the token's R / 2 cosines and
+// sines between them, one or two each, and take theirs from `lds` (the wave's own), where each
+// lane made its own eight before: 8 times the work for 128 channels, a third of the time of
+// 8192 tokens' keys into the cache.
+struct Turn {
+  double c, s;
+};
+constexpr int kMostPairs = BSF8_CACHE_MAX_HEAD_DIM / 2;
+template <int PAIRS>
+__device__ __forceinline__ void turn_factors(const HeadsJob& a, int c0, int64_t m, Turn* lds, double (&cs)[EPL], double (&sn)[EPL]) {
+  const int R = a.R, half = R >> 1;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) {
+    cs[e] = 1.0;
+    sn[e] = 0.0;
+  }
+  if (PAIRS == kNone) return;
+  const double p0 = a.n_axes == 1 ? position(a, 0, m) : 0.0;
+  for (int i = threadIdx.x & 63; i < half; i += 64) {
+    Turn t;
+    sine_cosine(angle(a, i, m, p0), t.s, t.c);
+    t.s *= a.scale;
+    t.c *= a.scale;
+    lds[i] = t;
+  }
+  // the wave's stores are before its loads: LDS takes a wave's instructions in order
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  if (c0 >= R) return;
+  if (PAIRS == kAdjacent) {
+#pragma unroll
+    for (int e = 0; e < EPL; e += 2) {
+      if (c0 + e >= R) continue;
+      const Turn t = lds[(c0 + e) >> 1];
+      cs[e] = cs[e + 1] = t.c;
+      sn[e + 1] = t.s;
+      sn[e] = -t.s;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const int ch = c0 + e;
+      if (PAIRS == kHalfOdd && ch >= R) continue;
+      const bool second = ch >= half;
+      const Turn t = lds[second ? ch - half : ch];
+      cs[e] = t.c;
+      sn[e] = second ? t.s : -t.s;
+    }
+  }
+}
+
+// A row of keys or values into the cache; the lanes of a row call it together.
+template <int LPR>
+__device__ __forceinline__ void store_cached(const CacheDev& c, bool is_v, uint32_t page, uint32_t row, int h, int c0, bool on,
+                                             const float (&f)[EPL]) {
+  uint8_t* out = (is_v ? c.v : c.k) + int64_t(page) * c.page + int64_t(row) * c.row + int64_t(h) * c.head;
+  if (!c.e4m3) {
+    store_row(out, true, c0, on ? EPL : 0, true, f);
+    return;
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(f[e]));
+#pragma unroll
+  for (int d = (LPR < LPG ? LPR : LPG) / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+  float s;
+  uint32_t packed[EPL / 4];
+  encode(f, amax, s, packed);
+  if (!on) return;
+  *reinterpret_cast<uint2*>(out + c0) = make_uint2(packed[0], packed[1]);
+  if (c0 % kBlock == 0)
+    (is_v ? c.v_scale : c.k_scale)[int64_t(page) * c.s_page + int64_t(row) * c.s_row + int64_t(h) * c.s_head +
+                                   int64_t(c0 / kBlock) * c.s_group] = s;
+}
+
+// the slot of token m, -1 where it has none
+__device__ __forceinline__ int64_t slot_of(const HeadsJob& a, int64_t m) {
+  if (!a.to_cache) return -1;
+  const int64_t s = a.slot64 ? static_cast<const int64_t*>(a.slots)[m] : int64_t(static_cast<const int32_t*>(a.slots)[m]);
+  return s < a.cache.rows ? max(s, int64_t(-1)) : -1;
+}
+
 template <int LPR, int PAIRS>
 __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
+  __shared__ Turn turn[kWaves][PAIRS == kNone ? 1 : kMostPairs];
   constexpr int RPP = 64 / LPR;                     // rows of a wave
   const int lane = threadIdx.x & 63;
   const uint32_t wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
@@ -83,46 +168,10 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
   const int on = c0 < D ? EPL : 0;                  // D is a multiple of a lane's channels
   const bool turns = PAIRS != kNone && c0 < R;
 
-  // y[e] = cs[e] x[e] + sn[e] partner[e]; the sign of the sine is the channel's
   double cs[EPL], sn[EPL];
-  if (PAIRS != kNone) {
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) {
-      cs[e] = 1.0;
-      sn[e] = 0.0;
-    }
-    if (turns) {
-      const double p0 = a.n_axes == 1 ? position(a, 0, m) : 0.0;
-      if (PAIRS == kAdjacent) {
-#pragma unroll
-        for (int e = 0; e < EPL; e += 2) {
-          if (c0 + e >= R) continue;
-          double s, c;
-          sine_cosine(angle(a, (c0 + e) >> 1, m, p0), s, c);
-          cs[e] = cs[e + 1] = c * a.scale;
-          sn[e + 1] = s * a.scale;
-          sn[e] = -sn[e + 1];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) {
-          const int ch = c0 + e;
-          if (PAIRS == kHalfOdd && ch >= R) continue;
-          const bool second = ch >= half;
-          double s, c;
-          sine_cosine(angle(a, second ? ch - half : ch, m, p0), s, c);
-          cs[e] = c * a.scale;
-          sn[e] = (second ? s : -s) * a.scale;
-        }
-      }
-    }
-  }
+  turn_factors<PAIRS>(a, c0, m, turn[threadIdx.x >> 6], cs, sn);
 
-  int64_t slot = -1;
-  if (a.to_cache) {
-    slot = a.slot64 ? static_cast<const int64_t*>(a.slots)[m] : int64_t(static_cast<const int32_t*>(a.slots)[m]);
-    if (slot >= a.cache.rows) slot = -1;
-  }
+  const int64_t slot = slot_of(a, m);
   const uint32_t page = slot >= 0 ? a.cache.page_of(uint32_t(slot)) : 0;
   const uint32_t row = slot >= 0 ? uint32_t(slot) - page * uint32_t(a.cache.page_size) : 0;
 
@@ -203,26 +252,103 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
       store_row(const_cast<void*>(dst.p), dst.bf16, m * dst.token + int64_t(h) * dst.head + c0, on, dst.vec, f);
       continue;
     }
-    if (skip) continue;
-    const CacheDev& c = a.cache;
-    uint8_t* out = (is_v ? c.v : c.k) + int64_t(page) * c.page + int64_t(row) * c.row + int64_t(h) * c.head;
-    if (!c.e4m3) {
-      store_row(out, true, c0, on, true, f);
-      continue;
+    if (!skip) store_cached<LPR>(a.cache, is_v, page, row, h, c0, on != 0, f);
+  }
+}
+
+// The same for inputs of one type whose rows, and the outputs', allow 16-byte accesses, and
+// pairs whose halves begin at a lane's first channel: the next rows are asked for before the
+// ones at hand are turned, and nothing branches around a load.
+template <int LPR, int PAIRS, bool XBF16, bool NORM>
+__global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
+  __shared__ Turn turn[kWaves][PAIRS == kNone ? 1 : kMostPairs];
+  constexpr int RPP = 64 / LPR;
+  const int lane = threadIdx.x & 63;
+  const uint32_t wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t tok = wave / uint32_t(a.parts), part = wave - tok * uint32_t(a.parts);
+  if (tok >= uint32_t(a.M)) return;
+  const int64_t m = a.m0 + tok;
+  const int D = a.D, R = a.R, half = R >> 1;
+  const int c0 = (lane & (LPR - 1)) * EPL, at0 = c0 < D ? c0 : 0;   // (lanes past the row read its first channels)
+  const bool on = c0 < D, turns = PAIRS != kNone && c0 < R;
+  const int pc = PAIRS == kHalf && turns ? (c0 < half ? c0 + half : c0 - half) : at0;
+
+  const int q_heads = a.q.heads, k_heads = a.k.heads, heads = q_heads + k_heads + a.v.heads;
+  const int first = int(part) * a.per_part, last = min(heads, first + a.per_part);
+  struct Fetched {
+    Raw<XBF16> x, p;
+  };
+  const auto fetch = [&](int at, Fetched& f) {
+    at = min(at, last - 1);
+    const bool is_q = at < q_heads, is_v = at >= q_heads + k_heads;
+    const void* p = is_q ? a.q.p : is_v ? a.v.p : a.k.p;
+    const int64_t base = is_q   ? m * a.q.token + int64_t(at) * a.q.head
+                         : is_v ? m * a.v.token + int64_t(at - q_heads - k_heads) * a.v.head
+                                : m * a.k.token + int64_t(at - q_heads) * a.k.head;
+    load_raw<XBF16>(p, base + at0, EPL, true, f.x);
+    if (PAIRS == kHalf) load_raw<XBF16>(p, base + pc, EPL, true, f.p);
+  };
+  Fetched next;
+  fetch(first + lane / LPR, next);
+  float wq[EPL], wk[EPL], wqp[EPL], wkp[EPL];
+  if (NORM) {
+    const void* any = a.qw ? a.qw : a.kw;
+    load_vec(a.qw ? a.qw : any, a.w_bf16, at0, EPL, a.w_vec, wq);
+    load_vec(a.kw ? a.kw : any, a.w_bf16, at0, EPL, a.w_vec, wk);
+    if (PAIRS == kHalf) {
+      load_vec(a.qw ? a.qw : any, a.w_bf16, pc, EPL, a.w_vec, wqp);
+      load_vec(a.kw ? a.kw : any, a.w_bf16, pc, EPL, a.w_vec, wkp);
     }
-    float amax = 0.0f;
+  }
+  const int64_t slot = slot_of(a, m);
+  const uint32_t page = slot >= 0 ? a.cache.page_of(uint32_t(slot)) : 0;
+  const uint32_t row = slot >= 0 ? uint32_t(slot) - page * uint32_t(a.cache.page_size) : 0;
+  double cs[EPL], sn[EPL];
+  turn_factors<PAIRS>(a, c0, m, turn[threadIdx.x >> 6], cs, sn);
+
+  for (int at = first + lane / LPR; at < last; at += RPP) {
+    const Fetched now = next;
+    fetch(at + RPP, next);
+    const bool is_q = at < q_heads, is_v = at >= q_heads + k_heads;
+    const int h = at - (is_q ? 0 : is_v ? q_heads + k_heads : q_heads);
+    float f[EPL];
+    if (is_v) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(f[e]));
+      for (int e = 0; e < EPL; ++e) f[e] = on ? value<XBF16>(now.x, e) : 0.f;
+    } else {
+      double v[EPL], vp[EPL];
 #pragma unroll
-    for (int d = (LPR < LPG ? LPR : LPG) / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-    float s;
-    uint32_t packed[EPL / 4];
-    encode(f, amax, s, packed);
-    if (on) {
-      *reinterpret_cast<uint2*>(out + c0) = make_uint2(packed[0], packed[1]);
-      if (c0 % kBlock == 0)
-        (is_v ? c.v_scale : c.k_scale)[int64_t(page) * c.s_page + int64_t(row) * c.s_row + int64_t(h) * c.s_head +
-                                       int64_t(c0 / kBlock) * c.s_group] = s;
+      for (int e = 0; e < EPL; ++e) {
+        v[e] = on ? double(value<XBF16>(now.x, e)) : 0.0;
+        vp[e] = PAIRS == kHalf ? double(value<XBF16>(now.p, e)) : 0.0;
+      }
+      if (NORM && (is_q ? a.qw : a.kw) != nullptr) {
+        double sum = 0.0;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) sum = fma(v[e], v[e], sum);
+#pragma unroll
+        for (int d = LPR / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+        const double rstd = 1.0 / sqrt(sum / double(D) + a.eps);
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) {
+          v[e] = v[e] * rstd * double(is_q ? wq[e] : wk[e]);
+          if (PAIRS == kHalf) vp[e] = vp[e] * rstd * double(is_q ? wqp[e] : wkp[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) {
+        double y = v[e];
+        if (PAIRS == kHalf && turns) y = fma(cs[e], v[e], sn[e] * vp[e]);
+        if (PAIRS == kAdjacent && c0 + e < R) y = fma(cs[e], v[e], sn[e] * v[e ^ 1]);
+        f[e] = to_f32(y);
+      }
+    }
+    if (is_q || !a.to_cache) {
+      const void* p = is_q ? a.q_out.p : a.k_out.p;
+      const int64_t off = is_q ? m * a.q_out.token + int64_t(h) * a.q_out.head : m * a.k_out.token + int64_t(h) * a.k_out.head;
+      store_row(const_cast<void*>(p), (is_q ? a.q_out.bf16 : a.k_out.bf16) != 0, off + c0, on ? EPL : 0, true, f);
+    } else if (slot >= 0) {
+      store_cached<LPR>(a.cache, is_v, page, row, h, c0, on, f);
     }
   }
 }
@@ -324,6 +450,24 @@ void launch_heads_pairs(const HeadsJob& a, int pairs, unsigned blocks, hipStream
   }
 }
 
+template <int LPR, int PAIRS>
+void launch_heads_wide(const HeadsJob& a, bool x_bf16, unsigned blocks, hipStream_t stream) {
+  const bool norm = a.qw || a.kw;
+  const dim3 grid(blocks), block(kThreads);
+  if (x_bf16 && norm) hipLaunchKernelGGL((heads_wide_kernel<LPR, PAIRS, true, true>), grid, block, 0, stream, a);
+  else if (x_bf16) hipLaunchKernelGGL((heads_wide_kernel<LPR, PAIRS, true, false>), grid, block, 0, stream, a);
+  else if (norm) hipLaunchKernelGGL((heads_wide_kernel<LPR, PAIRS, false, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((heads_wide_kernel<LPR, PAIRS, false, false>), grid, block, 0, stream, a);
+}
+template <int LPR>
+void launch_heads_any(const HeadsJob& a, int pairs, bool wide, unsigned blocks, hipStream_t stream) {
+  const bool x_bf16 = (a.q.heads ? a.q : a.k).bf16 != 0;
+  if (!wide) launch_heads_pairs<LPR>(a, pairs, blocks, stream);
+  else if (pairs == kNone) launch_heads_wide<LPR, kNone>(a, x_bf16, blocks, stream);
+  else if (pairs == kHalf) launch_heads_wide<LPR, kHalf>(a, x_bf16, blocks, stream);
+  else launch_heads_wide<LPR, kAdjacent>(a, x_bf16, blocks, stream);
+}
+
 }  // namespace
 
 bsf8_status launch_heads(HeadsJob a, int64_t M, hipStream_t stream) {
@@ -331,6 +475,9 @@ bsf8_status launch_heads(HeadsJob a, int64_t M, hipStream_t stream) {
   if (heads == 0) return BSF8_OK;
   const int lpr = a.D <= 64 ? 8 : a.D <= 128 ? 16 : 32, rows = 64 / lpr;
   const int pairs = a.R == 0 ? kNone : !a.half ? kAdjacent : (a.R / 2) % EPL == 0 ? kHalf : kHalfOdd;
+  bool wide = pairs != kHalfOdd;
+  for (const HeadsDev* h : {&a.q, &a.q_out, &a.k, &a.k_out, &a.v})
+    if (h->heads) wide = wide && h->vec && (h == &a.q_out || h == &a.k_out || h->bf16 == (a.q.heads ? a.q : a.k).bf16);
   const int64_t passes = (heads + rows - 1) / rows;
   int64_t per = M * passes / kEnoughWaves;
   per = per < 1 ? 1 : per > passes ? passes : per;
@@ -341,9 +488,9 @@ bsf8_status launch_heads(HeadsJob a, int64_t M, hipStream_t stream) {
     a.m0 = m0;
     a.M = int32_t(M - m0 < tokens ? M - m0 : tokens);
     const unsigned blocks = unsigned((int64_t(a.M) * a.parts + kWaves - 1) / kWaves);
-    if (lpr == 8) launch_heads_pairs<8>(a, pairs, blocks, stream);
-    else if (lpr == 16) launch_heads_pairs<16>(a, pairs, blocks, stream);
-    else launch_heads_pairs<32>(a, pairs, blocks, stream);
+    if (lpr == 8) launch_heads_any<8>(a, pairs, wide, blocks, stream);
+    else if (lpr == 16) launch_heads_any<16>(a, pairs, wide, blocks, stream);
+    else launch_heads_any<32>(a, pairs, wide, blocks, stream);
     const bsf8_status st = device_status(hipGetLastError(), "rope / cache_write launch");
     if (st != BSF8_OK) return st;
   }
