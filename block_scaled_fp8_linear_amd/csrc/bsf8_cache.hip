@@ -123,13 +123,48 @@ __device__ __forceinline__ void turn_factors(const HeadsJob& a, int c0, int64_t 
   }
 }
 
+// Eight channels at an address that a lane has picked among several: named as global memory,
+// since the compiler takes a pointer that it cannot trace for one that may be LDS (flat accesses
+// took 1.7 times as long).
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(1))) u4v* GlobalVec;
+template <bool BF16>
+__device__ __forceinline__ void load_global(uint64_t at, Raw<BF16>& r) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const u4v u = reinterpret_cast<GlobalVec>(at)[i];
+#pragma unroll
+    for (int y = 0; y < 4; ++y) r.w[4 * i + y] = u[y];
+  }
+}
+__device__ __forceinline__ void store_global(uint64_t row, bool bf16, int c0, const float (&f)[EPL]) {
+  GlobalVec p = reinterpret_cast<GlobalVec>(row + uint64_t(c0 * (bf16 ? 2 : 4)));
+  if (bf16) {
+    p[0] = u4v{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
+  } else {
+    p[0] = u4v{__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+    p[1] = u4v{__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])};
+  }
+}
+
 // A row of keys or values into the cache; the lanes of a row call it together.
+struct CacheRow {   // of a token: addresses of its keys, values and their scales
+  uint64_t k, v, ks, vs;
+};
+__device__ __forceinline__ CacheRow cache_row(const CacheDev& c, int64_t slot) {
+  if (slot < 0) return CacheRow{0, 0, 0, 0};
+  const uint32_t page = c.page_of(uint32_t(slot)), row = uint32_t(slot) - page * uint32_t(c.page_size);
+  const uint64_t at = uint64_t(int64_t(page) * c.page + int64_t(row) * c.row), s = uint64_t(int64_t(page) * c.s_page + int64_t(row) * c.s_row) * 4;
+  return CacheRow{uint64_t(c.k) + at, uint64_t(c.v) + at, uint64_t(c.k_scale) + s, uint64_t(c.v_scale) + s};
+}
 template <int LPR>
-__device__ __forceinline__ void store_cached(const CacheDev& c, bool is_v, uint32_t page, uint32_t row, int h, int c0, bool on,
+__device__ __forceinline__ void store_cached(const CacheDev& c, const CacheRow& to, bool is_v, int h, int c0, bool on,
                                              const float (&f)[EPL]) {
-  uint8_t* out = (is_v ? c.v : c.k) + int64_t(page) * c.page + int64_t(row) * c.row + int64_t(h) * c.head;
+  uint64_t out = to.k, scale = to.ks;
+  if (is_v) out = to.v, scale = to.vs;
+  out += uint64_t(int64_t(h) * c.head);
   if (!c.e4m3) {
-    store_row(out, true, c0, on ? EPL : 0, true, f);
+    if (on) store_global(out, true, c0, f);
     return;
   }
   float amax = 0.0f;
@@ -141,10 +176,10 @@ __device__ __forceinline__ void store_cached(const CacheDev& c, bool is_v, uint3
   uint32_t packed[EPL / 4];
   encode(f, amax, s, packed);
   if (!on) return;
-  *reinterpret_cast<uint2*>(out + c0) = make_uint2(packed[0], packed[1]);
+  typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<__attribute__((address_space(1))) u2v*>(out + uint64_t(c0)) = u2v{packed[0], packed[1]};
   if (c0 % kBlock == 0)
-    (is_v ? c.v_scale : c.k_scale)[int64_t(page) * c.s_page + int64_t(row) * c.s_row + int64_t(h) * c.s_head +
-                                   int64_t(c0 / kBlock) * c.s_group] = s;
+    reinterpret_cast<__attribute__((address_space(1))) float*>(scale)[int64_t(h) * c.s_head + int64_t(c0 / kBlock) * c.s_group] = s;
 }
 
 // the slot of token m, -1 where it has none
@@ -159,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
   __shared__ Turn turn[kWaves][PAIRS == kNone ? 1 : kMostPairs];
   constexpr int RPP = 64 / LPR;                     // rows of a wave
   const int lane = threadIdx.x & 63;
-  const uint32_t wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t wave = blockIdx.x * kWaves + uint32_t(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
   const uint32_t tok = wave / uint32_t(a.parts), part = wave - tok * uint32_t(a.parts);
   if (tok >= uint32_t(a.M)) return;                 // whole waves; nothing here waits for another
   const int64_t m = a.m0 + tok;
@@ -172,8 +207,7 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
   turn_factors<PAIRS>(a, c0, m, turn[threadIdx.x >> 6], cs, sn);
 
   const int64_t slot = slot_of(a, m);
-  const uint32_t page = slot >= 0 ? a.cache.page_of(uint32_t(slot)) : 0;
-  const uint32_t row = slot >= 0 ? uint32_t(slot) - page * uint32_t(a.cache.page_size) : 0;
+  const CacheRow to = cache_row(a.cache, slot);
 
   const int heads = a.q.heads + a.k.heads + a.v.heads;
   const int first = int(part) * a.per_part, last = min(heads, first + a.per_part);
@@ -252,8 +286,21 @@ __global__ __launch_bounds__(kThreads) void heads_kernel(HeadsJob a) {
       store_row(const_cast<void*>(dst.p), dst.bf16, m * dst.token + int64_t(h) * dst.head + c0, on, dst.vec, f);
       continue;
     }
-    if (!skip) store_cached<LPR>(a.cache, is_v, page, row, h, c0, on != 0, f);
+    if (!skip) store_cached<LPR>(a.cache, to, is_v, h, c0, on != 0, f);
   }
+}
+
+// The rows of a token in one numbering: queries, keys, values.
+struct Kinds {
+  int keys, values;   // the first key's and the first value's number
+  __device__ __forceinline__ bool is_q(int at) const { return at < keys; }
+  __device__ __forceinline__ bool is_v(int at) const { return at >= values; }
+  __device__ __forceinline__ int head(int at) const { return at - (at < keys ? 0 : at < values ? keys : values); }
+};
+// The one of three values that a row's kind asks for.  By value, and not as a choice between
+// variables: of those the compiler makes a choice between their addresses, and puts them in memory.
+__device__ __forceinline__ uint64_t pick(Kinds kinds, int at, uint64_t q, uint64_t k, uint64_t v) {
+  return at < kinds.keys ? q : at < kinds.values ? k : v;
 }
 
 // The same for inputs of one type whose rows, and the outputs', allow 16-byte accesses, and
@@ -264,7 +311,7 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
   __shared__ Turn turn[kWaves][PAIRS == kNone ? 1 : kMostPairs];
   constexpr int RPP = 64 / LPR;
   const int lane = threadIdx.x & 63;
-  const uint32_t wave = blockIdx.x * kWaves + (threadIdx.x >> 6);
+  const uint32_t wave = blockIdx.x * kWaves + uint32_t(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6));
   const uint32_t tok = wave / uint32_t(a.parts), part = wave - tok * uint32_t(a.parts);
   if (tok >= uint32_t(a.M)) return;
   const int64_t m = a.m0 + tok;
@@ -275,21 +322,20 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
 
   const int q_heads = a.q.heads, k_heads = a.k.heads, heads = q_heads + k_heads + a.v.heads;
   const int first = int(part) * a.per_part, last = min(heads, first + a.per_part);
-  struct Fetched {
-    Raw<XBF16> x, p;
-  };
-  const auto fetch = [&](int at, Fetched& f) {
+  // a lane's rows are of three kinds: it picks the token's address and the heads' distance
+  constexpr int XB = XBF16 ? 2 : 4;
+  const auto token_of = [&](const HeadsDev& h, int64_t bytes) { return uint64_t(h.p) + uint64_t(m * h.token * bytes); };
+  const uint64_t q_at = token_of(a.q, XB), k_at = token_of(a.k, XB), v_at = token_of(a.v, XB);
+  const int64_t q_step = a.q.head * XB, k_step = a.k.head * XB, v_step = a.v.head * XB;
+  const Kinds kinds{q_heads, q_heads + k_heads};
+  Raw<XBF16> next_x, next_p;
+  const auto fetch = [=](int at, Raw<XBF16>& x, Raw<XBF16>& p) __attribute__((always_inline)) {
     at = min(at, last - 1);
-    const bool is_q = at < q_heads, is_v = at >= q_heads + k_heads;
-    const void* p = is_q ? a.q.p : is_v ? a.v.p : a.k.p;
-    const int64_t base = is_q   ? m * a.q.token + int64_t(at) * a.q.head
-                         : is_v ? m * a.v.token + int64_t(at - q_heads - k_heads) * a.v.head
-                                : m * a.k.token + int64_t(at - q_heads) * a.k.head;
-    load_raw<XBF16>(p, base + at0, EPL, true, f.x);
-    if (PAIRS == kHalf) load_raw<XBF16>(p, base + pc, EPL, true, f.p);
+    const uint64_t row = pick(kinds, at, q_at, k_at, v_at) + uint64_t(int64_t(kinds.head(at)) * int64_t(pick(kinds, at, uint64_t(q_step), uint64_t(k_step), uint64_t(v_step))));
+    load_global(row + uint64_t(at0 * XB), x);
+    if (PAIRS == kHalf) load_global(row + uint64_t(pc * XB), p);
   };
-  Fetched next;
-  fetch(first + lane / LPR, next);
+  fetch(first + lane / LPR, next_x, next_p);
   float wq[EPL], wk[EPL], wqp[EPL], wkp[EPL];
   if (NORM) {
     const void* any = a.qw ? a.qw : a.kw;
@@ -301,26 +347,28 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
     }
   }
   const int64_t slot = slot_of(a, m);
-  const uint32_t page = slot >= 0 ? a.cache.page_of(uint32_t(slot)) : 0;
-  const uint32_t row = slot >= 0 ? uint32_t(slot) - page * uint32_t(a.cache.page_size) : 0;
+  const CacheRow to = cache_row(a.cache, slot);
+  const uint64_t qo_at = token_of(a.q_out, a.q_out.bf16 ? 2 : 4), ko_at = token_of(a.k_out, a.k_out.bf16 ? 2 : 4);
+  const int64_t qo_step = a.q_out.head * (a.q_out.bf16 ? 2 : 4), ko_step = a.k_out.head * (a.k_out.bf16 ? 2 : 4);
+  const uint64_t qo_bf16 = a.q_out.bf16, ko_bf16 = a.k_out.bf16;
   double cs[EPL], sn[EPL];
   turn_factors<PAIRS>(a, c0, m, turn[threadIdx.x >> 6], cs, sn);
 
   for (int at = first + lane / LPR; at < last; at += RPP) {
-    const Fetched now = next;
-    fetch(at + RPP, next);
-    const bool is_q = at < q_heads, is_v = at >= q_heads + k_heads;
-    const int h = at - (is_q ? 0 : is_v ? q_heads + k_heads : q_heads);
+    const Raw<XBF16> x = next_x, p = next_p;
+    fetch(at + RPP, next_x, next_p);
+    const bool is_q = kinds.is_q(at), is_v = kinds.is_v(at);
+    const int h = kinds.head(at);
     float f[EPL];
     if (is_v) {
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) f[e] = on ? value<XBF16>(now.x, e) : 0.f;
+      for (int e = 0; e < EPL; ++e) f[e] = on ? value<XBF16>(x, e) : 0.f;
     } else {
       double v[EPL], vp[EPL];
 #pragma unroll
       for (int e = 0; e < EPL; ++e) {
-        v[e] = on ? double(value<XBF16>(now.x, e)) : 0.0;
-        vp[e] = PAIRS == kHalf ? double(value<XBF16>(now.p, e)) : 0.0;
+        v[e] = on ? double(value<XBF16>(x, e)) : 0.0;
+        vp[e] = PAIRS == kHalf ? double(value<XBF16>(p, e)) : 0.0;
       }
       if (NORM && (is_q ? a.qw : a.kw) != nullptr) {
         double sum = 0.0;
@@ -328,7 +376,7 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
         for (int e = 0; e < EPL; ++e) sum = fma(v[e], v[e], sum);
 #pragma unroll
         for (int d = LPR / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-        const double rstd = 1.0 / sqrt(sum / double(D) + a.eps);
+        const double rstd = rsqrt64(fma(sum, 1.0 / double(D), a.eps));
 #pragma unroll
         for (int e = 0; e < EPL; ++e) {
           v[e] = v[e] * rstd * double(is_q ? wq[e] : wk[e]);
@@ -344,11 +392,11 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
       }
     }
     if (is_q || !a.to_cache) {
-      const void* p = is_q ? a.q_out.p : a.k_out.p;
-      const int64_t off = is_q ? m * a.q_out.token + int64_t(h) * a.q_out.head : m * a.k_out.token + int64_t(h) * a.k_out.head;
-      store_row(const_cast<void*>(p), (is_q ? a.q_out.bf16 : a.k_out.bf16) != 0, off + c0, on ? EPL : 0, true, f);
+      const uint64_t to_row = pick(kinds, at, qo_at, ko_at, ko_at) +
+                              uint64_t(int64_t(h) * int64_t(pick(kinds, at, uint64_t(qo_step), uint64_t(ko_step), uint64_t(ko_step))));
+      if (on) store_global(to_row, pick(kinds, at, qo_bf16, ko_bf16, ko_bf16) != 0, c0, f);
     } else if (slot >= 0) {
-      store_cached<LPR>(a.cache, is_v, page, row, h, c0, on, f);
+      store_cached<LPR>(a.cache, to, is_v, h, c0, on, f);
     }
   }
 }
@@ -436,8 +484,10 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadJob a) {
   }
 }
 
-// waves that fill the device a few times over; more rows per wave only behind that
-constexpr int64_t kEnoughWaves = 8192;
+// Waves that fill the device: a token is split over more of them only up to here, since each makes
+// the token's sines and cosines again (1024 tokens of 48 heads with norms: 4096 waves 15.7 us, 8192
+// 20.7; 4096 tokens with their cache rows 27, 29 and, at 16384, 36).  Rows read back share nothing.
+constexpr int64_t kEnoughWaves = 4096, kReadWaves = 8192;
 constexpr int64_t kMostWaves = int64_t(1) << 25;    // of one launch (2^31 threads)
 
 template <int LPR>
@@ -511,7 +561,7 @@ bsf8_status launch_cache_read(const CacheDev& cache, int64_t B, const int32_t* t
   a.B = int32_t(B);
   a.pages = int32_t(pages);
   a.R = int32_t(R);
-  const int64_t per = R / kEnoughWaves;
+  const int64_t per = R / kReadWaves;
   a.per_wave = int32_t(per < 1 ? 1 : per > 16 ? 16 : per);
   for (int64_t r0 = 0; r0 < R; r0 += kMostWaves * a.per_wave) {
     a.r0 = r0;

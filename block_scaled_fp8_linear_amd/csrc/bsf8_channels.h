@@ -147,4 +147,12 @@ __device__ __forceinline__ void encode(const float (&n)[EPL], float amax, float&
   }
 }
 
+// 1 / sqrt(x) to within an F64 rounding or two: the hardware's estimate and two Newton steps
+__device__ __forceinline__ double rsqrt64(double x) {
+  double y = __builtin_amdgcn_rsq(x);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y = fma(0.5 * y, fma(-x * y, y, 1.0), y);
+  return y;
+}
+
 }  // namespace bsf8

@@ -281,14 +281,6 @@ __device__ __forceinline__ double block_sum(double s, double (*lds)[16], int& tu
   return lane_value(s, 15);
 }
 
-// 1 / sqrt(x) to within an F64 rounding or two: the hardware's estimate and two Newton steps
-__device__ __forceinline__ double rsqrt64(double x) {
-  double y = __builtin_amdgcn_rsq(x);
-#pragma unroll
-  for (int i = 0; i < 2; ++i) y = fma(0.5 * y, fma(-x * y, y, 1.0), y);
-  return y;
-}
-
 // norm(v) as (v - mean) * rstd, or v * rstd in the RMS norm; `on`: the last
 // vector lies in the row.  The difference is taken before the scaling: in v *
 // rstd - mean * rstd the rounding of mean * rstd is left where v is near the
