@@ -142,3 +142,79 @@ def test_rope_axes():
             B.rope_axes(bad)
     with pytest.raises(ValueError):
         B.rope_axes([0, 4], interleaved=True)
+
+
+def _attention(cache=None, ws=FAKE, wsb=1 << 40, **kw):
+    a = B.AttentionArgs()
+    a.B, a.table, a.ld_table, a.pages, a.lens, a.scale = 3, FAKE, 100, 100, FAKE, 0.1
+    a.q = a.out = B.Heads(FAKE, B.DT_BF16, 8, 8 * 192, 192)
+    for key, val in kw.items():
+        setattr(a, key, val)
+    c = make_cache() if cache is None else cache
+    return name(B.lib().bsf8_paged_attention(ctypes.byref(c), ctypes.byref(a), ws, wsb, None))
+
+
+def test_attention_refusals():
+    L = B.lib()
+    wide = dict(token=8 * 192, head=192, heads=8)
+    assert _attention(B=0) == "OK" and _attention(B=0, lens=None, table=None) == "OK"
+    assert name(L.bsf8_paged_attention(ctypes.byref(make_cache()), None, None, 0, None)) == "INVALID_ARG"
+    assert name(L.bsf8_paged_attention(None, ctypes.byref(B.AttentionArgs()), None, 0, None)) == "INVALID_ARG"
+    for bad in (dict(cache=make_cache(heads=0)), dict(B=-1), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(q=H(heads=6, token=8 * 192, head=192)), dict(q=H(heads=0, token=8 * 192, head=192)), dict(q=H(None, **wide)),
+                dict(out=H(heads=4, token=8 * 192, head=192)), dict(out=H(None, **wide)), dict(q=H(dtype=B.DT_F16, **wide)),
+                dict(out=H(dtype=B.DT_F8_E4M3, **wide)), dict(out=H(heads=8, token=8 * 192 - 1, head=192)), dict(table=None),
+                dict(lens=None), dict(pages=0), dict(ld_table=99)):
+        assert _attention(**bad) == "INVALID_ARG", bad
+    for bad in (dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(lse=FAKE + 2), dict(q=H(FAKE + 1, **wide)), dict(out=H(FAKE + 1, **wide)),
+                dict(ws=FAKE + 128)):
+        assert _attention(**bad) == "ALIGNMENT", bad
+    for bad in (dict(B=1 << 31), dict(B=1 << 22, ld_table=1 << 30), dict(pages=1 << 27, ld_table=1 << 27), dict(B=1 << 20, pages=1 << 20, ld_table=1 << 20)):
+        assert _attention(**bad) == "UNSUPPORTED", bad
+    need = ctypes.c_size_t()
+    assert L.bsf8_attention_workspace_size(ctypes.byref(make_cache()), 3, 8, 100, ctypes.byref(need)) == 0 and need.value > 0
+    assert _attention(ws=None) == "WORKSPACE" and _attention(wsb=need.value - 1) == "WORKSPACE"
+    for bad in (dict(q=6), dict(q=0), dict(B=-1), dict(pages=0)):
+        kw = dict(dict(B=3, q=8, pages=100), **bad)
+        assert name(L.bsf8_attention_workspace_size(ctypes.byref(make_cache()), kw["B"], kw["q"], kw["pages"], ctypes.byref(need))) == "INVALID_ARG"
+        assert need.value == 0
+    assert name(L.bsf8_attention_workspace_size(ctypes.byref(make_cache()), 3, 8, 100, None)) == "INVALID_ARG"
+    assert L.bsf8_attention_workspace_size(ctypes.byref(make_cache()), 3, 8, 2, ctypes.byref(need)) == 0 and need.value == 0
+    assert L.bsf8_attention_workspace_size(ctypes.byref(make_cache()), 0, 8, 100, ctypes.byref(need)) == 0 and need.value == 0
+
+
+def test_workspace_covers_every_type_of_query():
+    """The workspace is asked for without the query's type; whatever it is, a call that joins finds room (the call checks
+    the same number)."""
+    L, need = B.lib(), ctypes.c_size_t()
+    for D in (64, 128, 144, 256):
+        for b in (1, 3, 40, 700):
+            for pages in (1, 9, 33, 70, 400, 5000):
+                c = make_cache(head_dim=D, row=D, head=16 * D, page=64 * D)
+                assert L.bsf8_attention_workspace_size(ctypes.byref(c), b, 8, pages, ctypes.byref(need)) == 0
+                assert need.value <= 64 << 20
+
+
+@pytest.mark.parametrize("current,owner", [(0, 1), (1, 0), (1, 1)])
+def test_workspace_is_asked_on_the_caches_device(monkeypatch, current, owner):
+    import types
+
+    import torch
+    state, seen = [current], []
+
+    class Guard:
+        def __init__(self, idx):
+            self.idx = idx
+
+        def __enter__(self):
+            self.old, state[0] = state[0], self.idx
+
+        def __exit__(self, *exc):
+            state[0] = self.old
+
+    monkeypatch.setattr(torch.cuda, "device", Guard)
+    monkeypatch.setattr(B, "_CURRENT", (lambda: state[0], lambda idx: 0))
+    monkeypatch.setattr(B, "lib", lambda: types.SimpleNamespace(bsf8_attention_workspace_size=lambda *a: seen.append(state[0]) or 0))
+    cache = types.SimpleNamespace(_idx=owner, _ref=None)
+    assert B.attention_workspace_size(cache, 3, 8, 100) == 0
+    assert seen == [owner] and state == [current]
