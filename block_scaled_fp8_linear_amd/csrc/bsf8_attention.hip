@@ -495,19 +495,24 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
       float s[8];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        f4 acc[NG];
+        f4 acc[NG], small[NG];   // (an F32 query's lower terms by themselves: a third of the roundings of the sum)
 #pragma unroll
-        for (int c = 0; c < NG; ++c) acc[c] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int c = 0; c < NG; ++c) acc[c] = small[c] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int p = 0; p < KV; ++p) {
           constexpr int PARTS = E4M3 ? 2 : 1;
 #pragma unroll
           for (int y = 0; y < PARTS; ++y) {
             const v8bf kf = E4M3 ? decode8(kr[x][p][2 * y], kr[x][p][2 * y + 1]) : as_bf16(kr[x][p]);
-            f4& to = acc[E4M3 ? p / 2 : 0];
+            const int c = E4M3 ? p / 2 : 0;
+            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[p * PARTS + y][0], acc[c], 0, 0, 0);
 #pragma unroll
-            for (int q = 0; q < QT; ++q) to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[p * PARTS + y][q], to, 0, 0, 0);
+            for (int q = 1; q < QT; ++q) small[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[p * PARTS + y][q], small[c], 0, 0, 0);
           }
+        }
+        if (QT > 1) {
+#pragma unroll
+          for (int c = 0; c < NG; ++c) acc[c] += small[c];
         }
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
