@@ -198,10 +198,10 @@ __device__ __forceinline__ void split(const float (&x)[8], v8bf (&t)[N]) {
 
 // What an instance is made for.
 // DIM: channels that its pieces cover (64, 128, 256).  FULL: a head has exactly DIM of them, so
-// that offsets are constants and rows are whole cache lines.  Values are then read
-// non-temporally, a line by one instruction and once (64 sequences to 8192 of 128 BF16 channels
-// 147 -> 135 us, of E4M3 91 -> 86); a key's line is asked for by two instructions, half each, and
-// is left to the cache (with non-temporal keys one sequence of 131072 takes 33 us, without 31).
+// that offsets are constants and rows are whole cache lines, which are read non-temporally: each
+// once (64 sequences to 8192 of 128 BF16 channels 147 -> 134 us, of E4M3 91 -> 84; rows that
+// share lines lose by it, 80 channels 185 -> 218.  Keys left to the cache, the values alone
+// non-temporal: one sequence of 131072 33 -> 31 us, the batch 84 -> 88).
 // QT: BF16 terms of a query (1: BF16 queries, 3: F32).  PT: of a softmax weight.  A weight in one
 // term would be off by 2^-9 of itself, as much as the rounding of a BF16 output; two leave 2^-17,
 // three 2^-25.
@@ -216,7 +216,15 @@ struct Config {
   static constexpr bool E4M3 = E4M3_, FULL = FULL_, PAGES16 = PAGES_ != kAny;
   static constexpr int DIM = DIM_, QT = QT_, PT = PT_, PAGES = PAGES_;
   static constexpr int NG = DIM > 128 ? 2 : 1;         // 128-channel groups
-  static constexpr int KV = E4M3 ? DIM / 64 : DIM / 32;   // 16-byte key loads per token and lane
+  // HP 2: a row of the keys' operand is half a line of a token, 64 bytes, so that one load of the
+  // wave covers eight tokens' whole lines where it would touch half of sixteen and every line be
+  // asked for twice; the matrix instructions double.  (64 sequences to 8192 of 128 E4M3 channels
+  // 86.3 -> 84.3 us, 32 of 256 BF16 ones 96 -> 92, one of 32768 36 -> 34.5.  Not where rows are
+  // 64 bytes, nor where the instructions tell: 256 E4M3 channels 53 -> 57, F32 queries 62 -> 65.)
+  static constexpr int HP = QT > 1 || (E4M3 && DIM != 128) ? 1 : 2;
+  static constexpr int LN = DIM * (E4M3 ? 1 : 2) / (64 * HP);   // 16-byte loads per lane and row of the operand
+  static constexpr int X = 2 * HP;                     // operands of 32 tokens
+  static constexpr int PER = 4 / HP;                   // tokens of a lane's logits in one of them
   static constexpr int QS = DIM / 32;                  // query pieces: 32 channels each
   static constexpr int CHANNELS = NG * 128;
   static constexpr int PITCH = CHANNELS + 4;           // floats of a row in LDS
@@ -289,7 +297,7 @@ struct Queries {
 template <class C>
 __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(C::DIM, C::QT > 1)) void attention_kernel(AttentionDev a) {
   constexpr bool E4M3 = C::E4M3, PAGES16 = C::PAGES16;
-  constexpr int NG = C::NG, KV = C::KV, QT = C::QT, PT = C::PT, QS = C::QS;
+  constexpr int NG = C::NG, QT = C::QT, PT = C::PT, QS = C::QS, HP = C::HP, LN = C::LN, X = C::X, PER = C::PER;
   constexpr int PITCH = C::PITCH;
   // a wave's part of a result: its sums (kRows x PITCH), and for all waves maxima and sums of weights
   extern __shared__ __attribute__((aligned(16))) float lds_o[];
@@ -332,15 +340,16 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
   }
   int h = item / a.row_tiles, row0 = (item - h * a.row_tiles) * kRows;
 
-  // byte offsets of a lane's pieces within a row, with its token's (the key's i16, the first
-  // value's 4 g); channels past head_dim are read as others that exist (queries are zero there,
-  // and outputs are not stored)
-  const auto key_channel = [&](int s) {
-    return C::FULL ? (E4M3 ? s * 64 + g * 16 : s * 32 + g * 8) : E4M3 ? min(s * 64 + g * 16, D - 16) : min(s * 32 + g * 8, D - 8);
+  // byte offsets of a lane's pieces within a row, with its token's among the operand's; channels
+  // past head_dim are read as others that exist (queries are zero there, and outputs are not stored)
+  const uint32_t k_row = PAGES16 ? uint32_t(i16 / HP) * uint32_t(a.c.row) : 0, v_row = PAGES16 ? uint32_t(PER * g) * uint32_t(a.c.row) : 0;
+  const auto key_offset = [&](int ln) {
+    const int at = ln * 64 * HP + (i16 % HP) * 64 + g * 16;
+    return k_row + uint32_t(C::FULL ? at : min(at, (D - (E4M3 ? 16 : 8)) * (E4M3 ? 1 : 2)));
   };
-  const uint32_t k_row = PAGES16 ? uint32_t(i16) * uint32_t(a.c.row) : 0, v_row = PAGES16 ? uint32_t(4 * g) * uint32_t(a.c.row) : 0;
-  const auto key_offset = [&](int s) { return k_row + uint32_t(key_channel(s)) * (E4M3 ? 1 : 2); };
   const auto value_offset = [&](int c) { return v_row + uint32_t(min(c * 128 + i16 * 8, D - 8)) * (E4M3 ? 1 : 2); };
+  // the lane's eight tokens of the 32: PER of each operand; the rest of their numbers is PER * g
+  const auto token = [](int e) constexpr { return e / PER * (16 / HP) + e % PER; };
 
   for (int t = t_begin; t < t_end;) {
     // the item's tiles j .. j_end - 1 are this block's
@@ -412,35 +421,38 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
       return w.at[0] + int64_t(__shfl(w.le, tok, 64)) * a.c.page + int64_t(__shfl(w.lr, tok, 64)) * a.c.row;
     };
 
-    u4 kr[2][KV];
-    float ksc[NG][2][4], vsc[NG][2][4];
+    u4 kr[X][LN];
+    float ksc[NG][8], vsc[NG][8];
     const auto load_keys = [&](const Where& w) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const uint8_t* p = a.c.k + (PAGES16 ? w.at[x] : lane_at(w, 16 * x + i16));
+      for (int x = 0; x < X; ++x) {
+        const uint8_t* p = a.c.k + (PAGES16 ? w.at[x / HP] + uint64_t(uint32_t(x % HP * 8)) * uint32_t(a.c.row)
+                                            : lane_at(w, x * (16 / HP) + i16 / HP));
 #pragma unroll
-        for (int s = 0; s < KV; ++s) kr[x][s] = fetch<C::FULL, u4>(p + key_offset(s));
+        for (int ln = 0; ln < LN; ++ln) kr[x][ln] = fetch<C::FULL, u4>(p + key_offset(ln));
       }
     };
     // scales of a lane's eight tokens
-    const auto load_scales = [&](const Where& w, const float* of, float (&sc)[NG][2][4]) {
+    const auto load_scales = [&](const Where& w, const float* of, float (&sc)[NG][8]) {
 #pragma unroll
       for (int c = 0; c < NG; ++c)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < X; ++x) {
           const float* p = of + int64_t(c) * a.c.s_group;
           if (C::PAGES == kHalvesWide) {
-            const f4 v = *reinterpret_cast<const f4*>(p + w.s_at[x] + 4 * g);
+            typedef float fper __attribute__((ext_vector_type(PER)));
+            const fper v = *reinterpret_cast<const fper*>(p + w.s_at[x / HP] + x % HP * 8 + PER * g);
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[c][x][r] = v[r];
+            for (int r = 0; r < PER; ++r) sc[c][x * PER + r] = v[r];
           } else if (PAGES16) {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) sc[c][x][r] = (p + w.s_at[x])[uint32_t(4 * g + r) * uint32_t(a.c.s_row)];
+            for (int r = 0; r < PER; ++r)
+              sc[c][x * PER + r] = (p + w.s_at[x / HP])[uint32_t(x % HP * 8 + PER * g + r) * uint32_t(a.c.s_row)];
           } else {
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const int tok = 16 * x + 4 * g + r;
-              sc[c][x][r] = p[w.s_at[0] + int64_t(__shfl(w.le, tok, 64)) * a.c.s_page + int64_t(__shfl(w.lr, tok, 64)) * a.c.s_row];
+            for (int r = 0; r < PER; ++r) {
+              const int tok = token(x * PER + r) + PER * g;
+              sc[c][x * PER + r] = p[w.s_at[0] + int64_t(__shfl(w.le, tok, 64)) * a.c.s_page + int64_t(__shfl(w.lr, tok, 64)) * a.c.s_row];
             }
           }
         }
@@ -451,8 +463,8 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
     const auto load_values = [&](const Where& w) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const uint8_t* p = a.c.v + (PAGES16 ? w.at[e >> 2] + uint64_t(uint32_t(e & 3)) * uint32_t(a.c.row)
-                                            : lane_at(w, (e >> 2) * 16 + 4 * g + (e & 3)));
+        const uint8_t* p = a.c.v + (PAGES16 ? w.at[token(e) / 16] + uint64_t(uint32_t(token(e) % 16)) * uint32_t(a.c.row)
+                                            : lane_at(w, token(e) + PER * g));
 #pragma unroll
         for (int c = 0; c < NG; ++c) vr[c][e] = fetch<C::FULL, vw>(p + value_offset(c));
       }
@@ -491,37 +503,48 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
         ahead = entries(pos + 2 * tile_tokens);
       }
 
-      // ---- logits of 8 tokens and one head per lane
+      // ---- logits of 8 tokens and one head per lane.  Each operand meets the queries of either half;
+      // of the rows that are tokens' first halves the one sum counts, of the second ones the other
       float s[8];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        f4 acc[NG], small[NG];   // (an F32 query's lower terms by themselves: a third of the roundings of the sum)
+      for (int x = 0; x < X; ++x) {
+        f4 acc[HP][NG], small[HP][NG];   // (an F32 query's lower terms by themselves: a third of the roundings of the sum)
 #pragma unroll
-        for (int c = 0; c < NG; ++c) acc[c] = small[c] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int hh = 0; hh < HP; ++hh)
 #pragma unroll
-        for (int p = 0; p < KV; ++p) {
+          for (int c = 0; c < NG; ++c) acc[hh][c] = small[hh][c] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int ln = 0; ln < LN; ++ln) {
           constexpr int PARTS = E4M3 ? 2 : 1;
+          const int c = E4M3 ? ln * 64 * HP / 128 : 0;
 #pragma unroll
           for (int y = 0; y < PARTS; ++y) {
-            const v8bf kf = E4M3 ? decode8(kr[x][p][2 * y], kr[x][p][2 * y + 1]) : as_bf16(kr[x][p]);
-            const int c = E4M3 ? p / 2 : 0;
-            acc[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[p * PARTS + y][0], acc[c], 0, 0, 0);
+            const v8bf kf = E4M3 ? decode8(kr[x][ln][2 * y], kr[x][ln][2 * y + 1]) : as_bf16(kr[x][ln]);
 #pragma unroll
-            for (int q = 1; q < QT; ++q) small[c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[p * PARTS + y][q], small[c], 0, 0, 0);
+            for (int hh = 0; hh < HP; ++hh) {
+              const int piece = (ln * HP + hh) * PARTS + y;
+              acc[hh][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[piece][0], acc[hh][c], 0, 0, 0);
+#pragma unroll
+              for (int q = 1; q < QT; ++q)
+                small[hh][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, qf[piece][q], small[hh][c], 0, 0, 0);
+            }
           }
         }
         if (QT > 1) {
 #pragma unroll
-          for (int c = 0; c < NG; ++c) acc[c] += small[c];
+          for (int hh = 0; hh < HP; ++hh)
+#pragma unroll
+            for (int c = 0; c < NG; ++c) acc[hh][c] += small[hh][c];
         }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          float v = acc[0][r];
+        for (int r = 0; r < PER; ++r) {
+          const auto sum = [&](int c) { return HP == 1 ? acc[0][c][r] : acc[0][c][(2 * r) & 3] + acc[HP - 1][c][(2 * r + 1) & 3]; };
+          float v = sum(0);
           if (E4M3) {
-            v *= ksc[0][x][r];
-            if (NG == 2) v = fmaf(acc[NG - 1][r], ksc[NG - 1][x][r], v);
+            v *= ksc[0][x * PER + r];
+            if (NG == 2) v = fmaf(sum(NG - 1), ksc[NG - 1][x * PER + r], v);
           }
-          s[4 * x + r] = v;
+          s[x * PER + r] = v;
         }
       }
       if (LOADS) {
@@ -529,10 +552,10 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
         load_keys(w);
       }
       if (mask != ~0u) {
-        const uint32_t mine = mask >> (4 * g);
+        const uint32_t mine = mask >> (PER * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (!((mine >> ((e >> 2) * 16 + (e & 3))) & 1)) s[e] = -INFINITY;
+          if (!((mine >> token(e)) & 1)) s[e] = -INFINITY;
       }
 
       // ---- running maximum and sum, of logits that are not scaled yet: a difference of two
@@ -560,13 +583,13 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
 
       // ---- values: rows of tokens that do not exist may hold anything
       if (mask != ~0u) {
-        const uint32_t mine = mask >> (4 * g);
+        const uint32_t mine = mask >> (PER * g);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const bool there = (mine >> ((e >> 2) * 16 + (e & 3))) & 1;
+          const bool there = (mine >> token(e)) & 1;
 #pragma unroll
           for (int c = 0; c < NG; ++c) {
-            if (E4M3 && !there) vsc[c][e >> 2][e & 3] = 0.f;
+            if (E4M3 && !there) vsc[c][e] = 0.f;
 #pragma unroll
             for (int x = 0; x < VW; ++x) vr[c][e][x] = there ? vr[c][e][x] : 0u;
           }
@@ -578,7 +601,7 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
         for (int c = 0; c < NG; ++c) {
           float ps[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) ps[e] = p[e] * vsc[c][e >> 2][e & 3];
+          for (int e = 0; e < 8; ++e) ps[e] = p[e] * vsc[c][e];
           split<PT>(ps, pt[c]);
         }
       } else {
