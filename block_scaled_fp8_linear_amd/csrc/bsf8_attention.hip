@@ -147,9 +147,10 @@ __device__ __forceinline__ float sum_of_groups(float x) {
 }
 
 // Four channels of a head's result: o / l, and with channel 0 the log of the sum, the maximum's
-// part of it in F64 (it can be large); zeros and -inf where there was no token.
+// part of it in F64 (it can be large); zeros and -inf where there was no token, which is where the
+// sum is zero (logits of nothing but NaN leave the maximum at -inf and the sum NaN).
 __device__ __forceinline__ void store_result(const AttentionDev& a, int b, int head, int ch, f4 o, float m, float l) {
-  const bool none = m == -INFINITY;
+  const bool none = l == 0.f;
   float v[4];
 #pragma unroll
   for (int x = 0; x < 4; ++x) v[x] = none ? 0.f : o[x] / l;
@@ -741,20 +742,26 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionDev a)
       const int blk = min(x + y * GROUPS, to);
       const float* p = a.part + int64_t(blk == from ? task.slot : 2 * blk) * C::SLOT;
       v[y] = on ? *reinterpret_cast<const f4*>(p + row * C::CHANNELS + ch) : f4{0.f, 0.f, 0.f, 0.f};
-      pm[y] = x + y * GROUPS <= to ? p[kRows * C::CHANNELS + row] : -INFINITY;
+      pm[y] = p[kRows * C::CHANNELS + row];
       pl[y] = p[kRows * C::CHANNELS + kRows + row];
     }
+#pragma unroll
+    for (int y = 1; y < FLIGHT; ++y)
+      if (x + y * GROUPS > to) {   // (read again, not counted again)
+        pm[y] = -INFINITY;
+        pl[y] = 0.f;
+        v[y] = f4{0.f, 0.f, 0.f, 0.f};
+      }
     float top = m;
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) top = fmaxf(top, pm[y]);
-    if (top == -INFINITY) continue;
-    float f = __builtin_amdgcn_exp2f((m - top) * a.scale);
+    const float ref = top == -INFINITY ? 0.f : top;   // (parts without a token count nothing, and those of NaN NaN)
+    float f = __builtin_amdgcn_exp2f((m - ref) * a.scale);
     l *= f;
     o *= f;
 #pragma unroll
     for (int y = 0; y < FLIGHT; ++y) {
-      f = __builtin_amdgcn_exp2f((pm[y] - top) * a.scale);
-      if (f == 0.f) continue;   // (a part without a token)
+      f = __builtin_amdgcn_exp2f((pm[y] - ref) * a.scale);
       l = fmaf(pl[y], f, l);
       o += v[y] * f;
     }
@@ -771,13 +778,12 @@ __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionDev a)
 #pragma unroll
   for (int y = 1; y < GROUPS; ++y) top = fmaxf(top, lds_m[y]);
   f4 v = f4{0.f, 0.f, 0.f, 0.f};
-  if (top != -INFINITY) {
+  const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-    for (int y = 0; y < GROUPS; ++y) {
-      const float f = __builtin_amdgcn_exp2f((lds_m[y] - top) * a.scale);
-      sum = fmaf(lds_l[y], f, sum);
-      v += *reinterpret_cast<const f4*>(&lds_o[y][ch]) * f;
-    }
+  for (int y = 0; y < GROUPS; ++y) {
+    const float f = __builtin_amdgcn_exp2f((lds_m[y] - ref) * a.scale);
+    sum = fmaf(lds_l[y], f, sum);
+    v += *reinterpret_cast<const f4*>(&lds_o[y][ch]) * f;
   }
   store_result(a, task.b, task.head0 + row, ch, v, top, sum);
 }

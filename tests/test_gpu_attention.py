@@ -37,7 +37,8 @@ def _check(out, lse, q, cache, values, table, lens, window, scale):
         got = to_f64(lse)
         none = np.isneginf(wl)
         assert (np.isneginf(got) == none).all()
-        assert (np.abs(got - wl)[~none] <= (tl + 2.0 ** -23 * np.abs(wl))[~none]).all()
+        with np.errstate(invalid="ignore"):
+            assert (np.abs(got - wl)[~none] <= (tl + 2.0 ** -23 * np.abs(wl))[~none]).all()
 
 
 def _run(lens, heads, kv, D, page, codes, layout="head_major", q_dt="bf16", out_dt=None, window=0, spoil=True, seed=0,
@@ -210,6 +211,40 @@ def test_same_result_every_time():
     first = B.paged_attention(q, cache, tab, ln)
     for _ in range(20):
         assert t.equal(first, B.paged_attention(q, cache, tab, ln))
+
+
+@pytest.mark.parametrize("lens", [[40, 300], [5000, 12]])
+@pytest.mark.parametrize("codes", [True, False])
+def test_nan_is_not_hidden(lens, codes):
+    """A query or a cached row of NaN gives NaN to the heads that meet it, in one block or joined, and to no other."""
+    t = torch()
+    g = np.random.default_rng(5)
+    pages = sum(-(-n // 16) for n in lens) + 1
+    cache, _ = new_cache("head_major", pages, 16, 2, 64, codes)
+    if codes:
+        cache.k_scale.mul_(0.01), cache.v_scale.mul_(0.01)
+    table = make_table(g, lens, 16, pages)
+    tab, ln = t.from_numpy(table).to(device()), t.tensor(lens, dtype=t.int32, device=device())
+    q = t.randn(2, 4, 64, device=device())
+    want, wl = B.paged_attention(q, cache, tab, ln, lse=True)
+    banner(f"paged_attention NaN lens={lens} codes={codes}")
+    bad = q.clone()
+    bad[0, 1, 3] = float("nan")
+    out, lse = B.paged_attention(bad, cache, tab, ln, lse=True)
+    assert bool(out[0, 1].isnan().all()) and bool(lse[0, 1].isnan())
+    keep = t.ones(2, 4, dtype=t.bool, device=device())
+    keep[0, 1] = False
+    assert t.equal(out[keep], want[keep]) and t.equal(lse[keep], wl[keep])
+    row = lens[0] // 2
+    page = int(table[0, row // 16])
+    for x in (cache.k, cache.v):
+        old = x.clone()
+        x[page, row % 16, 1, 5] = 0x7F if codes else float("nan")
+        out, lse = B.paged_attention(q, cache, tab, ln, lse=True)
+        hit = out[0, 2:].isnan()
+        assert bool(hit.all()) if x is cache.k else bool(hit[:, 5].all()) and int(hit.sum()) == 2
+        assert t.equal(out[0, :2], want[0, :2]) and t.equal(out[1], want[1])
+        x.copy_(old)
 
 
 def test_no_sequences():

@@ -298,6 +298,20 @@ def test_mixed_types_and_many_tokens():
     assert t.equal(k, k[:97][idx]) and t.equal(v, v[:97][idx])
 
 
+def test_more_tokens_than_one_launch():
+    """Tokens that repeat: every repetition of the first ones gives their bits."""
+    t = torch()
+    M, n = (1 << 25) + 70, 991
+    x0 = t.randn(n, 1, 16, device=device()).bfloat16()
+    f = t.rand(8, device=device())
+    idx = t.arange(M, device=device()) % n
+    banner(f"rope of {M} tokens")
+    want, _ = B.rope(x0, t.arange(n, device=device()), f)
+    x = x0[idx]
+    got, _ = B.rope(x, idx, f, out=x)
+    assert t.equal(got, want[idx])
+
+
 def test_refusals_of_the_binding():
     t = torch()
     d = device()
