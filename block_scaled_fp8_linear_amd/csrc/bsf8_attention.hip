@@ -28,6 +28,7 @@
 // parts are, so that the second kernel need not find them again.
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
 #include <type_traits>
 
 #include "bsf8_channels.h"
@@ -897,6 +898,7 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   a.natural = scale < 0.0 ? -scale : scale;
   a.scale = float(a.natural * 1.4426950408889634);
   if (!(a.scale > 1e-30f)) a.scale = 1e-30f;   // (the weights are 1 there, and -inf times it stays -inf)
+  if (a.scale > FLT_MAX) a.scale = FLT_MAX;    // (the largest logit's weight is 1 there, and 0 times it stays 0)
   if (c.e4m3) launch_dims<true>(a, f32, scale_vec, stream);
   else launch_dims<false>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");

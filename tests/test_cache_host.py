@@ -10,8 +10,8 @@ name = B.status_name
 
 
 def make_cache(**kw):
-    """Head-major E4M3 pages of 16 rows, 4 heads of 192 channels; ``kw`` replaces fields."""
-    c = B.Cache(B.DT_F8_E4M3, 4, 192, 16, 10, FAKE, FAKE, 4 * 16 * 192, 192, 16 * 192, FAKE, FAKE, 4 * 2 * 16, 1, 32, 16)
+    """Head-major E4M3 pages of 16 rows, 4 heads of 208 channels; ``kw`` replaces fields."""
+    c = B.Cache(B.DT_F8_E4M3, 4, 208, 16, 10, FAKE, FAKE, 4 * 16 * 208, 208, 16 * 208, FAKE, FAKE, 4 * 2 * 16, 1, 32, 16)
     for k, v in kw.items():
         setattr(c, k, v)
     return c
@@ -24,18 +24,18 @@ def _validate(**kw):
 def test_cache_descriptor():
     assert name(B.lib().bsf8_cache_validate(None)) == "INVALID_ARG"
     assert _validate() == "OK"
-    assert _validate(page=16 * 4 * 192, row=4 * 192, head=192) == "OK"                       # token-major
-    assert _validate(page=2 * 16 * 4 * 192, row=4 * 192, head=192) == "OK"                   # keys and values side by side
+    assert _validate(page=16 * 4 * 208, row=4 * 208, head=208) == "OK"                       # token-major
+    assert _validate(page=2 * 16 * 4 * 208, row=4 * 208, head=208) == "OK"                   # keys and values side by side
     assert _validate(dtype=B.DT_BF16, k_scale=None, v_scale=None) == "OK"
     assert _validate(n_pages=1, page=0) == "OK" and _validate(heads=1, head=0, s_head=0) == "OK"
     for bad in (dict(dtype=B.DT_F32), dict(dtype=B.DT_F8_E5M2), dict(heads=0), dict(head_dim=0), dict(page_size=0),
                 dict(n_pages=0), dict(heads=-1), dict(n_pages=-5), dict(k=None), dict(v=None), dict(k_scale=None),
-                dict(v_scale=None), dict(dtype=B.DT_BF16), dict(dtype=B.DT_BF16, k_scale=None), dict(page=-16), dict(row=-192),
-                dict(row=176), dict(head=192), dict(page=4 * 16 * 192 - 16), dict(page=0), dict(s_row=-1), dict(s_row=0),
+                dict(v_scale=None), dict(dtype=B.DT_BF16), dict(dtype=B.DT_BF16, k_scale=None), dict(page=-16), dict(row=-208),
+                dict(row=176), dict(head=208), dict(page=4 * 16 * 208 - 16), dict(page=0), dict(s_row=-1), dict(s_row=0),
                 dict(s_group=15), dict(s_head=16), dict(s_page=127), dict(page=1 << 62), dict(n_pages=1, page=1 << 62)):
         assert _validate(**bad) == "INVALID_ARG", bad
-    for bad in (dict(k=FAKE + 8), dict(v=FAKE + 1), dict(row=200, head=16 * 200, page=64 * 200), dict(k_scale=FAKE + 2),
-                dict(v_scale=FAKE + 1), dict(dtype=B.DT_BF16, k_scale=None, v_scale=None, head=16 * 192 + 4, page=1 << 14)):
+    for bad in (dict(k=FAKE + 8), dict(v=FAKE + 1), dict(row=216, head=16 * 216, page=64 * 216), dict(k_scale=FAKE + 2),
+                dict(v_scale=FAKE + 1), dict(dtype=B.DT_BF16, k_scale=None, v_scale=None, head=16 * 208 + 4, page=1 << 14)):
         assert _validate(**bad) == "ALIGNMENT", bad
     for bad in (dict(head_dim=72), dict(head_dim=272), dict(head_dim=8), dict(n_pages=1 << 27), dict(n_pages=1 << 40),
                 dict(heads=1, head=0, row=1 << 28, page=1 << 33), dict(page=1 << 32), dict(s_page=1 << 32),
@@ -78,7 +78,7 @@ def test_rope_refusals():
         assert _rope(**bad) == "UNSUPPORTED", bad
 
 
-def _write(cache=None, M=5, k=H(token=768, head=192, heads=4), v=H(token=768, head=192, heads=4), slots=FAKE, b=8, rope=None):
+def _write(cache=None, M=5, k=H(token=832, head=208, heads=4), v=H(token=832, head=208, heads=4), slots=FAKE, b=8, rope=None):
     c = make_cache() if cache is None else cache
     ref = lambda x: ctypes.byref(x) if x is not None else None
     return name(B.lib().bsf8_cache_write(ref(c), M, ref(k), ref(v), slots, b, ref(rope), None))
@@ -87,20 +87,20 @@ def _write(cache=None, M=5, k=H(token=768, head=192, heads=4), v=H(token=768, he
 def test_cache_write_refusals():
     def rope(**kw):
         a = B.RopeArgs()
-        a.M, a.head_dim, a.rotary_dim, a.n_axes, a.positions, a.position_bytes = 5, 192, 64, 1, FAKE, 4
+        a.M, a.head_dim, a.rotary_dim, a.n_axes, a.positions, a.position_bytes = 5, 208, 64, 1, FAKE, 4
         a.inv_freq, a.scale, a.eps, a.weight_dtype = FAKE, 1.0, 1e-6, B.DT_F32
         for key, val in kw.items():
             setattr(a, key, val)
         return a
 
-    heads = dict(token=768, head=192, heads=4)
+    heads = dict(token=832, head=208, heads=4)
     assert _write(M=0) == "OK" and _write(M=0, k=None, v=None, slots=None) == "OK"
     assert name(B.lib().bsf8_cache_write(None, 0, None, None, None, 8, None, None)) == "INVALID_ARG"
     for bad in (dict(cache=make_cache(heads=0)), dict(M=-1), dict(k=None), dict(v=None), dict(slots=None), dict(b=2),
-                dict(k=H(token=768, head=192, heads=3)), dict(v=H(token=768, head=192, heads=5)), dict(k=H(None, **heads)),
+                dict(k=H(token=832, head=208, heads=3)), dict(v=H(token=832, head=208, heads=5)), dict(k=H(None, **heads)),
                 dict(k=H(dtype=B.DT_U8, **heads)), dict(rope=rope(M=4)), dict(rope=rope(head_dim=64)),
                 dict(rope=rope(k=H(**heads))), dict(rope=rope(k_out=H(**heads))), dict(rope=rope(q=H(**heads))),
-                dict(rope=rope(q_weight=FAKE)), dict(rope=rope(k_weight=FAKE, eps=-1.0)), dict(rope=rope(rotary_dim=194))):
+                dict(rope=rope(q_weight=FAKE)), dict(rope=rope(k_weight=FAKE, eps=-1.0)), dict(rope=rope(rotary_dim=210))):
         assert _write(**bad) == "INVALID_ARG", bad
     for bad in (dict(k=H(FAKE + 1, **heads)), dict(v=H(FAKE + 2, B.DT_F32, **heads)), dict(slots=FAKE + 4), dict(slots=FAKE + 2, b=4),
                 dict(rope=rope(k_weight=FAKE + 1))):
@@ -109,20 +109,20 @@ def test_cache_write_refusals():
     assert _write(cache=make_cache(head_dim=72)) == "UNSUPPORTED"
 
 
-def _read(cache=None, B_=3, table=FAKE, ld=8, pages=8, starts=None, off=FAKE, R=20, k=H(token=768, head=192, heads=4),
-          v=H(token=768, head=192, heads=4)):
+def _read(cache=None, B_=3, table=FAKE, ld=8, pages=8, starts=None, off=FAKE, R=20, k=H(token=832, head=208, heads=4),
+          v=H(token=832, head=208, heads=4)):
     c = make_cache() if cache is None else cache
     ref = lambda x: ctypes.byref(x) if x is not None else None
     return name(B.lib().bsf8_cache_read(ref(c), B_, table, ld, pages, starts, off, R, ref(k), ref(v), None))
 
 
 def test_cache_read_refusals():
-    heads = dict(token=768, head=192, heads=4)
+    heads = dict(token=832, head=208, heads=4)
     assert _read(B_=0) == "OK" and _read(R=0) == "OK"
     assert name(B.lib().bsf8_cache_read(None, 0, None, 0, 0, None, None, 0, None, None, None)) == "INVALID_ARG"
     for bad in (dict(B_=-1), dict(R=-1), dict(table=None), dict(ld=7), dict(pages=0), dict(pages=-1), dict(off=None),
                 dict(k=None, v=None), dict(k=H(None, **heads), v=None), dict(k=H(dtype=B.DT_F32, **heads)),
-                dict(v=H(token=768, head=192, heads=3)), dict(k=H(token=700, head=192, heads=4)), dict(k=H(token=0, head=192, heads=4)),
+                dict(v=H(token=832, head=208, heads=3)), dict(k=H(token=700, head=208, heads=4)), dict(k=H(token=0, head=208, heads=4)),
                 dict(ld=1 << 61), dict(k=H(dtype=B.DT_U8, **heads))):
         assert _read(**bad) == "INVALID_ARG", bad
     for bad in (dict(table=FAKE + 2), dict(off=FAKE + 1), dict(starts=FAKE + 2), dict(k=H(FAKE + 1, **heads))):
@@ -147,7 +147,7 @@ def test_rope_axes():
 def _attention(cache=None, ws=FAKE, wsb=1 << 40, **kw):
     a = B.AttentionArgs()
     a.B, a.table, a.ld_table, a.pages, a.lens, a.scale = 3, FAKE, 100, 100, FAKE, 0.1
-    a.q = a.out = B.Heads(FAKE, B.DT_BF16, 8, 8 * 192, 192)
+    a.q = a.out = B.Heads(FAKE, B.DT_BF16, 8, 8 * 208, 208)
     for key, val in kw.items():
         setattr(a, key, val)
     c = make_cache() if cache is None else cache
@@ -156,14 +156,14 @@ def _attention(cache=None, ws=FAKE, wsb=1 << 40, **kw):
 
 def test_attention_refusals():
     L = B.lib()
-    wide = dict(token=8 * 192, head=192, heads=8)
+    wide = dict(token=8 * 208, head=208, heads=8)
     assert _attention(B=0) == "OK" and _attention(B=0, lens=None, table=None) == "OK"
     assert name(L.bsf8_paged_attention(ctypes.byref(make_cache()), None, None, 0, None)) == "INVALID_ARG"
     assert name(L.bsf8_paged_attention(None, ctypes.byref(B.AttentionArgs()), None, 0, None)) == "INVALID_ARG"
     for bad in (dict(cache=make_cache(heads=0)), dict(B=-1), dict(window=-1), dict(scale=float("nan")), dict(scale=float("inf")),
-                dict(q=H(heads=6, token=8 * 192, head=192)), dict(q=H(heads=0, token=8 * 192, head=192)), dict(q=H(None, **wide)),
-                dict(out=H(heads=4, token=8 * 192, head=192)), dict(out=H(None, **wide)), dict(q=H(dtype=B.DT_F16, **wide)),
-                dict(out=H(dtype=B.DT_F8_E4M3, **wide)), dict(out=H(heads=8, token=8 * 192 - 1, head=192)), dict(table=None),
+                dict(q=H(heads=6, token=8 * 208, head=208)), dict(q=H(heads=0, token=8 * 208, head=208)), dict(q=H(None, **wide)),
+                dict(out=H(heads=4, token=8 * 208, head=208)), dict(out=H(None, **wide)), dict(q=H(dtype=B.DT_F16, **wide)),
+                dict(out=H(dtype=B.DT_F8_E4M3, **wide)), dict(out=H(heads=8, token=8 * 208 - 1, head=208)), dict(table=None),
                 dict(lens=None), dict(pages=0), dict(ld_table=99)):
         assert _attention(**bad) == "INVALID_ARG", bad
     for bad in (dict(table=FAKE + 2), dict(lens=FAKE + 1), dict(lse=FAKE + 2), dict(q=H(FAKE + 1, **wide)), dict(out=H(FAKE + 1, **wide)),

@@ -105,7 +105,7 @@ def test_window(codes, window, page):
 
 
 @pytest.mark.parametrize("codes", [True, False])
-@pytest.mark.parametrize("lens,heads,kv,D,page", [([20000], 8, 1, 128, 16), ([30001], 4, 4, 64, 64), ([9000, 3, 17000], 12, 2, 256, 32),
+@pytest.mark.parametrize("lens,heads,kv,D,page", [([20000], 8, 1, 128, 16), ([30001], 4, 4, 64, 64), ([9000, 3, 17000], 10, 2, 256, 32),
                                                   ([5000] + [1] * 300, 4, 2, 128, 16), (list(range(1, 1200, 3)), 5, 5, 80, 16),
                                                   ([40000], 20, 1, 192, 128), ([4099] * 9, 32, 8, 128, 13)])
 def test_long_and_ragged(codes, lens, heads, kv, D, page):
@@ -184,6 +184,23 @@ def test_large_logits_and_scales(codes):
     _run([600, 40], 4, 2, 64, 16, codes, scale=3.0)
     _run([600, 40], 4, 2, 64, 16, codes, scale=0.0)
     _run([600, 40], 4, 2, 64, 16, codes, scale=-0.3, q_dt="f32")
+
+
+def test_a_scale_beyond_f32():
+    """Weights of one and zero: the value of the largest logit."""
+    t = torch()
+    cache, _ = new_cache("head_major", 50, 16, 1, 64, False)
+    cache.k.normal_(), cache.v.normal_()
+    table = t.arange(50, dtype=t.int32, device=device())[None]
+    q = t.zeros(1, 2, 64, device=device())
+    q[0, 0, 0], q[0, 1, 0] = 1.0, -1.0
+    cache.k[30, 5, 0, 0], cache.k[7, 2, 0, 0] = 100.0, -100.0
+    banner("paged_attention of a scale of 1e300")
+    for n in (400, 800):   # (the first head's largest logit is among the tokens of the second alone)
+        out = B.paged_attention(q, cache, table, t.tensor([n], dtype=t.int32, device=device()), scale=1e300)
+        assert t.equal(out[0, 1], cache.v[7, 2, 0].float())
+        assert n == 400 or t.equal(out[0, 0], cache.v[30, 5, 0].float())
+        assert bool(out.isfinite().all())
     t = torch()
     cache, _ = new_cache("head_major", 20, 16, 1, 64, False)
     n = 310
