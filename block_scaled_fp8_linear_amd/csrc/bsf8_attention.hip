@@ -26,6 +26,12 @@
 // the lengths alone decide.  The blocks find their ranges by a sum over the lengths, so nothing
 // is read on the host; the block that holds an item's beginning leaves a note of where its
 // parts are, so that the second kernel need not find them again.
+//
+// Measured (kernels alone, joining apart): 64 sequences to 8192, 8 key heads of 128 E4M3 channels,
+// 379 MB: 82 + 6 us, 4.6 TB/s; 256 to 1000, 24 heads of 80 BF16 channels, 661 MB: 125 us, 5.3 TB/s,
+// what a copy reaches; one of 131072, 4 key heads of E4M3, 138 MB: 28 + 5; F32 queries of 7 to 5000
+// (window 2048, 256 BF16 channels, 38 MB): 21.5 + 4, a tile or two for each compute unit, so that
+// the time is that of a wave's chain from lengths over table and rows to the products.
 #include <hip/hip_runtime.h>
 
 #include <cfloat>
@@ -722,6 +728,8 @@ __global__ __launch_bounds__(64 * most_waves(C::DIM, C::QT > 1), waves_per_simd(
 
 // Adds the parts of the items that lie in more than one block, a query head per block of this
 // kernel: groups of lanes take every so many parts, with a maximum of their own.
+// Bound by latency: the note, then the parts, then the groups' sums.  64 sequences of 40 heads
+// take 6 us, 32 heads of hundreds of parts each 5 with 1024 threads.
 template <int DIM, int THREADS>
 __global__ __launch_bounds__(THREADS) void attention_join_kernel(AttentionDev a) {
   using C = Config<false, DIM, false, 1, 2, kAny>;   // (a slot has one size for both types of cache)
