@@ -5,7 +5,12 @@
 //   x' = x / sqrt(mean(x^2) + eps) * w;  (a, b) -> (a cos t - b sin t, b cos t + a sin t)
 // Everything is F64 up to one rounding to F32, as in the norm step: a code next to a border
 // changes by a whole step with the last bit of an F32 sum, and F64 FMAs run at the F32 rate
-// here.  It bounds nothing: a channel costs some 15 vector instructions against 3 to 6 bytes.
+// here.  Memory bounds rows that only turn (4096 tokens of 48 heads of 128 F32 channels to BF16,
+// 151 MB: 30.5 us, 4.9 TB/s; 8192 of BF16, 201 MB: 41); where codes are made the vector
+// instructions take about as long as the bytes (8192 tokens' keys, turned, and values, 8 heads of
+// 128 each, 51 MB: 17.5 us, into BF16 rows, 67 MB, 14.6).  So a pass over values alone skips the
+// arithmetic, a lane past its row is left out only where it would count, and the largest of a
+// group is found by lane exchanges in the adder's path, not by LDS (20.5 -> 17.5 us together).
 //
 // A row is LPR = 8, 16 or 32 lanes of 8 channels (head_dim up to 64, 128, 256), so that a
 // 128-channel scale group is 16 lanes, and a wave holds 64 / LPR rows, all of one token:
@@ -14,6 +19,8 @@
 // rather than exchanged between lanes: it is in the cache line that the row's own lanes ask
 // for.  An output may be its input: a row's stores need values of all the loads of its wave.
 #include <hip/hip_runtime.h>
+
+#include <type_traits>
 
 #include "bsf8_channels.h"
 #include "bsf8_fused.h"
@@ -82,10 +89,12 @@ constexpr int kMostPairs = BSF8_CACHE_MAX_HEAD_DIM / 2;
 template <int PAIRS>
 __device__ __forceinline__ void turn_factors(const HeadsJob& a, int c0, int64_t m, Turn* lds, double (&cs)[EPL], double (&sn)[EPL]) {
   const int R = a.R, half = R >> 1;
+  if (PAIRS != kHalf) {
 #pragma unroll
-  for (int e = 0; e < EPL; ++e) {
-    cs[e] = 1.0;
-    sn[e] = 0.0;
+    for (int e = 0; e < EPL; ++e) {
+      cs[e] = 1.0;
+      sn[e] = 0.0;
+    }
   }
   if (PAIRS == kNone) return;
   const double p0 = a.n_axes == 1 ? position(a, 0, m) : 0.0;
@@ -100,6 +109,18 @@ __device__ __forceinline__ void turn_factors(const HeadsJob& a, int c0, int64_t 
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  if (PAIRS == kHalf) {
+    // a lane's channels are all of one half; those that do not turn take the first ones and leave them unused
+    const uint64_t sign = c0 >= half ? 0 : uint64_t(1) << 63;
+    const int i0 = c0 >= R ? 0 : c0 >= half ? c0 - half : c0;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) {
+      const Turn t = lds[i0 + e];
+      cs[e] = t.c;
+      sn[e] = __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, t.s) ^ sign);
+    }
+    return;
+  }
   if (c0 >= R) return;
   if (PAIRS == kAdjacent) {
 #pragma unroll
@@ -114,7 +135,7 @@ __device__ __forceinline__ void turn_factors(const HeadsJob& a, int c0, int64_t 
 #pragma unroll
     for (int e = 0; e < EPL; ++e) {
       const int ch = c0 + e;
-      if (PAIRS == kHalfOdd && ch >= R) continue;
+      if (ch >= R) continue;
       const bool second = ch >= half;
       const Turn t = lds[second ? ch - half : ch];
       cs[e] = t.c;
@@ -157,6 +178,18 @@ __device__ __forceinline__ CacheRow cache_row(const CacheDev& c, int64_t slot) {
   const uint64_t at = uint64_t(int64_t(page) * c.page + int64_t(row) * c.row), s = uint64_t(int64_t(page) * c.s_page + int64_t(row) * c.s_row) * 4;
   return CacheRow{uint64_t(c.k) + at, uint64_t(c.v) + at, uint64_t(c.k_scale) + s, uint64_t(c.v_scale) + s};
 }
+// the largest of 8 or 16 neighbouring lanes: exchanged in pairs, in fours, and mirrored in eights and sixteens
+template <int LANES>
+__device__ __forceinline__ float max_of_group(float x) {
+  const auto with = [](float v, auto control) {
+    return fmaxf(v, __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), decltype(control)::value, 0xF, 0xF, true)));
+  };
+  x = with(x, std::integral_constant<int, 0xB1>{});
+  x = with(x, std::integral_constant<int, 0x4E>{});
+  x = with(x, std::integral_constant<int, 0x141>{});
+  if (LANES == 16) x = with(x, std::integral_constant<int, 0x140>{});
+  return x;
+}
 template <int LPR>
 __device__ __forceinline__ void store_cached(const CacheDev& c, const CacheRow& to, bool is_v, int h, int c0, bool on,
                                              const float (&f)[EPL]) {
@@ -170,8 +203,7 @@ __device__ __forceinline__ void store_cached(const CacheDev& c, const CacheRow& 
   float amax = 0.0f;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) amax = fmaxf(amax, fabsf(f[e]));
-#pragma unroll
-  for (int d = (LPR < LPG ? LPR : LPG) / 2; d >= 1; d >>= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+  amax = max_of_group<LPR < LPG ? LPR : LPG>(on ? amax : 0.f);
   float s;
   uint32_t packed[EPL / 4];
   encode(f, amax, s, packed);
@@ -354,26 +386,28 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
   double cs[EPL], sn[EPL];
   turn_factors<PAIRS>(a, c0, m, turn[threadIdx.x >> 6], cs, sn);
 
-  for (int at = first + lane / LPR; at < last; at += RPP) {
+  for (int pass = first; pass < last; pass += RPP) {
+    const int at = pass + lane / LPR;
+    if (at >= last) break;
     const Raw<XBF16> x = next_x, p = next_p;
     fetch(at + RPP, next_x, next_p);
     const bool is_q = kinds.is_q(at), is_v = kinds.is_v(at);
     const int h = kinds.head(at);
-    float f[EPL];
-    if (is_v) {
+    float f[EPL];   // (of lanes past the row: its first channels, left unused)
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) f[e] = on ? value<XBF16>(x, e) : 0.f;
-    } else {
+    for (int e = 0; e < EPL; ++e) f[e] = value<XBF16>(x, e);
+    if ((PAIRS != kNone || NORM) && pass < kinds.values) {   // not values alone: one choice for the wave
       double v[EPL], vp[EPL];
 #pragma unroll
       for (int e = 0; e < EPL; ++e) {
-        v[e] = on ? double(value<XBF16>(x, e)) : 0.0;
+        v[e] = double(f[e]);
         vp[e] = PAIRS == kHalf ? double(value<XBF16>(p, e)) : 0.0;
       }
       if (NORM && (is_q ? a.qw : a.kw) != nullptr) {
         double sum = 0.0;
 #pragma unroll
         for (int e = 0; e < EPL; ++e) sum = fma(v[e], v[e], sum);
+        sum = on ? sum : 0.0;
 #pragma unroll
         for (int d = LPR / 2; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
         const double rstd = rsqrt64(fma(sum, 1.0 / double(D), a.eps));
@@ -385,10 +419,11 @@ __global__ __launch_bounds__(kThreads) void heads_wide_kernel(HeadsJob a) {
       }
 #pragma unroll
       for (int e = 0; e < EPL; ++e) {
-        double y = v[e];
-        if (PAIRS == kHalf && turns) y = fma(cs[e], v[e], sn[e] * vp[e]);
-        if (PAIRS == kAdjacent && c0 + e < R) y = fma(cs[e], v[e], sn[e] * v[e ^ 1]);
-        f[e] = to_f32(y);
+        // (chosen beside the sum: a channel that does not turn keeps its zero's sign)
+        const bool turned = PAIRS == kHalf ? turns : PAIRS == kAdjacent && c0 + e < R;
+        const double y = fma(cs[e], v[e], sn[e] * (PAIRS == kHalf ? vp[e] : v[e ^ 1]));
+        if (NORM) f[e] = is_v ? f[e] : to_f32(turned ? y : v[e]);
+        else f[e] = is_v || !turned ? f[e] : to_f32(y);
       }
     }
     if (is_q || !a.to_cache) {
@@ -487,8 +522,8 @@ __global__ __launch_bounds__(kThreads) void cache_read_kernel(ReadJob a) {
 }
 
 // Waves that fill the device: a token is split over more of them only up to here, since each makes
-// the token's sines and cosines again (1024 tokens of 48 heads with norms: 4096 waves 15.7 us, 8192
-// 20.7; 4096 tokens with their cache rows 27, 29 and, at 16384, 36).  Rows read back share nothing.
+// the token's sines and cosines again (1024 tokens of 48 heads with norms: 4096 waves 15 us, 8192
+// 19.4; 4096 tokens with their cache rows 25, 25 and, at 16384, 29).  Rows read back share nothing.
 constexpr int64_t kEnoughWaves = 4096, kReadWaves = 8192;
 constexpr int64_t kMostWaves = int64_t(1) << 25;    // of one launch (2^31 threads)
 
