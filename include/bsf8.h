@@ -677,7 +677,8 @@ bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* t
  *         position (length 0) has out = 0 and lse = -inf.
  * table : device int32 [B, pages], row pitch ld_table.  A position on a page outside
  *         [0, n_pages) is left out of the sums.  What rows past the length hold (NaN
- *         too) does not reach the result.
+ *         too) does not reach the result.  NaN in a query, or in a key or value that counts,
+ *         reaches every head that meets it; an infinity there may become NaN.
  * q, out : [B, heads] F32 or BF16; heads a multiple of the cache's.  out may not
  *         overlap an input.
  * lse   : device F32 [B, heads] contiguous, or NULL.
