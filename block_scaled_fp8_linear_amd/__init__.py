@@ -1074,6 +1074,10 @@ class RopeAxes(bytes):
         self.address = ctypes.addressof(self._held)
         return self
 
+    def __reduce__(self):
+        # a copy holds its bytes itself: the address of another's would be read after that one is gone
+        return RopeAxes, (bytes(self),)
+
 
 def rope_axes(sections: Sequence[int], interleaved: bool = False) -> RopeAxes:
     """The axis of each rotated pair, for ``axes`` of rope and cache_write: ``sections`` pairs of each axis one after the

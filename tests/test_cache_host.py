@@ -218,3 +218,17 @@ def test_workspace_is_asked_on_the_caches_device(monkeypatch, current, owner):
     cache = types.SimpleNamespace(_idx=owner, _ref=None)
     assert B.attention_workspace_size(cache, 3, 8, 100) == 0
     assert seen == [owner] and state == [current]
+
+
+def test_copied_axes_are_read_where_the_copy_keeps_them():
+    """What the library reads of a copied or pickled RopeAxes is the copy's own memory, which outlives the original's."""
+    import copy
+    import pickle
+
+    axes = B.rope_axes([2, 3, 1])
+    held = {"axes": axes}
+    for other in (copy.copy(axes), copy.deepcopy(axes), copy.deepcopy(held)["axes"], pickle.loads(pickle.dumps(axes)),
+                  pickle.loads(pickle.dumps(axes, 0))):
+        assert type(other) is B.RopeAxes and other == axes
+        assert other.address == ctypes.addressof(other._held) and bytes(other._held) == bytes(other)
+    assert copy.deepcopy(axes).address != axes.address
