@@ -517,10 +517,7 @@ static bsf8_status rope_checks(const bsf8_rope_args& r, bool keys, HeadsJob* a) 
   if (r.head_dim % 16 || r.head_dim > BSF8_CACHE_MAX_HEAD_DIM)
     return fail(BSF8_E_UNSUPPORTED, "head_dim %d (a multiple of 16 up to %d)", r.head_dim, BSF8_CACHE_MAX_HEAD_DIM);
   if (r.pairing != BSF8_PAIR_HALF && r.pairing != BSF8_PAIR_ADJACENT) return fail(BSF8_E_INVALID_ARG, "pairing %d", r.pairing);
-  if (r.q.data == nullptr && r.q_out.data != nullptr) return fail(BSF8_E_INVALID_ARG, "q_out without q");
-  if (r.q.data == nullptr && r.q_weight) return fail(BSF8_E_INVALID_ARG, "q_weight without q");
   if (!keys && (r.k.data || r.k_out.data)) return fail(BSF8_E_INVALID_ARG, "the keys of a cache write are its own");
-  if (keys && r.k.data == nullptr && (r.k_out.data || r.k_weight)) return fail(BSF8_E_INVALID_ARG, "k_out or k_weight without k");
   if (r.q_weight || r.k_weight) {
     if (!dtype_ok(r.weight_dtype, true, true)) return fail(BSF8_E_INVALID_ARG, "weight dtype %d (F32 or BF16)", r.weight_dtype);
     if (!(r.eps > 0.0) || !std::isfinite(r.eps)) return fail(BSF8_E_INVALID_ARG, "eps %g (positive)", r.eps);
@@ -537,6 +534,10 @@ static bsf8_status rope_checks(const bsf8_rope_args& r, bool keys, HeadsJob* a) 
   a->R = r.rotary_dim;
   a->half = r.pairing == BSF8_PAIR_HALF ? 1 : 0;
   if (r.M == 0) return BSF8_OK;
+  // (heads of no tokens may have no address: only from here on is NULL what is absent)
+  if (r.q.data == nullptr && r.q_out.data != nullptr) return fail(BSF8_E_INVALID_ARG, "q_out without q");
+  if (r.q.data == nullptr && r.q_weight) return fail(BSF8_E_INVALID_ARG, "q_weight without q");
+  if (keys && r.k.data == nullptr && (r.k_out.data || r.k_weight)) return fail(BSF8_E_INVALID_ARG, "k_out or k_weight without k");
   if (r.M > INT32_MAX) return fail(BSF8_E_UNSUPPORTED, "M too large");
   if (r.rotary_dim) {
     if (r.positions == nullptr || r.inv_freq == nullptr) return fail(BSF8_E_INVALID_ARG, "null positions or inv_freq");

@@ -537,7 +537,7 @@ const char* bsf8_experts_describe(const bsf8_experts* w, int64_t R);
  * taken where address and strides allow them.
  */
 typedef struct bsf8_heads {
-  void* data;      /* NULL: absent */
+  void* data;      /* NULL: absent (without tokens: absent or empty) */
   int32_t dtype;   /* BSF8_DT_F32 or BSF8_DT_BF16 */
   int32_t heads;
   int64_t token, head;

@@ -232,3 +232,47 @@ def test_copied_axes_are_read_where_the_copy_keeps_them():
         assert type(other) is B.RopeAxes and other == axes
         assert other.address == ctypes.addressof(other._held) and bytes(other._held) == bytes(other)
     assert copy.deepcopy(axes).address != axes.address
+
+
+def test_no_tokens_with_head_weights():
+    """An empty tensor has no address, so without tokens a weight is not refused for want of its heads: rope, and a cache's
+    queries and keys."""
+    none = H(None)
+    for kw in (dict(q_weight=FAKE), dict(k_weight=FAKE), dict(q_weight=FAKE, k_weight=FAKE), dict(q_out=H(), q_weight=FAKE),
+               dict(k_out=H(), k_weight=FAKE)):
+        kw = dict(dict(q_out=none), **kw)
+        assert _rope(M=0, q=none, **kw) == "OK", kw
+        assert _rope(M=5, q=none, **kw) == "INVALID_ARG", kw
+    for kw in (dict(q_weight=FAKE), dict(q_weight=FAKE, k_weight=FAKE), dict(q_out=H(heads=4), q_weight=FAKE)):
+        for M, want in ((0, "OK"), (5, "INVALID_ARG")):
+            a = B.RopeArgs()
+            a.M, a.head_dim, a.rotary_dim, a.n_axes, a.positions, a.position_bytes = M, 208, 64, 1, FAKE, 4
+            a.inv_freq, a.scale, a.eps, a.weight_dtype = FAKE, 1.0, 1e-6, B.DT_F32
+            for key, val in kw.items():
+                setattr(a, key, val)
+            assert _write(M=M, rope=a) == want, kw
+    # what is wrong whatever the tokens stays refused
+    assert _rope(M=0, q=none, q_out=none, q_weight=FAKE, eps=0.0) == "INVALID_ARG"
+    assert _rope(M=0, q=none, q_out=none, k_weight=FAKE, weight_dtype=B.DT_F16) == "INVALID_ARG"
+
+
+def test_the_binding_without_tokens_and_with_head_weights(monkeypatch):
+    """The same through the binding, which passes an empty tensor's address (host tensors, nothing is launched)."""
+    import types
+
+    import torch
+    monkeypatch.setattr(B, "_CURRENT", (lambda: -1, lambda idx: 0))
+    monkeypatch.setattr(B, "_gpu_index", lambda name, t: -1)
+    monkeypatch.setattr(B, "_T", torch)
+    x = torch.randn(3, 12, 208)
+    q, k, v = x[:0, :4], x[:0, 4:8], x[:0, 8:]
+    assert q.data_ptr() == 0
+    w, inv, pos = torch.ones(208), torch.ones(32), torch.arange(3)[:0]
+    for kw in (dict(q_weight=w), dict(k=k, k_weight=w), dict(k=k, q_weight=w, k_weight=w, k_out=torch.empty(0, 4, 208))):
+        y, yk = B.rope(q, pos, inv, **kw)
+        assert y.shape == (0, 4, 208) and (yk is None) == ("k" not in kw)
+    c = make_cache()
+    cache = types.SimpleNamespace(_idx=-1, heads=4, head_dim=208, _ref=ctypes.byref(c))
+    y = B.cache_write(cache, k, v, pos, positions=pos, inv_freq=inv, q=q, q_weight=w, k_weight=w)
+    assert y.shape == (0, 4, 208)
+    assert B.cache_write(cache, k, v, pos, positions=pos, inv_freq=inv, k_weight=w) is None
