@@ -47,6 +47,7 @@ constexpr int kMostWaves = 8;                 // of a block; four or eight
 constexpr int kWaveTokens = 32;
 constexpr int kRows = 16;                     // query heads of an item
 constexpr int kWholeTokens = 512;             // up to here an item is a block's
+constexpr float kDown = 0x1p-64f;             // of queries, where the scale is very small
 
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
@@ -75,8 +76,9 @@ struct AttentionDev {
   int32_t whole;        // a block per item, nothing to join
   int32_t tile_shift;   // a tile is 1 << tile_shift tokens: 32 for each wave of a block
   int32_t negative;     // the scale is: queries change their sign, and `scale` is its size
+  int32_t small;        // and very small: queries are taken down by 2^64, and `scale` is up by it
   float scale;          // log2(e) included; not zero
-  double natural;       // the size of the scale
+  double natural;       // the size of the scale, for such queries
 };
 
 // An item whose parts lie in blocks `slot / 2` .. `to`: the first in `slot`, the others in the
@@ -291,11 +293,16 @@ struct Queries {
         u4 v;
 #pragma unroll
         for (int x = 0; x < 4; ++x) v[x] = there ? raw[s][0][x] ^ sign : 0u;
+        if (a.small) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = bf16_pair(__uint_as_float(v[x] << 16) * kDown, __uint_as_float(v[x] & 0xFFFF0000u) * kDown);
+        }
         qf[s][0] = as_bf16(v);
       } else {
         float x[8];
+        const float by = a.small ? kDown : 1.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = there ? __uint_as_float(raw[s][(e >> 2) % W][e & 3] ^ sign) : 0.f;
+        for (int e = 0; e < 8; ++e) x[e] = there ? __uint_as_float(raw[s][(e >> 2) % W][e & 3] ^ sign) * by : 0.f;
         split<C::QT>(x, qf[s]);
       }
     }
@@ -904,9 +911,16 @@ bsf8_status launch_attention(const CacheDev& c, const HeadsDev& q, const HeadsDe
   }
   a.negative = scale < 0.0 ? 1 : 0;
   a.natural = scale < 0.0 ? -scale : scale;
-  a.scale = float(a.natural * 1.4426950408889634);
-  if (!(a.scale > 1e-30f)) a.scale = 1e-30f;   // (the weights are 1 there, and -inf times it stays -inf)
-  if (a.scale > FLT_MAX) a.scale = FLT_MAX;    // (the largest logit's weight is 1 there, and 0 times it stays 0)
+  constexpr double kLog2e = 1.4426950408889634;
+  // A scale below 2^-100 makes logits of products so large that their differences leave F32: queries
+  // 2^64 times smaller under a scale as much larger are the same logits.  (A query's bits below 2^-126
+  // of F32 go, 2^8 channels times 2^-126 times keys up to 2^128 times the scale's 2^-36: 2^-26 of a
+  // logit at most.)  Below 2^-126 then, zero among them, differences of up to 2^65 leave all weights 1.
+  a.small = a.natural * kLog2e < 0x1p-100 ? 1 : 0;
+  if (a.small) a.natural *= 0x1p64;
+  a.scale = float(a.natural * kLog2e);
+  if (!(a.scale > FLT_MIN)) a.scale = FLT_MIN;   // (-inf times it stays -inf)
+  if (a.scale > FLT_MAX) a.scale = FLT_MAX;      // (the largest logit's weight is 1 there, and 0 times it stays 0)
   if (c.e4m3) launch_dims<true>(a, f32, scale_vec, stream);
   else launch_dims<false>(a, f32, scale_vec, stream);
   bsf8_status st = device_status(hipGetLastError(), "paged_attention launch");

@@ -673,6 +673,9 @@ bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* t
  * their product with the values as two BF16 terms (17 bits or more; three, 24 bits,
  * where q or out is F32).  The sums' order depends on the batch and on the device's
  * compute units, never on timing.
+ * scale : any finite one, of either sign; the sums over d without it have to fit F32.  At
+ *         zero all weights are one.  One beyond 2.3e38 counts as that (differences of the sums
+ *         above some 1e-36 then pick the largest logit all the same).
  * lens  : device int32 [B]; clamped to [0, pages * page_size].  A sequence with no
  *         position (length 0) has out = 0 and lse = -inf.
  * table : device int32 [B, pages], row pitch ld_table.  A position on a page outside

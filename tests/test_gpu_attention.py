@@ -270,3 +270,56 @@ def test_no_sequences():
     e = t.empty(0, 3, 64, device=device())
     out, lse = B.paged_attention(e, cache, t.empty(0, 4, dtype=t.int32, device=device()), t.empty(0, dtype=t.int32, device=device()), lse=True)
     assert out.shape == (0, 3, 64) and lse.shape == (0, 3)
+
+
+def _small_scale(q_exp, k_exp, scale, q_dt, codes, lens, page=16, D=64):
+    """Queries of about 2^q_exp over keys of about 2^k_exp."""
+    t = torch()
+    g = np.random.default_rng(sum(lens) + page)
+    pages = sum(-(-n // page) for n in lens) + 2
+    cache, _ = new_cache("head_major", pages, page, 2, D, codes)
+    if codes:   # codes of about 2^4, and scales to match
+        cache.k_scale.mul_(2.0 ** (k_exp - 4)), cache.v_scale.mul_(0.01)
+    else:
+        cache.k.copy_((t.randn_like(cache.k, dtype=t.float32) * 2.0 ** k_exp).bfloat16()), cache.v.normal_()
+    table = make_table(g, lens, page, pages)
+    q = t.from_numpy((2.0 ** q_exp * g.standard_normal((len(lens), 6, D))).astype(np.float32)).to(device())
+    q = q.bfloat16() if q_dt == "bf16" else q
+    banner(f"paged_attention scale {scale} of 2^{q_exp} x 2^{k_exp} {q_dt} codes={codes} lens={lens} page={page} D={D}")
+    out, lse = B.paged_attention(q, cache, t.from_numpy(table).to(device()), t.tensor(lens, dtype=t.int32, device=device()),
+                                 scale=scale, lse=True, out_dtype=t.float32)
+    _check(out, lse, q, cache, cache_values(cache), table, lens, 0, scale)
+    return out
+
+
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("lens", [[40, 300, 0, 1], [5000, 12]])
+def test_small_scales(q_dt, codes, lens):
+    """A scale far below the smallest that a model has counts as it is: logits of about one and of some tens from queries and keys
+    of 10^18 (2^60), on either side of 2^-100, where queries are taken down by 2^64, and of either sign; a scale of zero, and
+    others whose logits are zero, whatever the products, weigh all tokens alike."""
+    for q_exp, k_exp, scale in ((60, 60, 2.0 ** -123), (60, 60, -3e-37), (60, 60, 2.0 ** -119), (30, 70, 0.11 * 2.0 ** -100),
+                                (70, 33, 0.5 * 2.0 ** -103), (50, 50, 0.68 * 2.0 ** -100), (50, 50, 0.70 * 2.0 ** -100),
+                                (50, 50, 1e-31), (60, 60, 0.0), (60, 60, -0.0), (60, 60, 1e-45), (60, 60, -5e-324), (60, 60, 1e-300)):
+        _small_scale(q_exp, k_exp, scale, q_dt, codes, lens)
+
+
+@pytest.mark.parametrize("D,page", [(128, 7), (128, 16), (80, 16), (256, 32), (256, 5)])
+def test_small_scales_of_every_width(D, page):
+    for q_dt in ("bf16", "f32"):
+        for codes in (True, False):
+            for scale in (0.0, 2.0 ** -123):
+                _small_scale(60, 59, scale, q_dt, codes, [200, 33], page, D)
+
+
+def test_nan_meets_a_scale_of_zero():
+    t = torch()
+    cache, _ = new_cache("head_major", 4, 16, 1, 64, False)
+    for dt in (t.bfloat16, t.float32):
+        q = t.randn(1, 4, 64, device=device()).to(dt)
+        q[0, 2, 7] = float("nan")
+        banner(f"paged_attention NaN at scale 0 {dt}")
+        out = B.paged_attention(q, cache, t.arange(4, dtype=t.int32, device=device())[None],
+                                t.tensor([50], dtype=t.int32, device=device()), scale=0.0)
+        assert bool(out[0, 2].isnan().all()) and bool(out[0, [0, 1, 3]].isfinite().all())
