@@ -323,3 +323,41 @@ def test_nan_meets_a_scale_of_zero():
         out = B.paged_attention(q, cache, t.arange(4, dtype=t.int32, device=device())[None],
                                 t.tensor([50], dtype=t.int32, device=device()), scale=0.0)
         assert bool(out[0, 2].isnan().all()) and bool(out[0, [0, 1, 3]].isfinite().all())
+
+
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["token_major", "side_by_side", "padded"])
+@pytest.mark.parametrize("D", [64, 128, 144, 256])
+def test_layouts_of_codes(D, layout, q_dt):
+    """Pages of whole halves whose scales lie apart (token-major) or next to each other, in one scale group and in two."""
+    for page in (16, 48):
+        _run([5, 700, 1, 130, 0, 64], 8, 2, D, page, True, layout=layout, q_dt=q_dt)
+    _run([3000, 17], 8, 2, D, 16, True, layout=layout, q_dt=q_dt, window=2500)
+
+
+@pytest.mark.parametrize("n", [310, 4000])
+@pytest.mark.parametrize("codes", [True, False])
+@pytest.mark.parametrize("q_dt", ["bf16", "f32"])
+def test_a_maximum_that_rises_late(n, codes, q_dt):
+    """Logits that rise along the sequence for one head, so that every tile rescales what was before it, and fall for the other."""
+    t = torch()
+    pages = n // 16 + 1
+    cache, _ = new_cache("head_major", pages, 16, 1, 64, codes)
+    cache.k.zero_()
+    ramp = t.arange(pages * 16, device=device(), dtype=t.float32).view(pages, 16, 1)
+    if codes:
+        cache.v_scale.mul_(0.01)
+        cache.k[..., 0] = 0x38                            # the code of 1
+        cache.k_scale.copy_(ramp[..., None])
+    else:
+        cache.k[..., 0] = ramp.bfloat16()
+    q = t.zeros(1, 2, 64, device=device())
+    q[0, 0, 0], q[0, 1, 0] = 1.0, -1.0
+    q = q.bfloat16() if q_dt == "bf16" else q
+    table = np.random.default_rng(n).permutation(pages).astype(np.int32)[None]
+    if n > 1000:   # along the sequence, not along the pages
+        table = np.arange(pages, dtype=np.int32)[None]
+    banner(f"paged_attention ramp n={n} codes={codes} {q_dt}")
+    out, lse = B.paged_attention(q, cache, t.from_numpy(table).to(device()), t.tensor([n], dtype=t.int32, device=device()), scale=0.5,
+                                 lse=True)
+    _check(out, lse, q, cache, cache_values(cache), table, [n], 0, 0.5)
