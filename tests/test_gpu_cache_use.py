@@ -354,3 +354,61 @@ def test_refusals_of_the_binding():
                  lambda: B.rope(x, t.stack([pos, pos]), inv, axes=bytes([0] * 63 + [2]))):
         with pytest.raises(B.BSF8Error, match="INVALID_ARG"):
             call()
+
+
+@pytest.mark.parametrize("D", [64, 128, 144, 256])
+@pytest.mark.parametrize("codes", [True, False])
+def test_the_workspace_holds_every_type_of_query(D, codes):
+    """The bytes that are asked for without the query's type are enough for each: calls that join write nothing behind them."""
+    t = torch()
+    joined = 0
+    for lens, heads, kv in (([3000], 4, 1), ([9000, 5, 700], 8, 2), ([600] * 40, 4, 4), ([1500, 2000] * 12, 20, 1)):
+        q, cache, table, ln = _attention_case(D, lens, codes, D, heads, kv)
+        need = B.attention_workspace_size(cache, len(lens), heads, table.shape[1])
+        joined += need > 0
+        guard = t.full((need + 512 + (1 << 20),), 0x5A, dtype=t.uint8, device=device())
+        ws = guard[256:256 + need]
+        for dt in (t.bfloat16, t.float32):
+            for out_dt in (t.bfloat16, t.float32):
+                banner(f"workspace of {need} bytes D={D} codes={codes} {lens[:3]} x {len(lens)} {dt} -> {out_dt}")
+                want = B.paged_attention(q.to(dt), cache, table, ln, out_dtype=out_dt)
+                got = B.paged_attention(q.to(dt), cache, table, ln, out_dtype=out_dt, workspace=(ws if need else None, need))
+                assert t.equal(got, want)
+                assert bool((guard[:256] == 0x5A).all()) and bool((guard[256 + need:] == 0x5A).all())
+    assert joined >= 2
+
+
+def test_types_that_are_no_cache():
+    """Caches of other types are refused, with scales and without."""
+    t = torch()
+    sc = [t.ones(3, 16, 2, 1, device=device()) for _ in "kv"]
+    for dt in (t.float32, t.float16, t.int8, t.float8_e5m2):
+        kv = [t.zeros(3, 16, 2, 64, device=device()).to(dt) for _ in "kv"]
+        for scales in ([], sc, sc[:1]):
+            with pytest.raises((ValueError, B.BSF8Error)):
+                B.PagedKVCache(*kv, *scales)
+    bf = [t.zeros(3, 16, 2, 64, device=device(), dtype=t.bfloat16) for _ in "kv"]
+    u8 = [t.zeros(3, 16, 2, 64, device=device(), dtype=t.uint8) for _ in "kv"]
+    for args in (bf + sc, bf + sc[:1], u8, u8 + sc[:1], [bf[0], u8[0]], [u8[0], bf[0]] + sc, u8 + [sc[0], sc[1].double()],
+                 u8 + [sc[0], sc[1][:2]]):
+        with pytest.raises((ValueError, B.BSF8Error)):
+            B.PagedKVCache(*args)
+    B.PagedKVCache(*bf), B.PagedKVCache(*u8, *sc)
+
+
+def test_no_tokens_with_head_norms():
+    """A step without tokens of a model with head norms does nothing."""
+    t = torch()
+    cache, held = new_cache("head_major", 2, 4, 2, 64, True)
+    before = [h.clone() for h in held]
+    x = t.randn(3, 8, 64, device=device()).bfloat16()
+    w, inv = t.ones(64, device=device()), t.ones(32, device=device())
+    pos, q, k, v = t.arange(3, device=device())[:0], x[:0, :4], x[:0, 4:6], x[:0, 6:]
+    y, yk = B.rope(q, pos, inv, k=k, q_weight=w, k_weight=w)
+    assert y.shape == (0, 4, 64) and yk.shape == (0, 2, 64)
+    assert B.rope(q, pos, inv, q_weight=w)[0].shape == (0, 4, 64)
+    y = B.cache_write(cache, k, v, pos, positions=pos, inv_freq=inv, q=q, q_weight=w, k_weight=w)
+    assert y.shape == (0, 4, 64) and y.dtype == t.bfloat16
+    t.cuda.synchronize()
+    for a, b in zip(before, held):
+        assert t.equal(a.view(t.uint8), b.view(t.uint8))
