@@ -5,7 +5,10 @@
 // bytes bound it: with G query heads per key head there are 4 G operations per element read,
 // and up to 16 query heads share one read of the keys and values.
 //
-// A wave takes 32 tokens at a time, for 16 query heads, and keeps everything in registers:
+// A wave takes 32 tokens at a time, for 16 query heads, and keeps them in registers (what does not
+// fit goes to scratch: with BF16 queries 37 registers of the instances of 256 BF16 channels and, where
+// pages are no multiple of 16 rows, 71 to 82, 25 to 27 of those of 128 BF16 channels and 10 to 23 of
+// 256 codes; 3 to 9 in heads of 129 to 255 codes; one with F32 queries of 256 codes; no others):
 //  * logits, transposed: S^T[token, head] = K[token, ch] Q^T[ch, head] by
 //    v_mfma_f32_16x16x32_bf16, keys as they lie in memory as the A operand (a lane holds 8
 //    channels of one token), queries as B.  A lane then holds one head's logits of 8 tokens:
@@ -211,10 +214,12 @@ __device__ __forceinline__ void split(const float (&x)[8], v8bf (&t)[N]) {
 // that offsets are constants and rows are whole cache lines, which are read non-temporally: each
 // once (64 sequences to 8192 of 128 BF16 channels 147 -> 134 us, of E4M3 91 -> 84; rows that
 // share lines lose by it, 80 channels 185 -> 218.  Keys left to the cache, the values alone
-// non-temporal: one sequence of 131072 33 -> 31 us, the batch 84 -> 88).
+// non-temporal, both sides three times in turn, each within 1 %: one sequence of 131072 33.0 -> 31.4
+// us, of 32768 34.2 -> 30.0, but the batch 85.3 -> 88.3, of BF16 132.6 -> 136.1, 32 of 256 BF16 channels
+// 90.5 -> 99.3).
 // QT: BF16 terms of a query (1: BF16 queries, 3: F32).  PT: of a softmax weight.  A weight in one
-// term would be off by 2^-9 of itself, as much as the rounding of a BF16 output; two leave 2^-17,
-// three 2^-25.
+// term would be off by up to 2^-8 of itself, as much as the rounding of a BF16 output; two leave 2^-17,
+// three nothing of its 24 bits.
 // PAGES: kAny, each lane looks up a token's page; kHalves, pages are a multiple of 16 rows, so
 // that each half of a wave's 32 tokens is on one page, whose rows all exist: addresses are
 // scalar, and rows past the length are read and left out; kHalvesWide, also four scales are
@@ -228,8 +233,9 @@ struct Config {
   static constexpr int NG = DIM > 128 ? 2 : 1;         // 128-channel groups
   // HP 2: a row of the keys' operand is half a line of a token, 64 bytes, so that one load of the
   // wave covers eight tokens' whole lines where it would touch half of sixteen and every line be
-  // asked for twice; the matrix instructions double.  (64 sequences to 8192 of 128 E4M3 channels
-  // 86.3 -> 84.3 us, 32 of 256 BF16 ones 96 -> 92, one of 32768 36 -> 34.5.  Not where rows are
+  // asked for twice; the matrix instructions double.  (Both sides three times in turn, each within 1 %:
+  // 256 sequences to 1000 of 80 BF16 channels 148 -> 124 us, 64 to 8192 of 128 E4M3 ones 86.7 -> 85.3,
+  // 32 of 256 BF16 ones, which spill, 93.9 -> 90.5, one of 32768 36.6 -> 34.2.  Not where rows are
   // 64 bytes, nor where the instructions tell: 256 E4M3 channels 53 -> 57, F32 queries 62 -> 65.)
   static constexpr int HP = QT > 1 || (E4M3 && DIM != 128) ? 1 : 2;
   static constexpr int LN = DIM * (E4M3 ? 1 : 2) / (64 * HP);   // 16-byte loads per lane and row of the operand
@@ -831,7 +837,10 @@ Plan plan_of(const CacheDev& c, int64_t B, int32_t q_heads, int64_t bound, bool 
   // A block per item where the longest is short (one sequence of 200 tokens 13.4 -> 10.0 us, with
   // eight waves) or where so many items follow each other on a compute unit that they even out (8
   // key heads: 256 sequences to 1000 88 -> 77 us, to 2000 149 -> 146, but to 4000 260 -> 282; 64 to
-  // 1000 29.0 -> 29.7, to 2000 44 -> 54; 24 key heads, 256 to 1000 174 -> 127).
+  // 1000 29.0 -> 29.7, to 2000 44 -> 54; 24 key heads of 80, 256 to 1000 165 -> 124).  These lengths grow
+  // as a square; the host knows the table's width alone, so other batches pay for it where one block's item
+  // is far longer than the rest: 256 sequences of 24 key heads under a table of 8000, one of them of 7999 and the
+  // others of 200, 103.5 -> 110, eight of 7999 187 -> 209, all of 700 244 -> 233.
   p.whole = bound <= kWholeTokens || tiles * held <= 8 * p.items ? 1 : 0;
   if (p.whole) {
     p.blocks = p.items;

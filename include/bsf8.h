@@ -669,7 +669,8 @@ bsf8_status bsf8_cache_read(const bsf8_cache* cache, int64_t B, const int32_t* t
  *   s_t = scale * sum_d q[b, h, d] * k_t[d],   t in [max(0, n - window), n)  (window 0: all)
  *   out[b, h] = sum_t exp(s_t) v_t / sum_t exp(s_t),    lse[b, h] = log(sum_t exp(s_t))
  * in F32 with a running maximum; BF16 and E4M3 values enter the products exactly, an
- * F32 query as three BF16 terms that hold all of its bits.  The softmax weights enter
+ * F32 query as three BF16 terms that hold all of its bits (up to 3.38e38, BF16's
+ * largest; a larger one counts as infinite).  The softmax weights enter
  * their product with the values as two BF16 terms (17 bits or more; three, 24 bits,
  * where q or out is F32).  The sums' order depends on the batch and on the device's
  * compute units, never on timing.
